@@ -53,6 +53,9 @@ struct LogprobsArgs {
     int32_t *top_idx;
     float *top_logprob;
 };
-hipError_t launch_logprobs(const LogprobsArgs &a, hipStream_t s);
+// Segments of a row; rows of more than one need ws: T * segments parts.
+int logprobs_segments(int64_t V);
+size_t logprobs_part_bytes(int n_top);
+hipError_t launch_logprobs(const LogprobsArgs &a, void *ws, hipStream_t s);
 
 }  // namespace moeq4

@@ -113,8 +113,11 @@ int moe_q4_delta_prefill(const void *q, int64_t ldq, const void *k, int64_t ldk,
 }
 
 size_t moe_q4_logprobs_workspace_size(int64_t T, int64_t V, int32_t n_top) {
-    (void)T, (void)V, (void)n_top;
-    return 0;
+    if (T <= 0 || V < 1 || n_top < 0 || n_top > MOE_Q4_MAX_TOP || T >= (int64_t)1 << 31 ||
+        V >= ((int64_t)1 << 31) - (1 << 16))
+        return 0;
+    const int segs = logprobs_segments(V);
+    return segs == 1 ? 0 : (size_t)T * segs * logprobs_part_bytes(n_top);
 }
 
 int moe_q4_logprobs(const void *logits, int32_t dtype, int64_t T, int64_t V, int64_t ld, const int32_t *tokens,
@@ -126,6 +129,7 @@ int moe_q4_logprobs(const void *logits, int32_t dtype, int64_t T, int64_t V, int
         return MOE_Q4_ERR_UNSUPPORTED;
     if (dtype != MOE_Q4_BF16 && dtype != MOE_Q4_F32) return MOE_Q4_ERR_UNSUPPORTED;
     if (T == 0) return MOE_Q4_OK;
+    if (T * logprobs_segments(V) >= (int64_t)1 << 31) return MOE_Q4_ERR_UNSUPPORTED;  // workgroups
     if (!logits || !aligned(logits, dtype == MOE_Q4_F32 ? 4 : 2) || ld < V) return MOE_Q4_ERR_INVALID_ARG;
     if ((tokens && !logprob) || (n_top > 0 && (!top_idx || !top_logprob))) return MOE_Q4_ERR_INVALID_ARG;
     if (!aligned(tokens, 4) || !aligned(logprob, 4) || !aligned(entropy, 4) || !aligned(top_idx, 4) ||
@@ -136,7 +140,7 @@ int moe_q4_logprobs(const void *logits, int32_t dtype, int64_t T, int64_t V, int
     if (need && !aligned(ws, 16)) return MOE_Q4_ERR_INVALID_ARG;
     if (!tokens && !entropy && n_top == 0) return MOE_Q4_OK;
     const LogprobsArgs a{logits, dtype == MOE_Q4_F32, T, V, ld, tokens, logprob, entropy, n_top, top_idx, top_logprob};
-    return hip_status(launch_logprobs(a, reinterpret_cast<hipStream_t>(stream)));
+    return hip_status(launch_logprobs(a, ws, reinterpret_cast<hipStream_t>(stream)));
 }
 
 }  // extern "C"
