@@ -76,7 +76,7 @@ typedef struct moe_q4_linear_weights {
  *   residual  bf16 [T] rows of N at distance ldr, or NULL; may be y itself
  *             (same pointer and distance, y_dtype MOE_Q4_BF16)
  *   y         bf16 or float (y_dtype) [T] rows of N at distance ldy
- * T < 2^31.
+ * T < 2^31, T * N < 2^40.
  */
 MOE_Q4_API int moe_q4_linear(const void *x, int64_t ldx, int64_t T, const moe_q4_linear_weights *w, int32_t act,
                              const void *residual, int64_t ldr, void *y, int64_t ldy, int32_t y_dtype,
@@ -123,7 +123,7 @@ typedef struct moe_q4_delta_shape {
  *   o          bf16 [T] rows of [v_heads][v_dim] at distance ldo, 16-byte
  *              aligned, ldo % 8 == 0; must not overlap the inputs
  * n_seq = 0 returns MOE_Q4_OK without launching anything.  With T = 0 the row
- * pointers may be NULL.  T < 2^31, n_seq < 2^20.
+ * pointers may be NULL.  T < 2^31, n_seq < 2^20, n_seq * v_heads < 2^28.
  *
  * moe_q4_delta_decode takes the tokens of a sequence one after another (tuned
  * for a few tokens per sequence); moe_q4_delta_prefill takes them in chunks of

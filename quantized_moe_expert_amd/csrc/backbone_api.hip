@@ -35,7 +35,8 @@ int delta_args(const void *q, int64_t ldq, const void *k, int64_t ldk, const voi
     int st = check_delta_shape(sh);
     if (st) return st;
     if (T < 0 || n_seq < 0 || n_states < 0) return MOE_Q4_ERR_INVALID_ARG;
-    if (T >= (int64_t)1 << 31 || n_seq >= 1 << 20) return MOE_Q4_ERR_UNSUPPORTED;
+    if (T >= (int64_t)1 << 31 || n_seq >= 1 << 20 || (int64_t)n_seq * sh->v_heads >= 1 << 28)
+        return MOE_Q4_ERR_UNSUPPORTED;
     if (n_seq == 0) return MOE_Q4_OK;
     if (!seq_start || !aligned(seq_start, 4) || !aligned(state_idx, 4) || !aligned(state_in, 16) ||
         !aligned(state_out, 16))
@@ -66,7 +67,8 @@ int moe_q4_linear(const void *x, int64_t ldx, int64_t T, const moe_q4_linear_wei
     if (w->format != MOE_Q4_LINEAR_INT8 && w->format != MOE_Q4_LINEAR_BF16) return MOE_Q4_ERR_UNSUPPORTED;
     const bool int8 = w->format == MOE_Q4_LINEAR_INT8;
     if (int8 && (!w->scale || !aligned(w->scale, 2))) return MOE_Q4_ERR_INVALID_ARG;
-    if (K % (int8 ? 128 : 8) || K > 65536 || N >= 1 << 24 || T >= (int64_t)1 << 31) return MOE_Q4_ERR_UNSUPPORTED;
+    if (K % (int8 ? 128 : 8) || K > 65536 || N >= 1 << 24 || T >= (int64_t)1 << 31 || T * N >= (int64_t)1 << 40)
+        return MOE_Q4_ERR_UNSUPPORTED;
     if (act < MOE_Q4_ACT_NONE || act > MOE_Q4_ACT_GELU) return MOE_Q4_ERR_UNSUPPORTED;
     if (y_dtype != MOE_Q4_BF16 && y_dtype != MOE_Q4_F32) return MOE_Q4_ERR_UNSUPPORTED;
     if (T == 0) return MOE_Q4_OK;

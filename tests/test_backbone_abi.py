@@ -53,7 +53,7 @@ def _linear(K=256, N=100, fmt=m.LINEAR_INT8, q=FAKE, scale=FAKE, bias=None, x=FA
     (UNSUPPORTED, dict(fmt=2)), (UNSUPPORTED, dict(fmt=-1)), (UNSUPPORTED, dict(act=3)), (UNSUPPORTED, dict(act=-1)),
     (UNSUPPORTED, dict(ydt=2)),
     (UNSUPPORTED, dict(K=192)), (UNSUPPORTED, dict(K=65664)), (UNSUPPORTED, dict(fmt=1, K=100)),
-    (UNSUPPORTED, dict(N=1 << 24)), (UNSUPPORTED, dict(T=1 << 31)),
+    (UNSUPPORTED, dict(N=1 << 24)), (UNSUPPORTED, dict(T=1 << 31)), (UNSUPPORTED, dict(T=1 << 20, N=1 << 20)),
     (INVALID, dict(ldx=248)), (INVALID, dict(ldx=260)), (UNSUPPORTED, dict(ldx=(1 << 22) + 8)),
     (INVALID, dict(ldy=99)), (UNSUPPORTED, dict(ldy=(1 << 22) + 1)),
     (INVALID, dict(res=FAKE + 64, ldr=99)), (UNSUPPORTED, dict(res=FAKE + 64, ldr=(1 << 22) + 1)),
@@ -89,6 +89,7 @@ def _delta(prefill, hk=2, hv=4, dk=128, dv=128, T=10, n_seq=2, n_states=2, q=FAK
     (UNSUPPORTED, dict(dk=96)), (UNSUPPORTED, dict(dv=256)), (UNSUPPORTED, dict(hk=1, hv=1025)),
     (INVALID, dict(T=-1)), (INVALID, dict(n_seq=-1)), (INVALID, dict(n_states=-1)),
     (UNSUPPORTED, dict(T=1 << 31)), (UNSUPPORTED, dict(n_seq=1 << 20)),
+    (UNSUPPORTED, dict(n_seq=1 << 19, hk=1, hv=512)),
     (INVALID, dict(q=None)), (INVALID, dict(k=None)), (INVALID, dict(v=None)), (INVALID, dict(o=None)),
     (INVALID, dict(g=None)), (INVALID, dict(beta=None)), (INVALID, dict(start=None)),
     (INVALID, dict(q=FAKE + 8)), (INVALID, dict(o=FAKE + 8)), (INVALID, dict(g=FAKE + 2)),
