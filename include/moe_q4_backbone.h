@@ -123,12 +123,15 @@ typedef struct moe_q4_delta_shape {
  *   o          bf16 [T] rows of [v_heads][v_dim] at distance ldo, 16-byte
  *              aligned, ldo % 8 == 0; must not overlap the inputs
  * n_seq = 0 returns MOE_Q4_OK without launching anything.  With T = 0 the row
- * pointers may be NULL.  T < 2^31, n_seq < 2^20, n_seq * v_heads < 2^28.
+ * pointers may be NULL.  T < 2^31, n_seq < 2^20, n_seq * v_heads < 2^28,
+ * (T / 64 + n_seq) * v_heads < 2^31.
  *
  * moe_q4_delta_decode takes the tokens of a sequence one after another (tuned
  * for a few tokens per sequence); moe_q4_delta_prefill takes them in chunks of
  * 64 on the matrix cores (tuned for prompts) and needs
  *   ws  >= moe_q4_delta_workspace_size(T, n_seq, shape) bytes, 256-byte aligned.
+ * A NaN or an infinity in a token's inputs makes the outputs of its sequence
+ * from that token on (prefill: from its chunk on) undefined numbers.
  */
 MOE_Q4_API size_t moe_q4_delta_workspace_size(int64_t T, int32_t n_seq, const moe_q4_delta_shape *shape);
 MOE_Q4_API int moe_q4_delta_decode(const void *q, int64_t ldq, const void *k, int64_t ldk, const void *v,

@@ -42,6 +42,8 @@ struct DeltaArgs {
     int64_t ldo;
 };
 hipError_t launch_delta_decode(const DeltaArgs &a, hipStream_t s);
+size_t delta_workspace_bytes(int64_t T, int n_seq, int hv);
+hipError_t launch_delta_prefill(const DeltaArgs &a, void *ws, hipStream_t s);
 
 struct LogprobsArgs {
     const void *logits;

@@ -35,7 +35,8 @@ int delta_args(const void *q, int64_t ldq, const void *k, int64_t ldk, const voi
     int st = check_delta_shape(sh);
     if (st) return st;
     if (T < 0 || n_seq < 0 || n_states < 0) return MOE_Q4_ERR_INVALID_ARG;
-    if (T >= (int64_t)1 << 31 || n_seq >= 1 << 20 || (int64_t)n_seq * sh->v_heads >= 1 << 28)
+    if (T >= (int64_t)1 << 31 || n_seq >= 1 << 20 || (int64_t)n_seq * sh->v_heads >= 1 << 28 ||
+        (T / 64 + n_seq) * sh->v_heads >= (int64_t)1 << 31)
         return MOE_Q4_ERR_UNSUPPORTED;
     if (n_seq == 0) return MOE_Q4_OK;
     if (!seq_start || !aligned(seq_start, 4) || !aligned(state_idx, 4) || !aligned(state_in, 16) ||
@@ -84,7 +85,7 @@ int moe_q4_linear(const void *x, int64_t ldx, int64_t T, const moe_q4_linear_wei
 
 size_t moe_q4_delta_workspace_size(int64_t T, int32_t n_seq, const moe_q4_delta_shape *shape) {
     if (T <= 0 || n_seq < 1 || check_delta_shape(shape)) return 0;
-    return 0;
+    return delta_workspace_bytes(T, n_seq, shape->v_heads);
 }
 
 int moe_q4_delta_decode(const void *q, int64_t ldq, const void *k, int64_t ldk, const void *v, int64_t ldv,
@@ -111,7 +112,7 @@ int moe_q4_delta_prefill(const void *q, int64_t ldq, const void *k, int64_t ldk,
     const size_t need = moe_q4_delta_workspace_size(T, n_seq, shape);
     if (need && (!ws || ws_bytes < need)) return MOE_Q4_ERR_WORKSPACE;
     if (need && !aligned(ws, 256)) return MOE_Q4_ERR_INVALID_ARG;
-    return hip_status(launch_delta_decode(a, reinterpret_cast<hipStream_t>(stream)));
+    return hip_status(launch_delta_prefill(a, ws, reinterpret_cast<hipStream_t>(stream)));
 }
 
 size_t moe_q4_logprobs_workspace_size(int64_t T, int64_t V, int32_t n_top) {

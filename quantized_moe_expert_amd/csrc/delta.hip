@@ -1,4 +1,4 @@
-// Gated delta rule, token by token.
+// Gated delta rule: token by token, and in chunks of 64 tokens (below).
 //
 // With a = exp(g), per value head:  S' = a S,  u = beta (v - S'^T k),
 // S = S' + k u^T,  o = scale S^T q.  Since S^T q = a S_old^T q + (k.q) u, the
@@ -128,7 +128,644 @@ hipError_t launch_decode(const DeltaArgs &a, hipStream_t s) {
     return hipGetLastError();
 }
 
+// ------------------------------------------------------- chunks of 64 tokens
+//
+// Within a chunk, with G the running sum of g, the updates u_i solve
+//   u_i + sum_{j<i} A_ij u_j = beta_i (v_i - e^{G_i} S0^T k_i),
+//   A_ij = beta_i e^{G_i - G_j} k_i.k_j,
+// so U = T' (V - diag(e^G) K S0) with T' = (I + A)^-1 diag(beta), and
+//   O  = scale (diag(e^G) Q S0 + P U),  P_ij = e^{G_i - G_j} q_i.k_j (j <= i),
+//   S1 = e^{G_63} S0 + sum_j e^{G_63 - G_j} k_j u_j^T.
+// T' and P do not depend on the state: delta_prep_kernel computes them for
+// every chunk and head at once; delta_scan_kernel walks the chunks of a
+// sequence with what is left, products of the matrix cores.
+//
+// Operands are f16: k, q rows, T', P rows and the columns of S, X, U are
+// scaled by a power of two each, taken off again in fp32 (so f16's range
+// limits none of them).  Products that reach the state take a second f16 with
+// the remainder of each operand (22 bits; k needs none, its 8 bits fit), those
+// that reach only o take one (12 bits against o's 8).  Sums are fp32.  G is
+// summed in double: e^{G_i - G_j} of neighbours is then right behind a strong
+// decay.
+//
+// The 16x16x32 product reads its right operand 8 rows per lane and leaves its
+// result 4 rows per lane (row 4 g + e, column lane % 16, g = lane / 16).  The
+// order of the inner index is free, so everything that meets such a result is
+// stored in the order "4 g + e of one tile, then of the next": a result goes
+// into the next product straight from its registers.
+typedef __attribute__((__vector_size__(4 * sizeof(float)))) float f32x4_t;
+typedef _Float16 f16x2_t __attribute__((ext_vector_type(2)));
+
+constexpr int CH = 64;
+// Per (chunk, head): 18 operands of 1 KB (T' first f16: 6, remainder: 6, P: 6;
+// row tile 0: inner tiles 0-1; 1: 0-1; 2: 0-1, 2-3; 3: 0-1, 2-3), then vectors
+// of 64 floats, then e^{G_63}.
+constexpr int UNIT = 20480, UNIT_VEC = 18432;
+enum { V_A, V_B, V_C, V_T, V_P, V_SK, V_SQ, V_COUNT };
+constexpr int UNIT_GAMMA = UNIT_VEC + V_COUNT * CH * 4;
+__device__ __forceinline__ constexpr int frag_index(int it, int ks) { return it < 2 ? it : 2 * it - 2 + ks; }
+
+__device__ __forceinline__ f32x4_t mfma_f16(u32x4_t a, u32x4_t b, f32x4_t c) {
+    return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8_t, a), __builtin_bit_cast(f16x8_t, b), c, 0,
+                                                  0, 0);
+}
+__device__ __forceinline__ uint32_t f16_pair(float a, float b) {
+    return __builtin_bit_cast(uint32_t, f16x2_t{(_Float16)a, (_Float16)b});
+}
+// a pair's remainders after rounding to f16, as f16
+__device__ __forceinline__ uint32_t f16_rest(float a, float b, uint32_t first) {
+    const f16x2_t h = __builtin_bit_cast(f16x2_t, first);
+    return f16_pair(a - (float)h[0], b - (float)h[1]);
+}
+// The power of two 2^s that puts values whose largest magnitude is m in
+// [2^14, 2^15) (as row_scale, over almost all of fp32's range: m from 2^-112).
+__device__ __forceinline__ RowScale unit_scale(float m) {
+    int be = (int)((__float_as_uint(m) >> 23) & 0xffu);
+    be = be < 15 ? 15 : (be > 254 ? 254 : be);
+    return RowScale{__uint_as_float((uint32_t)(268 - be) << 23), 141 - be};
+}
+// Largest over the four lane groups (lanes l, l ^ 16, l ^ 32, l ^ 48).
+__device__ __forceinline__ float groups_max(float v) {
+    typedef unsigned int u32x2_t __attribute__((ext_vector_type(2)));
+    const uint32_t a = __float_as_uint(v);
+    const u32x2_t p = __builtin_bit_cast(u32x2_t, __builtin_amdgcn_permlane16_swap(a, a, false, false));
+    const uint32_t b = __float_as_uint(fmaxf(__uint_as_float(p.x), __uint_as_float(p.y)));
+    const u32x2_t q = __builtin_bit_cast(u32x2_t, __builtin_amdgcn_permlane32_swap(b, b, false, false));
+    return fmaxf(__uint_as_float(q.x), __uint_as_float(q.y));
+}
+__device__ __forceinline__ float max_abs(f32x4_t v, float m) {
+    return fmaxf(fmaxf(fmaxf(fabsf(v[0]), fabsf(v[1])), fmaxf(fabsf(v[2]), fabsf(v[3]))), m);
+}
+
+// Rows [t0, t1) of sequence b, inside [0, T].
+__device__ __forceinline__ void seq_rows(const DeltaArgs &a, int b, int &t0, int &t1) {
+    t0 = a.seq_start[b];
+    t1 = a.seq_start[b + 1];
+    t0 = t0 < 0 ? 0 : (t0 > a.T ? (int)a.T : t0);
+    t1 = t1 < t0 ? t0 : (t1 > a.T ? (int)a.T : t1);
+}
+// First chunk number of a sequence: t0 / 64 + b leaves every sequence the
+// numbers it needs (the next one's start is at least t1 / 64 + b + 1) without
+// a prefix sum, and stays below T / 64 + n_seq.
+__device__ __forceinline__ int first_chunk(int t0, int b) { return t0 / CH + b; }
+
+// T', P and the row factors of one chunk and head.  Wave w owns row tile w.
+// Bound by latency chains (the 16 x 16 inversions) and the 20 KB it writes.
+template <int DK>
+__global__ __launch_bounds__(256) void delta_prep_kernel(DeltaArgs a, uint8_t *__restrict__ ws) {
+    constexpr int LDA = 68, PL = DK / 16;  // elements per lane of a row's 16 lanes
+    constexpr int KQ = 2 * CH * DK * 2, TB = CH * LDA * 4;
+    __shared__ __align__(16) uint8_t s_kq[KQ > TB ? KQ : TB];  // k, q as f16; then T
+    __shared__ __align__(16) float s_A[CH * LDA];
+    __shared__ float s_f[2][CH];   // k and q: what takes a row's scale off and normalises it
+    __shared__ float s_sc[2][CH];  // and the scale
+    __shared__ __align__(16) float s_beta[CH];
+    __shared__ double s_G[CH];
+    const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6, m = lane & 15, g4 = lane >> 4;
+    const int h = blockIdx.x % a.hv, id = blockIdx.x / a.hv;
+    // the sequence: the last whose first chunk is at most id
+    int lo = 0, hi = a.n_seq - 1;
+    while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        int t0, t1;
+        seq_rows(a, mid, t0, t1);
+        if (first_chunk(t0, mid) <= id) lo = mid;
+        else hi = mid - 1;
+    }
+    int t0, t1;
+    seq_rows(a, lo, t0, t1);
+    const int c = id - first_chunk(t0, lo);
+    if (c < 0 || t0 + (int64_t)c * CH >= t1) return;
+    t0 += c * CH;
+    const int len = t1 - t0 < CH ? t1 - t0 : CH;
+    const int hk = h / (a.hv / a.hk);
+
+    // rows of k and q to f16
+    constexpr int MASK = DK / 8 - 1;
+    auto place = [](int which, int row, int chunk) { return ((which * CH + row) * (DK / 8) + (chunk ^ (row & MASK))) * 16; };
+#pragma unroll
+    for (int which = 0; which < 2; ++which) {
+        const uint16_t *src = which ? a.q : a.k;
+        const int64_t ld = which ? a.ldq : a.ldk;
+#pragma unroll
+        for (int r4 = 0; r4 < 4; ++r4) {
+            const int row = 16 * w + 4 * r4 + g4;
+            float x[PL];
+#pragma unroll
+            for (int e = 0; e < PL; ++e) x[e] = 0.f;
+            if (row < len) {
+                const uint16_t *p = src + (int64_t)(t0 + row) * ld + hk * DK + m * PL;
+#pragma unroll
+                for (int e = 0; e < PL; e += 4) {
+                    const uint2 d = *reinterpret_cast<const uint2 *>(p + e);
+                    x[e] = __uint_as_float(d.x << 16);
+                    x[e + 1] = __uint_as_float(d.x & 0xffff0000u);
+                    x[e + 2] = __uint_as_float(d.y << 16);
+                    x[e + 3] = __uint_as_float(d.y & 0xffff0000u);
+                }
+            }
+            float mx = 0.f, ss = 0.f;
+#pragma unroll
+            for (int e = 0; e < PL; ++e) {
+                mx = fmaxf(mx, fabsf(x[e]));
+                ss += x[e] * x[e];
+            }
+            mx = row16_max(mx);
+            ss = seg_sum_dpp<16>(ss);
+            const RowScale sc = unit_scale(mx);
+#pragma unroll
+            for (int e = 0; e < PL; e += 4) {
+                uint2 d;
+                d.x = f16_pair(x[e] * sc.sc, x[e + 1] * sc.sc);
+                d.y = f16_pair(x[e + 2] * sc.sc, x[e + 3] * sc.sc);
+                const int at = m * PL + e;
+                *reinterpret_cast<uint2 *>(s_kq + place(which, row, at / 8) + at % 8 * 2) = d;
+            }
+            if (m == 0) {
+                s_f[which][row] = (a.norm ? 1.0f / sqrtf(ss + 1e-6f) : 1.0f) * exp2i(-sc.s) * (which ? a.scale : 1.0f);
+                s_sc[which][row] = sc.sc;
+            }
+        }
+    }
+    if (w == 0) {
+        const int64_t at = (int64_t)(t0 + lane) * a.hv + h;
+        const float gl = lane < len ? a.g[at] : 0.f;
+        double G = gl < -1000.f ? -1000.0 : (double)gl;  // e^-1000 is 0 too, and -inf - -inf is not
+#pragma unroll
+        for (int o = 1; o < 64; o <<= 1) {
+            const double up = __shfl_up(G, o);
+            if (lane >= o) G += up;
+        }
+        s_G[lane] = G;
+        s_beta[lane] = lane < len ? a.beta[at] : 0.f;
+    }
+    __syncthreads();
+
+    // k_j.k_i and k_j.q_i, row j = 16 jt + 4 g4 + e, column i = 16 w + m
+    uint8_t *unit = ws + ((int64_t)id * a.hv + h) * UNIT;
+    float *vec = reinterpret_cast<float *>(unit + UNIT_VEC);
+    const int i = 16 * w + m;
+    f32x4_t P[4];
+    {
+        u32x4_t bk[DK / 32], bq[DK / 32];
+#pragma unroll
+        for (int ks = 0; ks < DK / 32; ++ks) {
+            bk[ks] = *reinterpret_cast<const u32x4_t *>(s_kq + place(0, i, 4 * ks + g4));
+            bq[ks] = *reinterpret_cast<const u32x4_t *>(s_kq + place(1, i, 4 * ks + g4));
+        }
+        const double Gi = s_G[i];
+        const float fi = s_f[0][i], fqi = s_f[1][i], bi = s_beta[i];
+#pragma unroll
+        for (int jt = 0; jt < 4; ++jt) {
+            P[jt] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+            if (jt <= w) {
+                f32x4_t kk = {0.f, 0.f, 0.f, 0.f}, kq = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                for (int ks = 0; ks < DK / 32; ++ks) {
+                    const u32x4_t ak = *reinterpret_cast<const u32x4_t *>(s_kq + place(0, 16 * jt + m, 4 * ks + g4));
+                    kk = mfma_f16(ak, bk[ks], kk);
+                    kq = mfma_f16(ak, bq[ks], kq);
+                }
+                f32x4_t A;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const int j = 16 * jt + 4 * g4 + e;
+                    const float d = j <= i ? expf((float)(Gi - s_G[j])) * s_f[0][j] : 0.f;
+                    A[e] = j < i ? kk[e] * fi * d * bi : 0.f;
+                    P[jt][e] = j <= i ? kq[e] * fqi * d : 0.f;
+                }
+                *reinterpret_cast<f32x4_t *>(&s_A[i * LDA + 16 * jt + 4 * g4]) = A;
+            }
+        }
+    }
+    {
+        float mx = 0.f;
+#pragma unroll
+        for (int jt = 0; jt < 4; ++jt) mx = max_abs(P[jt], mx);
+        const RowScale sc = unit_scale(groups_max(mx));
+        if (g4 == 0) vec[V_P * CH + i] = exp2i(-sc.s);
+#pragma unroll
+        for (int ks = 0; ks < 2; ++ks)
+            if (ks <= w / 2) {
+                u32x4_t f;
+#pragma unroll
+                for (int t = 0; t < 2; ++t) {
+                    const f32x4_t p = P[2 * ks + t];
+                    f[2 * t] = f16_pair(p[0] * sc.sc, p[1] * sc.sc);
+                    f[2 * t + 1] = f16_pair(p[2] * sc.sc, p[3] * sc.sc);
+                }
+                *reinterpret_cast<u32x4_t *>(unit + (12 + (w < 2 ? w : 2 * w - 2 + ks)) * 1024 + lane * 16) = f;
+            }
+    }
+    __syncthreads();  // s_A is whole, k and q are used
+
+    // T = (I + A)^-1 by 16 x 16 tiles: the diagonal ones by substitution (a
+    // lane a column), then T_ij = -T_ii sum_k A_ik T_kj, one distance from the
+    // diagonal after another
+    float *T = reinterpret_cast<float *>(s_kq);
+    {
+        float col[16];
+#pragma unroll
+        for (int r = 0; r < 16; ++r) {
+            float t = r == m ? 1.f : 0.f;
+#pragma unroll
+            for (int q = 0; q < (r + 3) / 4; ++q) {
+                const f32x4_t A = *reinterpret_cast<const f32x4_t *>(&s_A[(16 * w + r) * LDA + 16 * w + 4 * q]);
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    if (4 * q + e < r) t = fmaf(-A[e], col[4 * q + e], t);
+            }
+            col[r] = t;
+        }
+        if (g4 == 0) {
+#pragma unroll
+            for (int r = 0; r < 16; ++r) T[(16 * w + r) * LDA + 16 * w + m] = col[r];
+        }
+    }
+    __syncthreads();
+#pragma unroll
+    for (int d = 1; d < 4; ++d) {
+        if (w >= d) {
+            const int j = w - d;
+            f32x4_t M = {0.f, 0.f, 0.f, 0.f}, R = {0.f, 0.f, 0.f, 0.f};
+            for (int k = j; k < w; ++k) {
+                const f32x4_t A = *reinterpret_cast<const f32x4_t *>(&s_A[i * LDA + 16 * k + 4 * g4]);
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    M = __builtin_amdgcn_mfma_f32_16x16x4f32(A[e], T[(16 * k + 4 * g4 + e) * LDA + 16 * j + m], M, 0, 0, 0);
+            }
+            const f32x4_t D = *reinterpret_cast<const f32x4_t *>(&T[i * LDA + 16 * w + 4 * g4]);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) R = __builtin_amdgcn_mfma_f32_16x16x4f32(-D[e], M[e], R, 0, 0, 0);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) T[(16 * w + 4 * g4 + e) * LDA + 16 * j + m] = R[e];
+        }
+        __syncthreads();
+    }
+    {
+        f32x4_t t[4];
+        float mx = 0.f;
+#pragma unroll
+        for (int jt = 0; jt < 4; ++jt) {
+            t[jt] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+            if (jt <= w) {
+                const f32x4_t x = *reinterpret_cast<const f32x4_t *>(&T[i * LDA + 16 * jt + 4 * g4]);
+                const f32x4_t be = *reinterpret_cast<const f32x4_t *>(&s_beta[16 * jt + 4 * g4]);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) t[jt][e] = x[e] * be[e];
+            }
+            mx = max_abs(t[jt], mx);
+        }
+        const RowScale sc = unit_scale(groups_max(mx));
+        if (g4 == 0) vec[V_T * CH + i] = exp2i(-sc.s);
+#pragma unroll
+        for (int ks = 0; ks < 2; ++ks)
+            if (ks <= w / 2) {
+                u32x4_t f, r;
+#pragma unroll
+                for (int q = 0; q < 2; ++q)
+#pragma unroll
+                    for (int e = 0; e < 4; e += 2) {
+                        const float x = t[2 * ks + q][e] * sc.sc, y = t[2 * ks + q][e + 1] * sc.sc;
+                        f[2 * q + e / 2] = f16_pair(x, y);
+                        r[2 * q + e / 2] = f16_rest(x, y, f[2 * q + e / 2]);
+                    }
+                const int at = w < 2 ? w : 2 * w - 2 + ks;
+                *reinterpret_cast<u32x4_t *>(unit + at * 1024 + lane * 16) = f;
+                *reinterpret_cast<u32x4_t *>(unit + (6 + at) * 1024 + lane * 16) = r;
+            }
+    }
+    if (tid < CH) {
+        const double G = s_G[tid], last = s_G[CH - 1];
+        const float f = s_f[0][tid], eg = expf((float)G);
+        vec[V_A * CH + tid] = eg * f;
+        vec[V_B * CH + tid] = eg * s_f[1][tid];
+        vec[V_C * CH + tid] = expf((float)(last - G)) * f;
+        vec[V_SK * CH + tid] = s_sc[0][tid];
+        vec[V_SQ * CH + tid] = s_sc[1][tid];
+        if (tid == 0) *reinterpret_cast<float *>(unit + UNIT_GAMMA) = expf((float)last);
+    }
+}
+
+// The chunks of one sequence, head and 64 columns, one after another.  Waves
+// 0-3 hold 16 columns of the state each, in registers from the first chunk to
+// the last; waves 4-7 bring the next chunk to LDS meanwhile: k and q as f16
+// rows, k transposed, and the operands of delta_prep_kernel.
+template <int DK>
+__global__ __launch_bounds__(512) void delta_scan_kernel(DeltaArgs a, const uint8_t *__restrict__ ws) {
+    constexpr int NT = DK / 16, NQ = DK / 32;
+    constexpr int ROWS = CH * DK * 2;                              // bytes of k, of q, of k transposed
+    constexpr int FR = 3 * ROWS, VEC = FR + 18 * 1024, BUF = VEC + V_COUNT * CH * 4 + 16;
+    __shared__ __align__(16) uint8_t s_buf[2][BUF];
+    const int tid = threadIdx.x, lane = tid & 63, m = lane & 15, g4 = lane >> 4;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    // the workgroups that read the same k and q on one XCD (they are dealt to
+    // the 8 XCDs in turn)
+    const int rep = a.hv / a.hk, blocks = a.dv / 64, per = rep * blocks;
+    const int group = blockIdx.x / (8 * per) * 8 + blockIdx.x % 8, in = blockIdx.x / 8 % per;
+    if (group >= a.n_seq * a.hk) return;
+    const int b = group / a.hk, hk = group % a.hk, h = hk * rep + in / blocks;
+    const int col0 = in % blocks * 64;
+    int t0, t1;
+    seq_rows(a, b, t0, t1);
+    const int chunks = (t1 - t0 + CH - 1) / CH;
+    const uint8_t *units = ws + ((int64_t)first_chunk(t0, b) * a.hv + h) * UNIT;
+    const int64_t unit_step = (int64_t)a.hv * UNIT;
+    constexpr int MASK = DK / 8 - 1;
+    // chunk `at` (8 f16) of row `row` of k (which 0) or q (1)
+    auto row_at = [](int which, int row, int at) { return which * ROWS + (row * (DK / 8) + (at ^ (row & MASK))) * 16; };
+    // and of row d of k transposed
+    auto col_at = [](int d, int at) { return 2 * ROWS + (d * (CH / 8) + (at ^ ((d ^ d >> 3) & 7))) * 16; };
+
+    if (wave >= 4) {
+        // ---- producers
+        const int p = tid - 256;
+        constexpr int KI = 32 * (DK / 8) / 256, QI = CH * (DK / 8) / 256;  // items: row pairs x 8 of k, rows x 8 of q
+        constexpr int QN = QI;
+        u32x4_t k_reg[KI][2], q_reg[QN], f_reg[5];
+        float v_reg[2], k_sc[KI][2], q_sc[QN];
+        auto load = [&](int c) {
+            const int64_t r0 = t0 + (int64_t)c * CH;
+            const int len = t1 - r0 < CH ? (int)(t1 - r0) : CH;
+            const uint8_t *unit = units + c * unit_step;
+            const float *vec = reinterpret_cast<const float *>(unit + UNIT_VEC);
+            const u32x4_t zero = {0, 0, 0, 0};
+#pragma unroll
+            for (int it = 0; it < KI; ++it) {
+                const int x = it * 256 + p, pair = x / (DK / 8), at = x % (DK / 8);
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    k_sc[it][e] = vec[V_SK * CH + 2 * pair + e];
+                    k_reg[it][e] = 2 * pair + e < len ? *reinterpret_cast<const u32x4_t *>(
+                                                            a.k + (r0 + 2 * pair + e) * a.ldk + hk * DK + at * 8)
+                                                      : zero;
+                }
+            }
+#pragma unroll
+            for (int it = 0; it < QN; ++it) {
+                const int x = it * 256 + p, row = x / (DK / 8), at = x % (DK / 8);
+                q_sc[it] = vec[V_SQ * CH + row];
+                q_reg[it] = row < len ? *reinterpret_cast<const u32x4_t *>(a.q + (r0 + row) * a.ldq + hk * DK + at * 8)
+                                      : zero;
+            }
+#pragma unroll
+            for (int it = 0; it < 5; ++it)
+                if (it < 4 || p < 128)
+                    f_reg[it] = *reinterpret_cast<const u32x4_t *>(unit + (it * 256 + p) * 16);
+#pragma unroll
+            for (int it = 0; it < 2; ++it)
+                if (it * 256 + p <= V_COUNT * CH)
+                    v_reg[it] = *reinterpret_cast<const float *>(unit + UNIT_VEC + (it * 256 + p) * 4);
+        };
+        // 8 bf16 times f as f16
+        auto halves = [](u32x4_t x, float f) {
+            u32x4_t r;
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                r[e] = f16_pair(__uint_as_float(x[e] << 16) * f, __uint_as_float(x[e] & 0xffff0000u) * f);
+            return r;
+        };
+        // inner order of the products: elements 0-3 of an 8-chunk u of a block
+        // of 32 to chunk 2 (u % 2), 4-7 to the next, half u / 2
+        auto store_row = [&](uint8_t *buf, int which, int row, int at, u32x4_t x) {
+            const int blk = at / 4, u = at % 4;
+            uint8_t *d = buf + (u / 2) * 8;
+            *reinterpret_cast<uint2 *>(d + row_at(which, row, 4 * blk + 2 * (u & 1))) = make_uint2(x[0], x[1]);
+            *reinterpret_cast<uint2 *>(d + row_at(which, row, 4 * blk + 2 * (u & 1) + 1)) = make_uint2(x[2], x[3]);
+        };
+        auto store = [&](int c) {
+            uint8_t *buf = s_buf[c & 1];
+#pragma unroll
+            for (int it = 0; it < KI; ++it) {
+                const int x = it * 256 + p, pair = x / (DK / 8), at = x % (DK / 8);
+                const u32x4_t r0 = halves(k_reg[it][0], k_sc[it][0]), r1 = halves(k_reg[it][1], k_sc[it][1]);
+                store_row(buf, 0, 2 * pair, at, r0);
+                store_row(buf, 0, 2 * pair + 1, at, r1);
+                const int o = 2 * pair % 32, slot = 4 * (pair / 16) + o % 16 / 4, in8 = (o / 16) * 4 + o % 4;
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    const uint32_t two = __builtin_amdgcn_perm(r1[e / 2], r0[e / 2], e & 1 ? 0x07060302u : 0x05040100u);
+                    *reinterpret_cast<uint32_t *>(buf + col_at(8 * at + e, slot) + in8 * 2) = two;
+                }
+            }
+#pragma unroll
+            for (int it = 0; it < QN; ++it) {
+                const int x = it * 256 + p, row = x / (DK / 8), at = x % (DK / 8);
+                store_row(buf, 1, row, at, halves(q_reg[it], q_sc[it]));
+            }
+#pragma unroll
+            for (int it = 0; it < 5; ++it)
+                if (it < 4 || p < 128) *reinterpret_cast<u32x4_t *>(buf + FR + (it * 256 + p) * 16) = f_reg[it];
+#pragma unroll
+            for (int it = 0; it < 2; ++it)
+                if (it * 256 + p <= V_COUNT * CH) *reinterpret_cast<float *>(buf + VEC + (it * 256 + p) * 4) = v_reg[it];
+        };
+        if (chunks > 0) {
+            load(0);
+            store(0);
+            if (chunks > 1) load(1);
+        }
+        __syncthreads();
+        for (int c = 0; c < chunks; ++c) {
+            if (c + 1 < chunks) {
+                store(c + 1);
+                if (c + 2 < chunks) load(c + 2);
+            }
+            __syncthreads();
+        }
+        return;
+    }
+
+    // ---- the state's waves
+    const int slot = a.state_idx ? a.state_idx[b] : b;
+    const bool kept = slot >= 0 && slot < a.n_states;
+    const int col = col0 + 16 * wave + m;
+    const int64_t soff = ((int64_t)(kept ? slot : 0) * a.hv + h) * DK * a.dv + col;
+    f32x4_t S[NT];
+#pragma unroll
+    for (int t = 0; t < NT; ++t)
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            S[t][e] = kept && a.s_in ? a.s_in[soff + (int64_t)(16 * t + 4 * g4 + e) * a.dv] : 0.f;
+    uint16_t v_next[16];
+    auto load_v = [&](int c) {
+        const int64_t r0 = t0 + (int64_t)c * CH;
+        const int len = t1 - r0 < CH ? (int)(t1 - r0) : CH;
+#pragma unroll
+        for (int t = 0; t < 4; ++t)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const int row = 16 * t + 4 * g4 + e;
+                v_next[4 * t + e] = a.v[(r0 + (row < len ? row : len - 1)) * a.ldv + (int64_t)h * a.dv + col];
+            }
+    };
+    if (chunks > 0) load_v(0);
+    const f32x4_t zero4 = {0.f, 0.f, 0.f, 0.f};
+    __syncthreads();
+    for (int c = 0; c < chunks; ++c) {
+        const uint8_t *buf = s_buf[c & 1];
+        auto frag = [&](int at) { return *reinterpret_cast<const u32x4_t *>(buf + at); };
+        auto vec4 = [&](int which, int t) {
+            return *reinterpret_cast<const f32x4_t *>(buf + VEC + (which * CH + 16 * t + 4 * g4) * 4);
+        };
+        float v[16];
+#pragma unroll
+        for (int x = 0; x < 16; ++x) v[x] = bf16_to_f32(v_next[x]);
+        if (c + 1 < chunks) load_v(c + 1);
+        const float gamma = *reinterpret_cast<const float *>(buf + VEC + V_COUNT * CH * 4);
+
+        // the state as right operand
+        u32x4_t sh[NQ], sl[NQ];
+        float mx = 0.f;
+#pragma unroll
+        for (int t = 0; t < NT; ++t) mx = max_abs(S[t], mx);
+        const RowScale ss = unit_scale(groups_max(mx));
+        const float s_off = exp2i(-ss.s);
+#pragma unroll
+        for (int t = 0; t < NT; ++t)
+#pragma unroll
+            for (int e = 0; e < 4; e += 2) {
+                const float x = S[t][e] * ss.sc, y = S[t][e + 1] * ss.sc;
+                const uint32_t f = f16_pair(x, y);
+                sh[t / 2][2 * (t & 1) + e / 2] = f;
+                sl[t / 2][2 * (t & 1) + e / 2] = f16_rest(x, y, f);
+            }
+        // K S and Q S, X = V - diag(e^G) K S
+        f32x4_t QS[4], X[4];
+        mx = 0.f;
+#pragma unroll
+        for (int t = 0; t < 4; ++t) {
+            f32x4_t ks = zero4, kl = zero4;
+            QS[t] = zero4;
+#pragma unroll
+            for (int q = 0; q < NQ; ++q) {
+                const u32x4_t fk = frag(row_at(0, 16 * t + m, 4 * q + g4)), fq = frag(row_at(1, 16 * t + m, 4 * q + g4));
+                ks = mfma_f16(fk, sh[q], ks);
+                QS[t] = mfma_f16(fq, sh[q], QS[t]);
+                kl = mfma_f16(fk, sl[q], kl);
+            }
+            const f32x4_t fa = vec4(V_A, t);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) X[t][e] = fmaf(-(ks[e] + kl[e]) * s_off, fa[e], v[4 * t + e]);
+            mx = max_abs(X[t], mx);
+        }
+        // U = T' X
+        const RowScale xs = unit_scale(groups_max(mx));
+        const float x_off = exp2i(-xs.s);
+        u32x4_t xh[2], xl[2];
+#pragma unroll
+        for (int t = 0; t < 4; ++t)
+#pragma unroll
+            for (int e = 0; e < 4; e += 2) {
+                const float x = X[t][e] * xs.sc, y = X[t][e + 1] * xs.sc;
+                const uint32_t f = f16_pair(x, y);
+                xh[t / 2][2 * (t & 1) + e / 2] = f;
+                xl[t / 2][2 * (t & 1) + e / 2] = f16_rest(x, y, f);
+            }
+        f32x4_t U[4];
+        mx = 0.f;
+#pragma unroll
+        for (int t = 0; t < 4; ++t) {
+            f32x4_t hh = zero4, hl = zero4;
+#pragma unroll
+            for (int ks = 0; ks <= t / 2; ++ks) {
+                const int at = FR + frag_index(t, ks) * 1024 + lane * 16;
+                const u32x4_t th = frag(at), tl = frag(at + 6 * 1024);
+                hh = mfma_f16(th, xh[ks], hh);
+                hl = mfma_f16(th, xl[ks], hl);
+                hl = mfma_f16(tl, xh[ks], hl);
+            }
+            const f32x4_t ft = vec4(V_T, t);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) U[t][e] = (hh[e] + hl[e]) * (ft[e] * x_off);
+            mx = max_abs(U[t], mx);
+        }
+        // O = diag(b) Q S + P U
+        const RowScale us = unit_scale(groups_max(mx));
+        const float u_off = exp2i(-us.s);
+        u32x4_t uh[2];
+#pragma unroll
+        for (int t = 0; t < 4; ++t)
+#pragma unroll
+            for (int e = 0; e < 4; e += 2)
+                uh[t / 2][2 * (t & 1) + e / 2] = f16_pair(U[t][e] * us.sc, U[t][e + 1] * us.sc);
+        const int64_t r0 = t0 + (int64_t)c * CH;
+        const int len = t1 - r0 < CH ? (int)(t1 - r0) : CH;
+#pragma unroll
+        for (int t = 0; t < 4; ++t) {
+            f32x4_t o = zero4;
+#pragma unroll
+            for (int ks = 0; ks <= t / 2; ++ks)
+                o = mfma_f16(frag(FR + (12 + frag_index(t, ks)) * 1024 + lane * 16), uh[ks], o);
+            const f32x4_t fb = vec4(V_B, t), fp = vec4(V_P, t);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const int row = 16 * t + 4 * g4 + e;
+                const float z = fmaf(QS[t][e] * s_off, fb[e], o[e] * (fp[e] * u_off));
+                if (row < len) a.o[(r0 + row) * a.ldo + (int64_t)h * a.dv + col] = f32_to_bf16_rne(z);
+            }
+        }
+        // S = e^{G_63} S + K^T diag(c) U
+        mx = 0.f;
+#pragma unroll
+        for (int t = 0; t < 4; ++t) {
+            const f32x4_t fc = vec4(V_C, t);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) U[t][e] *= fc[e];
+            mx = max_abs(U[t], mx);
+        }
+        const RowScale ws_ = unit_scale(groups_max(mx));
+        const float w_off = exp2i(-ws_.s);
+        u32x4_t wh[2], wl[2];
+#pragma unroll
+        for (int t = 0; t < 4; ++t)
+#pragma unroll
+            for (int e = 0; e < 4; e += 2) {
+                const float x = U[t][e] * ws_.sc, y = U[t][e + 1] * ws_.sc;
+                const uint32_t f = f16_pair(x, y);
+                wh[t / 2][2 * (t & 1) + e / 2] = f;
+                wl[t / 2][2 * (t & 1) + e / 2] = f16_rest(x, y, f);
+            }
+#pragma unroll
+        for (int t = 0; t < NT; ++t) {
+            f32x4_t dh = zero4, dl = zero4;
+#pragma unroll
+            for (int ks = 0; ks < 2; ++ks) {
+                const u32x4_t fk = frag(col_at(16 * t + m, 4 * ks + g4));
+                dh = mfma_f16(fk, wh[ks], dh);
+                dl = mfma_f16(fk, wl[ks], dl);
+            }
+#pragma unroll
+            for (int e = 0; e < 4; ++e) S[t][e] = fmaf(gamma, S[t][e], (dh[e] + dl[e]) * w_off);
+        }
+        __syncthreads();
+    }
+    if (kept && a.s_out && !(chunks == 0 && a.s_in == a.s_out)) {
+#pragma unroll
+        for (int t = 0; t < NT; ++t)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) a.s_out[soff + (int64_t)(16 * t + 4 * g4 + e) * a.dv] = S[t][e];
+    }
+}
+
+template <int DK>
+hipError_t launch_chunks(const DeltaArgs &a, void *ws, hipStream_t s) {
+    if (a.T > 0)
+        hipLaunchKernelGGL((delta_prep_kernel<DK>), dim3((unsigned)((a.T / CH + a.n_seq) * a.hv)), dim3(256), 0, s, a,
+                           static_cast<uint8_t *>(ws));
+    const int64_t groups = (int64_t)a.n_seq * a.hk, per = a.hv / a.hk * (a.dv / 64);
+    hipLaunchKernelGGL((delta_scan_kernel<DK>), dim3((unsigned)((groups + 7) / 8 * 8 * per)), dim3(512), 0, s, a,
+                       static_cast<const uint8_t *>(ws));
+    return hipGetLastError();
+}
+
 }  // namespace
+
+size_t delta_workspace_bytes(int64_t T, int n_seq, int hv) { return (size_t)(T / CH + n_seq) * hv * UNIT; }
+
+hipError_t launch_delta_prefill(const DeltaArgs &a, void *ws, hipStream_t s) {
+    return a.dk == 64 ? launch_chunks<64>(a, ws, s) : launch_chunks<128>(a, ws, s);
+}
 
 hipError_t launch_delta_decode(const DeltaArgs &a, hipStream_t s) {
     if (a.dk == 64) return a.dv == 64 ? launch_decode<64, 64>(a, s) : launch_decode<64, 128>(a, s);

@@ -223,19 +223,22 @@ def test_malformed_starts_stay_in_bounds(kind):
 
 @pytest.mark.parametrize("kind", KINDS)
 def test_nan_stays_in_its_sequence(kind):
-    lens = [70, 70]
+    """Other sequences and the chunks (tokens, in decode) before it keep
+    their bits."""
+    lens = [140, 70]
     q, k, v, g, beta, s0, start = inputs(lens, 2, 4, 128, 128, True, 10)
     outs = []
     for bad in (False, True):
         if bad:
-            v[10], k[30, 0, 3] = float("nan"), float("inf")
-        o, s1 = torch.zeros(140, 4, 128, dtype=torch.bfloat16, device="cuda"), torch.zeros_like(s0)
+            v[80], k[100, 0, 3] = float("nan"), float("inf")
+        o, s1 = torch.zeros(210, 4, 128, dtype=torch.bfloat16, device="cuda"), torch.zeros_like(s0)
         call(kind, q, k, v, g, beta, start, None, s0, s1, o, 0.1, True)
         outs.append((o, s1))
     torch.cuda.synchronize()
-    assert torch.equal(outs[0][0][70:], outs[1][0][70:]) and torch.equal(outs[0][1][1], outs[1][1][1])
-    assert torch.equal(outs[0][0][:10], outs[1][0][:10])  # causal: earlier tokens too
-    assert torch.isnan(outs[1][0][10]).all()
+    assert torch.equal(outs[0][0][140:], outs[1][0][140:]) and torch.equal(outs[0][1][1], outs[1][1][1])
+    before = 80 if kind == "decode" else 64
+    assert torch.equal(outs[0][0][:before], outs[1][0][:before])
+    assert torch.isnan(outs[1][0][80]).all()
 
 
 def test_decode_continues_a_prompt():
