@@ -184,6 +184,16 @@ __device__ __forceinline__ RowScale unit_scale(float m) {
     be = be < 15 ? 15 : (be > 254 ? 254 : be);
     return RowScale{__uint_as_float((uint32_t)(268 - be) << 23), 141 - be};
 }
+// v sc as f16 and its remainder, half `which` of a right operand.
+__device__ __forceinline__ void split(f32x4_t v, float sc, u32x4_t &first, u32x4_t &rest, int which) {
+#pragma unroll
+    for (int e = 0; e < 4; e += 2) {
+        const f16x2_t h = {(_Float16)(v[e] * sc), (_Float16)(v[e + 1] * sc)};
+        const f16x2_t r = {(_Float16)fmaf(v[e], sc, -(float)h[0]), (_Float16)fmaf(v[e + 1], sc, -(float)h[1])};
+        first[2 * which + e / 2] = __builtin_bit_cast(uint32_t, h);
+        rest[2 * which + e / 2] = __builtin_bit_cast(uint32_t, r);
+    }
+}
 // Largest over the four lane groups (lanes l, l ^ 16, l ^ 32, l ^ 48).
 __device__ __forceinline__ float groups_max(float v) {
     typedef unsigned int u32x2_t __attribute__((ext_vector_type(2)));
@@ -195,6 +205,16 @@ __device__ __forceinline__ float groups_max(float v) {
 }
 __device__ __forceinline__ float max_abs(f32x4_t v, float m) {
     return fmaxf(fmaxf(fmaxf(fabsf(v[0]), fabsf(v[1])), fmaxf(fabsf(v[2]), fabsf(v[3]))), m);
+}
+
+// Barrier that orders LDS only: loads and stores in flight stay in flight
+// (waiting for them at every chunk took 4.6 us a chunk).
+__device__ __forceinline__ void lds_barrier() {
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_s_waitcnt(0xc07f);  // lgkmcnt(0)
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
 }
 
 // Rows [t0, t1) of sequence b, inside [0, T].
@@ -447,12 +467,14 @@ __global__ __launch_bounds__(256) void delta_prep_kernel(DeltaArgs a, uint8_t *_
     }
 }
 
-// The chunks of one sequence, head and 64 columns, one after another.  Waves
-// 0-3 hold 16 columns of the state each, in registers from the first chunk to
-// the last; waves 4-7 bring the next chunk to LDS meanwhile: k and q as f16
-// rows, k transposed, and the operands of delta_prep_kernel.
-template <int DK>
-__global__ __launch_bounds__(512) void delta_scan_kernel(DeltaArgs a, const uint8_t *__restrict__ ws) {
+// The chunks of one sequence, head and 16 COMP columns, one after another.
+// The first COMP waves hold 16 columns of the state each, in registers from
+// the first chunk to the last; the others (PROD waves) bring the next chunk to
+// LDS meanwhile: k and q as f16 rows, k transposed, and the operands of
+// delta_prep_kernel.  Bound by a state wave's own chain (products, then the
+// vector work between them) once a chunk's loads are out of its way.
+template <int DK, int COMP, int PROD>
+__global__ __launch_bounds__(64 * (COMP + PROD)) void delta_scan_kernel(DeltaArgs a, const uint8_t *__restrict__ ws) {
     constexpr int NT = DK / 16, NQ = DK / 32;
     constexpr int ROWS = CH * DK * 2;                              // bytes of k, of q, of k transposed
     constexpr int FR = 3 * ROWS, VEC = FR + 18 * 1024, BUF = VEC + V_COUNT * CH * 4 + 16;
@@ -461,11 +483,11 @@ __global__ __launch_bounds__(512) void delta_scan_kernel(DeltaArgs a, const uint
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     // the workgroups that read the same k and q on one XCD (they are dealt to
     // the 8 XCDs in turn)
-    const int rep = a.hv / a.hk, blocks = a.dv / 64, per = rep * blocks;
+    const int rep = a.hv / a.hk, blocks = a.dv / (16 * COMP), per = rep * blocks;
     const int group = blockIdx.x / (8 * per) * 8 + blockIdx.x % 8, in = blockIdx.x / 8 % per;
     if (group >= a.n_seq * a.hk) return;
     const int b = group / a.hk, hk = group % a.hk, h = hk * rep + in / blocks;
-    const int col0 = in % blocks * 64;
+    const int col0 = in % blocks * (16 * COMP);
     int t0, t1;
     seq_rows(a, b, t0, t1);
     const int chunks = (t1 - t0 + CH - 1) / CH;
@@ -477,101 +499,122 @@ __global__ __launch_bounds__(512) void delta_scan_kernel(DeltaArgs a, const uint
     // and of row d of k transposed
     auto col_at = [](int d, int at) { return 2 * ROWS + (d * (CH / 8) + (at ^ ((d ^ d >> 3) & 7))) * 16; };
 
-    if (wave >= 4) {
-        // ---- producers
-        const int p = tid - 256;
-        constexpr int KI = 32 * (DK / 8) / 256, QI = CH * (DK / 8) / 256;  // items: row pairs x 8 of k, rows x 8 of q
-        constexpr int QN = QI;
-        u32x4_t k_reg[KI][2], q_reg[QN], f_reg[5];
-        float v_reg[2], k_sc[KI][2], q_sc[QN];
-        auto load = [&](int c) {
-            const int64_t r0 = t0 + (int64_t)c * CH;
-            const int len = t1 - r0 < CH ? (int)(t1 - r0) : CH;
-            const uint8_t *unit = units + c * unit_step;
-            const float *vec = reinterpret_cast<const float *>(unit + UNIT_VEC);
-            const u32x4_t zero = {0, 0, 0, 0};
+    if (wave >= COMP) {
+    // ---- bringing chunks to LDS: PN threads
+    constexpr int PN = 64 * PROD;
+    const int p = tid - 64 * COMP;
+    constexpr int K_ITEMS = 32 * (DK / 8), Q_ITEMS = CH * (DK / 8), F_ITEMS = 18 * 64, V_ITEMS = V_COUNT * CH + 1;
+    // items: row pairs x 8 of k, rows x 8 of q, 16 bytes of operands, vectors
+    constexpr int KI = (K_ITEMS + PN - 1) / PN, QN = (Q_ITEMS + PN - 1) / PN, FN = (F_ITEMS + PN - 1) / PN,
+                  VN = (V_ITEMS + PN - 1) / PN;
+    u32x4_t k_reg[KI][2], q_reg[QN], f_reg[FN];
+    float v_reg[VN], k_sc[KI][2], q_sc[QN];
+    // byte offsets of the thread's pieces from the chunk's first row (64 rows of
+    // at most 2^22 elements); pieces behind the last take the last one's again
+    uint32_t k_off[KI], q_off[QN];
+    int k_item[KI], q_item[QN];
 #pragma unroll
-            for (int it = 0; it < KI; ++it) {
-                const int x = it * 256 + p, pair = x / (DK / 8), at = x % (DK / 8);
+    for (int it = 0; it < KI; ++it) {
+        k_item[it] = it * PN + p < K_ITEMS ? it * PN + p : K_ITEMS - 1;
+        k_off[it] = (uint32_t)(2 * (k_item[it] / (DK / 8))) * (uint32_t)a.ldk * 2 + k_item[it] % (DK / 8) * 16;
+    }
 #pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    k_sc[it][e] = vec[V_SK * CH + 2 * pair + e];
-                    k_reg[it][e] = 2 * pair + e < len ? *reinterpret_cast<const u32x4_t *>(
-                                                            a.k + (r0 + 2 * pair + e) * a.ldk + hk * DK + at * 8)
-                                                      : zero;
-                }
+    for (int it = 0; it < QN; ++it) {
+        q_item[it] = it * PN + p < Q_ITEMS ? it * PN + p : Q_ITEMS - 1;
+        q_off[it] = (uint32_t)(q_item[it] / (DK / 8)) * (uint32_t)a.ldq * 2 + q_item[it] % (DK / 8) * 16;
+    }
+    auto load = [&](int c) {
+        const int64_t r0 = t0 + (int64_t)c * CH;
+        const int len = t1 - r0 < CH ? (int)(t1 - r0) : CH;
+        const uint8_t *unit = units + c * unit_step;
+        const uint8_t *kb = reinterpret_cast<const uint8_t *>(a.k + r0 * a.ldk + hk * DK),
+                      *qb = reinterpret_cast<const uint8_t *>(a.q + r0 * a.ldq + hk * DK);
+        const u32x4_t zero = {0, 0, 0, 0};
+#pragma unroll
+        for (int it = 0; it < KI; ++it)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const int row = 2 * (k_item[it] / (DK / 8)) + e;
+                k_sc[it][e] = *reinterpret_cast<const float *>(unit + (uint32_t)(UNIT_VEC + (V_SK * CH + row) * 4));
+                k_reg[it][e] = len == CH || row < len
+                                   ? *reinterpret_cast<const u32x4_t *>(kb + (k_off[it] + e * (uint32_t)a.ldk * 2))
+                                   : zero;
             }
 #pragma unroll
-            for (int it = 0; it < QN; ++it) {
-                const int x = it * 256 + p, row = x / (DK / 8), at = x % (DK / 8);
-                q_sc[it] = vec[V_SQ * CH + row];
-                q_reg[it] = row < len ? *reinterpret_cast<const u32x4_t *>(a.q + (r0 + row) * a.ldq + hk * DK + at * 8)
-                                      : zero;
+        for (int it = 0; it < QN; ++it) {
+            const int row = q_item[it] / (DK / 8);
+            q_sc[it] = *reinterpret_cast<const float *>(unit + (uint32_t)(UNIT_VEC + (V_SQ * CH + row) * 4));
+            q_reg[it] = len == CH || row < len ? *reinterpret_cast<const u32x4_t *>(qb + q_off[it]) : zero;
+        }
+#pragma unroll
+        for (int it = 0; it < FN; ++it) {
+            const int x = it * PN + p < F_ITEMS ? it * PN + p : F_ITEMS - 1;
+            f_reg[it] = *reinterpret_cast<const u32x4_t *>(unit + (uint32_t)(x * 16));
+        }
+#pragma unroll
+        for (int it = 0; it < VN; ++it) {
+            const int x = it * PN + p < V_ITEMS ? it * PN + p : V_ITEMS - 1;
+            v_reg[it] = *reinterpret_cast<const float *>(unit + (uint32_t)(UNIT_VEC + x * 4));
+        }
+    };
+    // 8 bf16 times f as f16
+    auto halves = [](u32x4_t x, float f) {
+        u32x4_t r;
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            r[e] = f16_pair(__uint_as_float(x[e] << 16) * f, __uint_as_float(x[e] & 0xffff0000u) * f);
+        return r;
+    };
+    // inner order of the products: elements 0-3 of an 8-chunk u of a block of
+    // 32 to chunk 2 (u % 2), 4-7 to the next, half u / 2
+    auto store_row = [&](uint8_t *buf, int which, int row, int at, u32x4_t x) {
+        const int blk = at / 4, u = at % 4;
+        uint8_t *d = buf + (u / 2) * 8;
+        *reinterpret_cast<uint2 *>(d + row_at(which, row, 4 * blk + 2 * (u & 1))) = make_uint2(x[0], x[1]);
+        *reinterpret_cast<uint2 *>(d + row_at(which, row, 4 * blk + 2 * (u & 1) + 1)) = make_uint2(x[2], x[3]);
+    };
+    // (pieces behind the last write the last one's values once more)
+    auto store = [&](int c) {
+        uint8_t *buf = s_buf[c & 1];
+#pragma unroll
+        for (int it = 0; it < KI; ++it) {
+            const int pair = k_item[it] / (DK / 8), at = k_item[it] % (DK / 8);
+            const u32x4_t r0 = halves(k_reg[it][0], k_sc[it][0]), r1 = halves(k_reg[it][1], k_sc[it][1]);
+            store_row(buf, 0, 2 * pair, at, r0);
+            store_row(buf, 0, 2 * pair + 1, at, r1);
+            const int o = 2 * pair % 32, slot = 4 * (pair / 16) + o % 16 / 4, in8 = (o / 16) * 4 + o % 4;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                const uint32_t two = __builtin_amdgcn_perm(r1[e / 2], r0[e / 2], e & 1 ? 0x07060302u : 0x05040100u);
+                *reinterpret_cast<uint32_t *>(buf + col_at(8 * at + e, slot) + in8 * 2) = two;
             }
+        }
 #pragma unroll
-            for (int it = 0; it < 5; ++it)
-                if (it < 4 || p < 128)
-                    f_reg[it] = *reinterpret_cast<const u32x4_t *>(unit + (it * 256 + p) * 16);
+        for (int it = 0; it < QN; ++it)
+            store_row(buf, 1, q_item[it] / (DK / 8), q_item[it] % (DK / 8), halves(q_reg[it], q_sc[it]));
 #pragma unroll
-            for (int it = 0; it < 2; ++it)
-                if (it * 256 + p <= V_COUNT * CH)
-                    v_reg[it] = *reinterpret_cast<const float *>(unit + UNIT_VEC + (it * 256 + p) * 4);
-        };
-        // 8 bf16 times f as f16
-        auto halves = [](u32x4_t x, float f) {
-            u32x4_t r;
+        for (int it = 0; it < FN; ++it) {
+            const int x = it * PN + p < F_ITEMS ? it * PN + p : F_ITEMS - 1;
+            *reinterpret_cast<u32x4_t *>(buf + FR + x * 16) = f_reg[it];
+        }
 #pragma unroll
-            for (int e = 0; e < 4; ++e)
-                r[e] = f16_pair(__uint_as_float(x[e] << 16) * f, __uint_as_float(x[e] & 0xffff0000u) * f);
-            return r;
-        };
-        // inner order of the products: elements 0-3 of an 8-chunk u of a block
-        // of 32 to chunk 2 (u % 2), 4-7 to the next, half u / 2
-        auto store_row = [&](uint8_t *buf, int which, int row, int at, u32x4_t x) {
-            const int blk = at / 4, u = at % 4;
-            uint8_t *d = buf + (u / 2) * 8;
-            *reinterpret_cast<uint2 *>(d + row_at(which, row, 4 * blk + 2 * (u & 1))) = make_uint2(x[0], x[1]);
-            *reinterpret_cast<uint2 *>(d + row_at(which, row, 4 * blk + 2 * (u & 1) + 1)) = make_uint2(x[2], x[3]);
-        };
-        auto store = [&](int c) {
-            uint8_t *buf = s_buf[c & 1];
-#pragma unroll
-            for (int it = 0; it < KI; ++it) {
-                const int x = it * 256 + p, pair = x / (DK / 8), at = x % (DK / 8);
-                const u32x4_t r0 = halves(k_reg[it][0], k_sc[it][0]), r1 = halves(k_reg[it][1], k_sc[it][1]);
-                store_row(buf, 0, 2 * pair, at, r0);
-                store_row(buf, 0, 2 * pair + 1, at, r1);
-                const int o = 2 * pair % 32, slot = 4 * (pair / 16) + o % 16 / 4, in8 = (o / 16) * 4 + o % 4;
-#pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    const uint32_t two = __builtin_amdgcn_perm(r1[e / 2], r0[e / 2], e & 1 ? 0x07060302u : 0x05040100u);
-                    *reinterpret_cast<uint32_t *>(buf + col_at(8 * at + e, slot) + in8 * 2) = two;
-                }
-            }
-#pragma unroll
-            for (int it = 0; it < QN; ++it) {
-                const int x = it * 256 + p, row = x / (DK / 8), at = x % (DK / 8);
-                store_row(buf, 1, row, at, halves(q_reg[it], q_sc[it]));
-            }
-#pragma unroll
-            for (int it = 0; it < 5; ++it)
-                if (it < 4 || p < 128) *reinterpret_cast<u32x4_t *>(buf + FR + (it * 256 + p) * 16) = f_reg[it];
-#pragma unroll
-            for (int it = 0; it < 2; ++it)
-                if (it * 256 + p <= V_COUNT * CH) *reinterpret_cast<float *>(buf + VEC + (it * 256 + p) * 4) = v_reg[it];
-        };
+        for (int it = 0; it < VN; ++it) {
+            const int x = it * PN + p < V_ITEMS ? it * PN + p : V_ITEMS - 1;
+            *reinterpret_cast<float *>(buf + VEC + x * 4) = v_reg[it];
+        }
+    };
         if (chunks > 0) {
             load(0);
             store(0);
             if (chunks > 1) load(1);
         }
-        __syncthreads();
+        lds_barrier();
         for (int c = 0; c < chunks; ++c) {
             if (c + 1 < chunks) {
                 store(c + 1);
                 if (c + 2 < chunks) load(c + 2);
             }
-            __syncthreads();
+            lds_barrier();
         }
         return;
     }
@@ -587,21 +630,31 @@ __global__ __launch_bounds__(512) void delta_scan_kernel(DeltaArgs a, const uint
 #pragma unroll
         for (int e = 0; e < 4; ++e)
             S[t][e] = kept && a.s_in ? a.s_in[soff + (int64_t)(16 * t + 4 * g4 + e) * a.dv] : 0.f;
+    // rows 16 t + 4 g4 + e of v and o: a uniform base and the lane's offset
     uint16_t v_next[16];
+    const uint32_t v_lane = ((uint32_t)(4 * g4) * (uint32_t)a.ldv + m) * 2;
+    const uint32_t o_lane = ((uint32_t)(4 * g4) * (uint32_t)a.ldo + m) * 2;
+    const int64_t head_col = (int64_t)h * a.dv + col0 + 16 * wave;
     auto load_v = [&](int c) {
         const int64_t r0 = t0 + (int64_t)c * CH;
         const int len = t1 - r0 < CH ? (int)(t1 - r0) : CH;
+        const uint16_t *base = a.v + r0 * a.ldv + head_col;
+        if (len == CH) {
 #pragma unroll
-        for (int t = 0; t < 4; ++t)
+            for (int x = 0; x < 16; ++x)
+                v_next[x] = *reinterpret_cast<const uint16_t *>(
+                    reinterpret_cast<const uint8_t *>(base + (int64_t)(16 * (x / 4) + x % 4) * a.ldv) + v_lane);
+        } else {
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const int row = 16 * t + 4 * g4 + e;
-                v_next[4 * t + e] = a.v[(r0 + (row < len ? row : len - 1)) * a.ldv + (int64_t)h * a.dv + col];
+            for (int x = 0; x < 16; ++x) {
+                const int row = 16 * (x / 4) + 4 * g4 + x % 4;
+                v_next[x] = base[(int64_t)(row < len ? row : len - 1) * a.ldv + m];
             }
+        }
     };
     if (chunks > 0) load_v(0);
     const f32x4_t zero4 = {0.f, 0.f, 0.f, 0.f};
-    __syncthreads();
+    lds_barrier();
     for (int c = 0; c < chunks; ++c) {
         const uint8_t *buf = s_buf[c & 1];
         auto frag = [&](int at) { return *reinterpret_cast<const u32x4_t *>(buf + at); };
@@ -611,7 +664,7 @@ __global__ __launch_bounds__(512) void delta_scan_kernel(DeltaArgs a, const uint
         float v[16];
 #pragma unroll
         for (int x = 0; x < 16; ++x) v[x] = bf16_to_f32(v_next[x]);
-        if (c + 1 < chunks) load_v(c + 1);
+        load_v(c + 1 < chunks ? c + 1 : c);
         const float gamma = *reinterpret_cast<const float *>(buf + VEC + V_COUNT * CH * 4);
 
         // the state as right operand
@@ -622,123 +675,132 @@ __global__ __launch_bounds__(512) void delta_scan_kernel(DeltaArgs a, const uint
         const RowScale ss = unit_scale(groups_max(mx));
         const float s_off = exp2i(-ss.s);
 #pragma unroll
-        for (int t = 0; t < NT; ++t)
-#pragma unroll
-            for (int e = 0; e < 4; e += 2) {
-                const float x = S[t][e] * ss.sc, y = S[t][e + 1] * ss.sc;
-                const uint32_t f = f16_pair(x, y);
-                sh[t / 2][2 * (t & 1) + e / 2] = f;
-                sl[t / 2][2 * (t & 1) + e / 2] = f16_rest(x, y, f);
-            }
-        // K S and Q S, X = V - diag(e^G) K S
+        for (int t = 0; t < NT; ++t) split(S[t], ss.sc, sh[t / 2], sl[t / 2], t & 1);
+        // K S, X = V - diag(e^G) K S (the remainders' products go into the same
+        // sums).  Here and below the inner index is the outer loop, so that
+        // products into one sum are four or more apart: one after another they
+        // wait for each other's result.
         f32x4_t QS[4], X[4];
+#pragma unroll
+        for (int t = 0; t < 4; ++t) X[t] = QS[t] = zero4;
+#pragma unroll
+        for (int q = 0; q < NQ; ++q) {
+            u32x4_t fk[4];
+#pragma unroll
+            for (int t = 0; t < 4; ++t) fk[t] = frag(row_at(0, 16 * t + m, 4 * q + g4));
+#pragma unroll
+            for (int t = 0; t < 4; ++t) X[t] = mfma_f16(fk[t], sl[q], X[t]);
+#pragma unroll
+            for (int t = 0; t < 4; ++t) X[t] = mfma_f16(fk[t], sh[q], X[t]);
+        }
         mx = 0.f;
 #pragma unroll
         for (int t = 0; t < 4; ++t) {
-            f32x4_t ks = zero4, kl = zero4;
-            QS[t] = zero4;
-#pragma unroll
-            for (int q = 0; q < NQ; ++q) {
-                const u32x4_t fk = frag(row_at(0, 16 * t + m, 4 * q + g4)), fq = frag(row_at(1, 16 * t + m, 4 * q + g4));
-                ks = mfma_f16(fk, sh[q], ks);
-                QS[t] = mfma_f16(fq, sh[q], QS[t]);
-                kl = mfma_f16(fk, sl[q], kl);
-            }
             const f32x4_t fa = vec4(V_A, t);
 #pragma unroll
-            for (int e = 0; e < 4; ++e) X[t][e] = fmaf(-(ks[e] + kl[e]) * s_off, fa[e], v[4 * t + e]);
+            for (int e = 0; e < 4; ++e) X[t][e] = fmaf(-X[t][e], fa[e] * s_off, v[4 * t + e]);
             mx = max_abs(X[t], mx);
         }
-        // U = T' X
+        // U = T' X (in units of 2^-xs.s), W = diag(c) U
         const RowScale xs = unit_scale(groups_max(mx));
         const float x_off = exp2i(-xs.s);
         u32x4_t xh[2], xl[2];
 #pragma unroll
-        for (int t = 0; t < 4; ++t)
+        for (int t = 0; t < 4; ++t) split(X[t], xs.sc, xh[t / 2], xl[t / 2], t & 1);
 #pragma unroll
-            for (int e = 0; e < 4; e += 2) {
-                const float x = X[t][e] * xs.sc, y = X[t][e + 1] * xs.sc;
-                const uint32_t f = f16_pair(x, y);
-                xh[t / 2][2 * (t & 1) + e / 2] = f;
-                xl[t / 2][2 * (t & 1) + e / 2] = f16_rest(x, y, f);
-            }
-        f32x4_t U[4];
+        for (int q = 0; q < NQ; ++q)
+#pragma unroll
+            for (int t = 0; t < 4; ++t) QS[t] = mfma_f16(frag(row_at(1, 16 * t + m, 4 * q + g4)), sh[q], QS[t]);
+        f32x4_t U[4], W[4];
+#pragma unroll
+        for (int t = 0; t < 4; ++t) U[t] = zero4;
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+#pragma unroll
+            for (int t = 2 * x; t < 4; ++t)
+                U[t] = mfma_f16(frag(FR + (6 + frag_index(t, x)) * 1024 + lane * 16), xh[x], U[t]);
+#pragma unroll
+            for (int t = 2 * x; t < 4; ++t) U[t] = mfma_f16(frag(FR + frag_index(t, x) * 1024 + lane * 16), xl[x], U[t]);
+#pragma unroll
+            for (int t = 2 * x; t < 4; ++t) U[t] = mfma_f16(frag(FR + frag_index(t, x) * 1024 + lane * 16), xh[x], U[t]);
+        }
         mx = 0.f;
+        float mw = 0.f;
 #pragma unroll
         for (int t = 0; t < 4; ++t) {
-            f32x4_t hh = zero4, hl = zero4;
+            const f32x4_t ft = vec4(V_T, t), fc = vec4(V_C, t);
 #pragma unroll
-            for (int ks = 0; ks <= t / 2; ++ks) {
-                const int at = FR + frag_index(t, ks) * 1024 + lane * 16;
-                const u32x4_t th = frag(at), tl = frag(at + 6 * 1024);
-                hh = mfma_f16(th, xh[ks], hh);
-                hl = mfma_f16(th, xl[ks], hl);
-                hl = mfma_f16(tl, xh[ks], hl);
+            for (int e = 0; e < 4; ++e) {
+                U[t][e] *= ft[e];
+                W[t][e] = U[t][e] * fc[e];
             }
-            const f32x4_t ft = vec4(V_T, t);
-#pragma unroll
-            for (int e = 0; e < 4; ++e) U[t][e] = (hh[e] + hl[e]) * (ft[e] * x_off);
             mx = max_abs(U[t], mx);
+            mw = max_abs(W[t], mw);
         }
+        // S = e^{G_63} S + K^T W first: the next chunk waits for it
+        const RowScale wsc = unit_scale(groups_max(mw));
+        const float w_off = exp2i(-wsc.s) * x_off;
+        u32x4_t wh[2], wl[2];
+#pragma unroll
+        for (int t = 0; t < 4; ++t) split(W[t], wsc.sc, wh[t / 2], wl[t / 2], t & 1);
+        f32x4_t D[NT];
+#pragma unroll
+        for (int t = 0; t < NT; ++t) D[t] = zero4;
+#pragma unroll
+        for (int x = 0; x < 2; ++x)
+#pragma unroll
+            for (int t4 = 0; t4 < NT; t4 += 4) {
+                u32x4_t fk[4];
+#pragma unroll
+                for (int t = 0; t < 4; ++t) fk[t] = frag(col_at(16 * (t4 + t) + m, 4 * x + g4));
+#pragma unroll
+                for (int t = 0; t < 4; ++t) D[t4 + t] = mfma_f16(fk[t], wl[x], D[t4 + t]);
+#pragma unroll
+                for (int t = 0; t < 4; ++t) D[t4 + t] = mfma_f16(fk[t], wh[x], D[t4 + t]);
+            }
+#pragma unroll
+        for (int t = 0; t < NT; ++t)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) S[t][e] = fmaf(D[t][e], w_off, gamma * S[t][e]);
         // O = diag(b) Q S + P U
         const RowScale us = unit_scale(groups_max(mx));
-        const float u_off = exp2i(-us.s);
+        const float u_off = exp2i(-us.s) * x_off;
         u32x4_t uh[2];
 #pragma unroll
         for (int t = 0; t < 4; ++t)
 #pragma unroll
             for (int e = 0; e < 4; e += 2)
                 uh[t / 2][2 * (t & 1) + e / 2] = f16_pair(U[t][e] * us.sc, U[t][e + 1] * us.sc);
-        const int64_t r0 = t0 + (int64_t)c * CH;
-        const int len = t1 - r0 < CH ? (int)(t1 - r0) : CH;
+        f32x4_t O[4];
+#pragma unroll
+        for (int t = 0; t < 4; ++t) O[t] = zero4;
+#pragma unroll
+        for (int x = 0; x < 2; ++x)
+#pragma unroll
+            for (int t = 2 * x; t < 4; ++t)
+                O[t] = mfma_f16(frag(FR + (12 + frag_index(t, x)) * 1024 + lane * 16), uh[x], O[t]);
 #pragma unroll
         for (int t = 0; t < 4; ++t) {
-            f32x4_t o = zero4;
-#pragma unroll
-            for (int ks = 0; ks <= t / 2; ++ks)
-                o = mfma_f16(frag(FR + (12 + frag_index(t, ks)) * 1024 + lane * 16), uh[ks], o);
             const f32x4_t fb = vec4(V_B, t), fp = vec4(V_P, t);
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const int row = 16 * t + 4 * g4 + e;
-                const float z = fmaf(QS[t][e] * s_off, fb[e], o[e] * (fp[e] * u_off));
-                if (row < len) a.o[(r0 + row) * a.ldo + (int64_t)h * a.dv + col] = f32_to_bf16_rne(z);
+            for (int e = 0; e < 4; ++e) O[t][e] = fmaf(QS[t][e], fb[e] * s_off, O[t][e] * (fp[e] * u_off));
+        }
+        const int64_t r0 = t0 + (int64_t)c * CH;
+        const int len = t1 - r0 < CH ? (int)(t1 - r0) : CH;
+        uint16_t *ob = a.o + r0 * a.ldo + head_col;
+        if (len == CH) {
+#pragma unroll
+            for (int x = 0; x < 16; ++x)
+                *reinterpret_cast<__bf16 *>(reinterpret_cast<uint8_t *>(ob + (int64_t)(16 * (x / 4) + x % 4) * a.ldo) +
+                                            o_lane) = (__bf16)O[x / 4][x % 4];
+        } else {
+#pragma unroll
+            for (int x = 0; x < 16; ++x) {
+                const int row = 16 * (x / 4) + 4 * g4 + x % 4;
+                if (row < len) *reinterpret_cast<__bf16 *>(ob + (int64_t)row * a.ldo + m) = (__bf16)O[x / 4][x % 4];
             }
         }
-        // S = e^{G_63} S + K^T diag(c) U
-        mx = 0.f;
-#pragma unroll
-        for (int t = 0; t < 4; ++t) {
-            const f32x4_t fc = vec4(V_C, t);
-#pragma unroll
-            for (int e = 0; e < 4; ++e) U[t][e] *= fc[e];
-            mx = max_abs(U[t], mx);
-        }
-        const RowScale ws_ = unit_scale(groups_max(mx));
-        const float w_off = exp2i(-ws_.s);
-        u32x4_t wh[2], wl[2];
-#pragma unroll
-        for (int t = 0; t < 4; ++t)
-#pragma unroll
-            for (int e = 0; e < 4; e += 2) {
-                const float x = U[t][e] * ws_.sc, y = U[t][e + 1] * ws_.sc;
-                const uint32_t f = f16_pair(x, y);
-                wh[t / 2][2 * (t & 1) + e / 2] = f;
-                wl[t / 2][2 * (t & 1) + e / 2] = f16_rest(x, y, f);
-            }
-#pragma unroll
-        for (int t = 0; t < NT; ++t) {
-            f32x4_t dh = zero4, dl = zero4;
-#pragma unroll
-            for (int ks = 0; ks < 2; ++ks) {
-                const u32x4_t fk = frag(col_at(16 * t + m, 4 * ks + g4));
-                dh = mfma_f16(fk, wh[ks], dh);
-                dl = mfma_f16(fk, wl[ks], dl);
-            }
-#pragma unroll
-            for (int e = 0; e < 4; ++e) S[t][e] = fmaf(gamma, S[t][e], (dh[e] + dl[e]) * w_off);
-        }
-        __syncthreads();
+        lds_barrier();
     }
     if (kept && a.s_out && !(chunks == 0 && a.s_in == a.s_out)) {
 #pragma unroll
@@ -753,9 +815,17 @@ hipError_t launch_chunks(const DeltaArgs &a, void *ws, hipStream_t s) {
     if (a.T > 0)
         hipLaunchKernelGGL((delta_prep_kernel<DK>), dim3((unsigned)((a.T / CH + a.n_seq) * a.hv)), dim3(256), 0, s, a,
                            static_cast<uint8_t *>(ws));
-    const int64_t groups = (int64_t)a.n_seq * a.hk, per = a.hv / a.hk * (a.dv / 64);
-    hipLaunchKernelGGL((delta_scan_kernel<DK>), dim3((unsigned)((groups + 7) / 8 * 8 * per)), dim3(512), 0, s, a,
-                       static_cast<const uint8_t *>(ws));
+    // One column tile of 16 per compute unit: a wave of its own; more: four of
+    // them share what is brought to LDS.
+    const int64_t tiles = (int64_t)a.n_seq * a.hv * (a.dv / 16);
+    const int comp = tiles > 256 ? 4 : 1;
+    const int64_t groups = (int64_t)a.n_seq * a.hk, per = a.hv / a.hk * (a.dv / (16 * comp));
+    const dim3 grid((unsigned)((groups + 7) / 8 * 8 * per));
+    const uint8_t *units = static_cast<const uint8_t *>(ws);
+    if (comp == 4)
+        hipLaunchKernelGGL((delta_scan_kernel<DK, 4, 4>), grid, dim3(512), 0, s, a, units);
+    else
+        hipLaunchKernelGGL((delta_scan_kernel<DK, 1, 3>), grid, dim3(256), 0, s, a, units);
     return hipGetLastError();
 }
 
