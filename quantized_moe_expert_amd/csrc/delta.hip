@@ -229,6 +229,11 @@ __device__ __forceinline__ void seq_rows(const DeltaArgs &a, int b, int &t0, int
 // a prefix sum, and stays below T / 64 + n_seq.
 __device__ __forceinline__ int first_chunk(int t0, int b) { return t0 / CH + b; }
 
+// e^d (d rounded to fp32 only after the factor log2 e).
+__device__ __forceinline__ float exp_diff(double d) {
+    return __builtin_amdgcn_exp2f((float)(d * 1.4426950408889634));
+}
+
 // T', P and the row factors of one chunk and head.  Wave w owns row tile w.
 // Bound by latency chains (the 16 x 16 inversions) and the 20 KB it writes.
 template <int DK>
@@ -260,29 +265,52 @@ __global__ __launch_bounds__(256) void delta_prep_kernel(DeltaArgs a, uint8_t *_
     const int len = t1 - t0 < CH ? t1 - t0 : CH;
     const int hk = h / (a.hv / a.hk);
 
-    // rows of k and q to f16
+    // rows of k and q to f16: every load first (rows behind the last read the
+    // last one's and are cleared)
     constexpr int MASK = DK / 8 - 1;
     auto place = [](int which, int row, int chunk) { return ((which * CH + row) * (DK / 8) + (chunk ^ (row & MASK))) * 16; };
+    const int64_t gate_at = (int64_t)(t0 + (lane < len ? lane : len - 1)) * a.hv + h;
+    const float g_raw = a.g[gate_at], beta_raw = a.beta[gate_at];
+    uint2 raw[2][4][PL / 4];
 #pragma unroll
     for (int which = 0; which < 2; ++which) {
-        const uint16_t *src = which ? a.q : a.k;
-        const int64_t ld = which ? a.ldq : a.ldk;
+        const uint8_t *base = reinterpret_cast<const uint8_t *>((which ? a.q + (int64_t)t0 * a.ldq : a.k + (int64_t)t0 * a.ldk) + hk * DK);
+        const uint32_t ld = (uint32_t)(which ? a.ldq : a.ldk) * 2;
 #pragma unroll
         for (int r4 = 0; r4 < 4; ++r4) {
             const int row = 16 * w + 4 * r4 + g4;
+            const uint32_t at = (uint32_t)(row < len ? row : len - 1) * ld + m * PL * 2;
+#pragma unroll
+            for (int e = 0; e < PL / 4; ++e) raw[which][r4][e] = *reinterpret_cast<const uint2 *>(base + (at + 8 * e));
+        }
+    }
+    {
+        const float gl = lane < len ? g_raw : 0.f;
+        double G = gl < -1000.f ? -1000.0 : (double)gl;  // e^-1000 is 0 too, and -inf - -inf is not
+        if (w == 0) {
+#pragma unroll
+            for (int o = 1; o < 64; o <<= 1) {
+                const double up = __shfl_up(G, o);
+                if (lane >= o) G += up;
+            }
+            s_G[lane] = G;
+            s_beta[lane] = lane < len ? beta_raw : 0.f;
+        }
+    }
+#pragma unroll
+    for (int which = 0; which < 2; ++which) {
+#pragma unroll
+        for (int r4 = 0; r4 < 4; ++r4) {
+            const int row = 16 * w + 4 * r4 + g4;
+            const uint32_t keep = row < len ? ~0u : 0u;
             float x[PL];
 #pragma unroll
-            for (int e = 0; e < PL; ++e) x[e] = 0.f;
-            if (row < len) {
-                const uint16_t *p = src + (int64_t)(t0 + row) * ld + hk * DK + m * PL;
-#pragma unroll
-                for (int e = 0; e < PL; e += 4) {
-                    const uint2 d = *reinterpret_cast<const uint2 *>(p + e);
-                    x[e] = __uint_as_float(d.x << 16);
-                    x[e + 1] = __uint_as_float(d.x & 0xffff0000u);
-                    x[e + 2] = __uint_as_float(d.y << 16);
-                    x[e + 3] = __uint_as_float(d.y & 0xffff0000u);
-                }
+            for (int e = 0; e < PL; e += 4) {
+                const uint32_t dx = raw[which][r4][e / 4].x & keep, dy = raw[which][r4][e / 4].y & keep;
+                x[e] = __uint_as_float(dx << 16);
+                x[e + 1] = __uint_as_float(dx & 0xffff0000u);
+                x[e + 2] = __uint_as_float(dy << 16);
+                x[e + 3] = __uint_as_float(dy & 0xffff0000u);
             }
             float mx = 0.f, ss = 0.f;
 #pragma unroll
@@ -306,18 +334,6 @@ __global__ __launch_bounds__(256) void delta_prep_kernel(DeltaArgs a, uint8_t *_
                 s_sc[which][row] = sc.sc;
             }
         }
-    }
-    if (w == 0) {
-        const int64_t at = (int64_t)(t0 + lane) * a.hv + h;
-        const float gl = lane < len ? a.g[at] : 0.f;
-        double G = gl < -1000.f ? -1000.0 : (double)gl;  // e^-1000 is 0 too, and -inf - -inf is not
-#pragma unroll
-        for (int o = 1; o < 64; o <<= 1) {
-            const double up = __shfl_up(G, o);
-            if (lane >= o) G += up;
-        }
-        s_G[lane] = G;
-        s_beta[lane] = lane < len ? a.beta[at] : 0.f;
     }
     __syncthreads();
 
@@ -350,7 +366,7 @@ __global__ __launch_bounds__(256) void delta_prep_kernel(DeltaArgs a, uint8_t *_
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
                     const int j = 16 * jt + 4 * g4 + e;
-                    const float d = j <= i ? expf((float)(Gi - s_G[j])) * s_f[0][j] : 0.f;
+                    const float d = j <= i ? exp_diff(Gi - s_G[j]) * s_f[0][j] : 0.f;
                     A[e] = j < i ? kk[e] * fi * d * bi : 0.f;
                     P[jt][e] = j <= i ? kq[e] * fqi * d : 0.f;
                 }
@@ -457,13 +473,13 @@ __global__ __launch_bounds__(256) void delta_prep_kernel(DeltaArgs a, uint8_t *_
     }
     if (tid < CH) {
         const double G = s_G[tid], last = s_G[CH - 1];
-        const float f = s_f[0][tid], eg = expf((float)G);
+        const float f = s_f[0][tid], eg = exp_diff(G);
         vec[V_A * CH + tid] = eg * f;
         vec[V_B * CH + tid] = eg * s_f[1][tid];
-        vec[V_C * CH + tid] = expf((float)(last - G)) * f;
+        vec[V_C * CH + tid] = exp_diff(last - G) * f;
         vec[V_SK * CH + tid] = s_sc[0][tid];
         vec[V_SQ * CH + tid] = s_sc[1][tid];
-        if (tid == 0) *reinterpret_cast<float *>(unit + UNIT_GAMMA) = expf((float)last);
+        if (tid == 0) *reinterpret_cast<float *>(unit + UNIT_GAMMA) = exp_diff(last);
     }
 }
 
@@ -667,6 +683,22 @@ __global__ __launch_bounds__(64 * (COMP + PROD)) void delta_scan_kernel(DeltaArg
         load_v(c + 1 < chunks ? c + 1 : c);
         const float gamma = *reinterpret_cast<const float *>(buf + VEC + V_COUNT * CH * 4);
 
+        // Operands are read a phase ahead of their products where registers
+        // allow (one wave per SIMD has 512): a phase is short against an LDS
+        // read.
+        constexpr bool AHEAD_K = COMP == 1, AHEAD = COMP == 1;
+        auto k_frag = [&](int t, int q) { return frag(row_at(0, 16 * t + m, 4 * q + g4)); };
+        auto q_frag = [&](int t, int q) { return frag(row_at(1, 16 * t + m, 4 * q + g4)); };
+        auto kt_frag = [&](int t, int x) { return frag(col_at(16 * t + m, 4 * x + g4)); };
+        auto op_frag = [&](int which, int t, int x) { return frag(FR + (6 * which + frag_index(t, x)) * 1024 + lane * 16); };
+        u32x4_t ak[AHEAD_K ? NQ : 1][4], aq[AHEAD ? NQ : 1][4], at_[AHEAD ? 18 : 1], akt[AHEAD ? NT : 1][2];
+        if (AHEAD_K) {
+#pragma unroll
+            for (int q = 0; q < NQ; ++q)
+#pragma unroll
+                for (int t = 0; t < 4; ++t) ak[q][t] = k_frag(t, q);
+            __builtin_amdgcn_sched_barrier(0);
+        }
         // the state as right operand
         u32x4_t sh[NQ], sl[NQ];
         float mx = 0.f;
@@ -683,11 +715,21 @@ __global__ __launch_bounds__(64 * (COMP + PROD)) void delta_scan_kernel(DeltaArg
         f32x4_t QS[4], X[4];
 #pragma unroll
         for (int t = 0; t < 4; ++t) X[t] = QS[t] = zero4;
+        if (AHEAD) {
+            __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+            for (int x = 0; x < 12; ++x) at_[x] = frag(FR + x * 1024 + lane * 16);
+#pragma unroll
+            for (int q = 0; q < NQ; ++q)
+#pragma unroll
+                for (int t = 0; t < 4; ++t) aq[q][t] = q_frag(t, q);
+            __builtin_amdgcn_sched_barrier(0);
+        }
 #pragma unroll
         for (int q = 0; q < NQ; ++q) {
             u32x4_t fk[4];
 #pragma unroll
-            for (int t = 0; t < 4; ++t) fk[t] = frag(row_at(0, 16 * t + m, 4 * q + g4));
+            for (int t = 0; t < 4; ++t) fk[t] = AHEAD_K ? ak[AHEAD_K ? q : 0][t] : k_frag(t, q);
 #pragma unroll
             for (int t = 0; t < 4; ++t) X[t] = mfma_f16(fk[t], sl[q], X[t]);
 #pragma unroll
@@ -710,19 +752,30 @@ __global__ __launch_bounds__(64 * (COMP + PROD)) void delta_scan_kernel(DeltaArg
 #pragma unroll
         for (int q = 0; q < NQ; ++q)
 #pragma unroll
-            for (int t = 0; t < 4; ++t) QS[t] = mfma_f16(frag(row_at(1, 16 * t + m, 4 * q + g4)), sh[q], QS[t]);
+            for (int t = 0; t < 4; ++t) QS[t] = mfma_f16(AHEAD ? aq[AHEAD ? q : 0][t] : q_frag(t, q), sh[q], QS[t]);
         f32x4_t U[4], W[4];
 #pragma unroll
         for (int t = 0; t < 4; ++t) U[t] = zero4;
+        if (AHEAD) {
+            __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+            for (int t = 0; t < NT; ++t)
+#pragma unroll
+                for (int x = 0; x < 2; ++x) akt[t][x] = kt_frag(t, x);
+#pragma unroll
+            for (int x = 12; x < 18; ++x) at_[x] = frag(FR + x * 1024 + lane * 16);
+            __builtin_amdgcn_sched_barrier(0);
+        }
+        auto op = [&](int which, int t, int x) { return AHEAD ? at_[AHEAD ? 6 * which + frag_index(t, x) : 0] : op_frag(which, t, x); };
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
 #pragma unroll
             for (int t = 2 * x; t < 4; ++t)
-                U[t] = mfma_f16(frag(FR + (6 + frag_index(t, x)) * 1024 + lane * 16), xh[x], U[t]);
+                U[t] = mfma_f16(op(1, t, x), xh[x], U[t]);
 #pragma unroll
-            for (int t = 2 * x; t < 4; ++t) U[t] = mfma_f16(frag(FR + frag_index(t, x) * 1024 + lane * 16), xl[x], U[t]);
+            for (int t = 2 * x; t < 4; ++t) U[t] = mfma_f16(op(0, t, x), xl[x], U[t]);
 #pragma unroll
-            for (int t = 2 * x; t < 4; ++t) U[t] = mfma_f16(frag(FR + frag_index(t, x) * 1024 + lane * 16), xh[x], U[t]);
+            for (int t = 2 * x; t < 4; ++t) U[t] = mfma_f16(op(0, t, x), xh[x], U[t]);
         }
         mx = 0.f;
         float mw = 0.f;
@@ -752,7 +805,7 @@ __global__ __launch_bounds__(64 * (COMP + PROD)) void delta_scan_kernel(DeltaArg
             for (int t4 = 0; t4 < NT; t4 += 4) {
                 u32x4_t fk[4];
 #pragma unroll
-                for (int t = 0; t < 4; ++t) fk[t] = frag(col_at(16 * (t4 + t) + m, 4 * x + g4));
+                for (int t = 0; t < 4; ++t) fk[t] = AHEAD ? akt[AHEAD ? t4 + t : 0][x] : kt_frag(t4 + t, x);
 #pragma unroll
                 for (int t = 0; t < 4; ++t) D[t4 + t] = mfma_f16(fk[t], wl[x], D[t4 + t]);
 #pragma unroll
@@ -778,7 +831,7 @@ __global__ __launch_bounds__(64 * (COMP + PROD)) void delta_scan_kernel(DeltaArg
         for (int x = 0; x < 2; ++x)
 #pragma unroll
             for (int t = 2 * x; t < 4; ++t)
-                O[t] = mfma_f16(frag(FR + (12 + frag_index(t, x)) * 1024 + lane * 16), uh[x], O[t]);
+                O[t] = mfma_f16(op(2, t, x), uh[x], O[t]);
 #pragma unroll
         for (int t = 0; t < 4; ++t) {
             const f32x4_t fb = vec4(V_B, t), fp = vec4(V_P, t);
