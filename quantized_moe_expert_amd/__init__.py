@@ -21,6 +21,7 @@ from ._backbone import (ACT_GELU, ACT_NONE, ACT_SILU, BACKBONE_EXPORTS, LINEAR_B
                         LinearWeights, delta_workspace_size, linear_struct, logprobs_workspace_size,
                         moe_q4_delta_decode, moe_q4_delta_prefill, moe_q4_linear, moe_q4_logprobs)
 from .layer import MoeQ4Layer
+from .mixer import DeltaMixer
 
 __all__ = ["ASYM_G64", "SYM_G128", "FP8_B128", "NVFP4", "WS_DECODE", "WS_GROUP", "WS_PREFILL", "WS_ROUTE", "EXPORTS", "MoeQ4Error",
            "error_string", "layer_struct", "lib", "moe_q4_decode", "moe_q4_dequant", "moe_q4_group",
@@ -33,4 +34,4 @@ __all__ = ["ASYM_G64", "SYM_G128", "FP8_B128", "NVFP4", "WS_DECODE", "WS_GROUP",
            "FRAME_MAX_LANES", "frame_workspace_size", "moe_q4_frame",
            "ACT_GELU", "ACT_NONE", "ACT_SILU", "BACKBONE_EXPORTS", "LINEAR_BF16", "LINEAR_INT8", "MAX_TOP", "DeltaShape",
            "LinearWeights", "delta_workspace_size", "linear_struct", "logprobs_workspace_size",
-           "moe_q4_delta_decode", "moe_q4_delta_prefill", "moe_q4_linear", "moe_q4_logprobs"]
+           "moe_q4_delta_decode", "moe_q4_delta_prefill", "moe_q4_linear", "moe_q4_logprobs", "DeltaMixer"]
