@@ -483,27 +483,36 @@ __global__ __launch_bounds__(256) void delta_prep_kernel(DeltaArgs a, uint8_t *_
     }
 }
 
-// The chunks of one sequence, head and 16 COMP columns, one after another.
-// The first COMP waves hold 16 columns of the state each, in registers from
-// the first chunk to the last; the others (PROD waves) bring the next chunk to
-// LDS meanwhile: k and q as f16 rows, k transposed, and the operands of
-// delta_prep_kernel.  Bound by a state wave's own chain (products, then the
-// vector work between them) once a chunk's loads are out of its way.
-template <int DK, int COMP, int PROD>
-__global__ __launch_bounds__(64 * (COMP + PROD)) void delta_scan_kernel(DeltaArgs a, const uint8_t *__restrict__ ws) {
+// The chunks of one sequence and head, one after another.  Waves 0-3 hold the
+// state in registers from the first chunk to the last, waves 4-7 bring the next
+// chunk to LDS meanwhile: k and q as f16 rows, k transposed, and the operands
+// of delta_prep_kernel.
+//   SPLIT false: 64 columns per workgroup, each state wave has 16 of them and
+//     works alone (its chain of products and vector work takes 4.2 us a chunk).
+//   SPLIT true: 16 columns per workgroup, the state waves share their rows (of
+//     the state and of the chunk) and hand each other S, X and U through LDS:
+//     a shorter chain, more LDS traffic per column.  For few columns in all.
+template <int DK, bool SPLIT>
+__global__ __launch_bounds__(512) void delta_scan_kernel(DeltaArgs a, const uint8_t *__restrict__ ws) {
+    constexpr int COLS = SPLIT ? 16 : 64;
     constexpr int NT = DK / 16, NQ = DK / 32;
     constexpr int ROWS = CH * DK * 2;                              // bytes of k, of q, of k transposed
     constexpr int FR = 3 * ROWS, VEC = FR + 18 * 1024, BUF = VEC + V_COUNT * CH * 4 + 16;
     __shared__ __align__(16) uint8_t s_buf[2][BUF];
+    // SPLIT: S as right operands (f16 and remainders), X and U tiles, largest
+    // magnitude of each column of S in each wave's rows
+    __shared__ __align__(16) uint8_t s_S[SPLIT ? 2 * NQ * 1024 : 16];
+    __shared__ f32x4_t s_X[SPLIT ? 4 * 64 : 1], s_U[SPLIT ? 4 * 64 : 1];
+    __shared__ float s_max[SPLIT ? 64 : 1];
     const int tid = threadIdx.x, lane = tid & 63, m = lane & 15, g4 = lane >> 4;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     // the workgroups that read the same k and q on one XCD (they are dealt to
     // the 8 XCDs in turn)
-    const int rep = a.hv / a.hk, blocks = a.dv / (16 * COMP), per = rep * blocks;
+    const int rep = a.hv / a.hk, blocks = a.dv / COLS, per = rep * blocks;
     const int group = blockIdx.x / (8 * per) * 8 + blockIdx.x % 8, in = blockIdx.x / 8 % per;
     if (group >= a.n_seq * a.hk) return;
     const int b = group / a.hk, hk = group % a.hk, h = hk * rep + in / blocks;
-    const int col0 = in % blocks * (16 * COMP);
+    const int col0 = in % blocks * COLS;
     int t0, t1;
     seq_rows(a, b, t0, t1);
     const int chunks = (t1 - t0 + CH - 1) / CH;
@@ -515,86 +524,82 @@ __global__ __launch_bounds__(64 * (COMP + PROD)) void delta_scan_kernel(DeltaArg
     // and of row d of k transposed
     auto col_at = [](int d, int at) { return 2 * ROWS + (d * (CH / 8) + (at ^ ((d ^ d >> 3) & 7))) * 16; };
 
-    if (wave >= COMP) {
-    // ---- bringing chunks to LDS: PN threads
-    constexpr int PN = 64 * PROD;
-    const int p = tid - 64 * COMP;
-    constexpr int K_ITEMS = 32 * (DK / 8), Q_ITEMS = CH * (DK / 8), F_ITEMS = 18 * 64, V_ITEMS = V_COUNT * CH + 1;
-    // items: row pairs x 8 of k, rows x 8 of q, 16 bytes of operands, vectors
-    constexpr int KI = (K_ITEMS + PN - 1) / PN, QN = (Q_ITEMS + PN - 1) / PN, FN = (F_ITEMS + PN - 1) / PN,
-                  VN = (V_ITEMS + PN - 1) / PN;
-    u32x4_t k_reg[KI][2], q_reg[QN], f_reg[FN];
-    float v_reg[VN], k_sc[KI][2], q_sc[QN];
-    // byte offsets of the thread's pieces from the chunk's first row (64 rows of
-    // at most 2^22 elements); pieces behind the last take the last one's again
-    uint32_t k_off[KI], q_off[QN];
-    int k_item[KI], q_item[QN];
+    if (wave >= 4) {
+        // ---- bringing chunks to LDS.  Items of a thread: KI pairs of rows x 8
+        // of k, QN rows x 8 of q, FN 16-byte pieces of operands (the last only
+        // for half of the threads), VN floats
+        const int p = tid - 256;
+        constexpr int KI = 32 * (DK / 8) / 256, QN = CH * (DK / 8) / 256, FN = 5, VN = 2;
+        u32x4_t k_reg[KI][2], q_reg[QN], f_reg[FN];
+        float v_reg[VN], k_sc[KI][2], q_sc[QN];
+        // byte offsets from the chunk's first row (64 rows of at most 2^22
+        // elements)
+        uint32_t k_off[KI], q_off[QN];
 #pragma unroll
-    for (int it = 0; it < KI; ++it) {
-        k_item[it] = it * PN + p < K_ITEMS ? it * PN + p : K_ITEMS - 1;
-        k_off[it] = (uint32_t)(2 * (k_item[it] / (DK / 8))) * (uint32_t)a.ldk * 2 + k_item[it] % (DK / 8) * 16;
-    }
+        for (int it = 0; it < KI; ++it) {
+            const int x = it * 256 + p;
+            k_off[it] = (uint32_t)(2 * (x / (DK / 8))) * (uint32_t)a.ldk * 2 + x % (DK / 8) * 16;
+        }
 #pragma unroll
-    for (int it = 0; it < QN; ++it) {
-        q_item[it] = it * PN + p < Q_ITEMS ? it * PN + p : Q_ITEMS - 1;
-        q_off[it] = (uint32_t)(q_item[it] / (DK / 8)) * (uint32_t)a.ldq * 2 + q_item[it] % (DK / 8) * 16;
-    }
-    auto load = [&](int c) {
-        const int64_t r0 = t0 + (int64_t)c * CH;
-        const int len = t1 - r0 < CH ? (int)(t1 - r0) : CH;
-        const uint8_t *unit = units + c * unit_step;
-        const uint8_t *kb = reinterpret_cast<const uint8_t *>(a.k + r0 * a.ldk + hk * DK),
-                      *qb = reinterpret_cast<const uint8_t *>(a.q + r0 * a.ldq + hk * DK);
+        for (int it = 0; it < QN; ++it) {
+            const int x = it * 256 + p;
+            q_off[it] = (uint32_t)(x / (DK / 8)) * (uint32_t)a.ldq * 2 + x % (DK / 8) * 16;
+        }
         const u32x4_t zero = {0, 0, 0, 0};
-#pragma unroll
-        for (int it = 0; it < KI; ++it)
+        auto rows_of = [&](int c) { return t1 - t0 - c * CH < CH ? t1 - t0 - c * CH : CH; };
+        auto load_k = [&](int c, int it) {
+            const int len = rows_of(c);
+            const uint8_t *unit = units + c * unit_step;
+            const uint8_t *kb = reinterpret_cast<const uint8_t *>(a.k + (t0 + (int64_t)c * CH) * a.ldk + hk * DK);
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-                const int row = 2 * (k_item[it] / (DK / 8)) + e;
+                const int row = 2 * ((it * 256 + p) / (DK / 8)) + e;
                 k_sc[it][e] = *reinterpret_cast<const float *>(unit + (uint32_t)(UNIT_VEC + (V_SK * CH + row) * 4));
                 k_reg[it][e] = len == CH || row < len
                                    ? *reinterpret_cast<const u32x4_t *>(kb + (k_off[it] + e * (uint32_t)a.ldk * 2))
                                    : zero;
             }
+        };
+        auto load_q = [&](int c) {
+            const int len = rows_of(c);
+            const uint8_t *unit = units + c * unit_step;
+            const uint8_t *qb = reinterpret_cast<const uint8_t *>(a.q + (t0 + (int64_t)c * CH) * a.ldq + hk * DK);
 #pragma unroll
-        for (int it = 0; it < QN; ++it) {
-            const int row = q_item[it] / (DK / 8);
-            q_sc[it] = *reinterpret_cast<const float *>(unit + (uint32_t)(UNIT_VEC + (V_SQ * CH + row) * 4));
-            q_reg[it] = len == CH || row < len ? *reinterpret_cast<const u32x4_t *>(qb + q_off[it]) : zero;
-        }
+            for (int it = 0; it < QN; ++it) {
+                const int row = (it * 256 + p) / (DK / 8);
+                q_sc[it] = *reinterpret_cast<const float *>(unit + (uint32_t)(UNIT_VEC + (V_SQ * CH + row) * 4));
+                q_reg[it] = len == CH || row < len ? *reinterpret_cast<const u32x4_t *>(qb + q_off[it]) : zero;
+            }
+        };
+        auto load_f = [&](int c) {
+            const uint8_t *unit = units + c * unit_step;
 #pragma unroll
-        for (int it = 0; it < FN; ++it) {
-            const int x = it * PN + p < F_ITEMS ? it * PN + p : F_ITEMS - 1;
-            f_reg[it] = *reinterpret_cast<const u32x4_t *>(unit + (uint32_t)(x * 16));
-        }
+            for (int it = 0; it < FN; ++it)
+                if (it < 4 || p < 128) f_reg[it] = *reinterpret_cast<const u32x4_t *>(unit + (uint32_t)((it * 256 + p) * 16));
 #pragma unroll
-        for (int it = 0; it < VN; ++it) {
-            const int x = it * PN + p < V_ITEMS ? it * PN + p : V_ITEMS - 1;
-            v_reg[it] = *reinterpret_cast<const float *>(unit + (uint32_t)(UNIT_VEC + x * 4));
-        }
-    };
-    // 8 bf16 times f as f16
-    auto halves = [](u32x4_t x, float f) {
-        u32x4_t r;
+            for (int it = 0; it < VN; ++it)
+                if (it * 256 + p <= V_COUNT * CH)
+                    v_reg[it] = *reinterpret_cast<const float *>(unit + (uint32_t)(UNIT_VEC + (it * 256 + p) * 4));
+        };
+        // 8 bf16 times f as f16
+        auto halves = [](u32x4_t x, float f) {
+            u32x4_t r;
 #pragma unroll
-        for (int e = 0; e < 4; ++e)
-            r[e] = f16_pair(__uint_as_float(x[e] << 16) * f, __uint_as_float(x[e] & 0xffff0000u) * f);
-        return r;
-    };
-    // inner order of the products: elements 0-3 of an 8-chunk u of a block of
-    // 32 to chunk 2 (u % 2), 4-7 to the next, half u / 2
-    auto store_row = [&](uint8_t *buf, int which, int row, int at, u32x4_t x) {
-        const int blk = at / 4, u = at % 4;
-        uint8_t *d = buf + (u / 2) * 8;
-        *reinterpret_cast<uint2 *>(d + row_at(which, row, 4 * blk + 2 * (u & 1))) = make_uint2(x[0], x[1]);
-        *reinterpret_cast<uint2 *>(d + row_at(which, row, 4 * blk + 2 * (u & 1) + 1)) = make_uint2(x[2], x[3]);
-    };
-    // (pieces behind the last write the last one's values once more)
-    auto store = [&](int c) {
-        uint8_t *buf = s_buf[c & 1];
-#pragma unroll
-        for (int it = 0; it < KI; ++it) {
-            const int pair = k_item[it] / (DK / 8), at = k_item[it] % (DK / 8);
+            for (int e = 0; e < 4; ++e)
+                r[e] = f16_pair(__uint_as_float(x[e] << 16) * f, __uint_as_float(x[e] & 0xffff0000u) * f);
+            return r;
+        };
+        // inner order of the products: elements 0-3 of an 8-chunk u of a block
+        // of 32 to chunk 2 (u % 2), 4-7 to the next, half u / 2
+        auto store_row = [&](uint8_t *buf, int which, int row, int at, u32x4_t x) {
+            const int blk = at / 4, u = at % 4;
+            uint8_t *d = buf + (u / 2) * 8;
+            *reinterpret_cast<uint2 *>(d + row_at(which, row, 4 * blk + 2 * (u & 1))) = make_uint2(x[0], x[1]);
+            *reinterpret_cast<uint2 *>(d + row_at(which, row, 4 * blk + 2 * (u & 1) + 1)) = make_uint2(x[2], x[3]);
+        };
+        auto store_k = [&](int c, int it) {
+            uint8_t *buf = s_buf[c & 1];
+            const int x = it * 256 + p, pair = x / (DK / 8), at = x % (DK / 8);
             const u32x4_t r0 = halves(k_reg[it][0], k_sc[it][0]), r1 = halves(k_reg[it][1], k_sc[it][1]);
             store_row(buf, 0, 2 * pair, at, r0);
             store_row(buf, 0, 2 * pair + 1, at, r1);
@@ -604,33 +609,57 @@ __global__ __launch_bounds__(64 * (COMP + PROD)) void delta_scan_kernel(DeltaArg
                 const uint32_t two = __builtin_amdgcn_perm(r1[e / 2], r0[e / 2], e & 1 ? 0x07060302u : 0x05040100u);
                 *reinterpret_cast<uint32_t *>(buf + col_at(8 * at + e, slot) + in8 * 2) = two;
             }
-        }
+        };
+        auto store_q = [&](int c) {
+            uint8_t *buf = s_buf[c & 1];
 #pragma unroll
-        for (int it = 0; it < QN; ++it)
-            store_row(buf, 1, q_item[it] / (DK / 8), q_item[it] % (DK / 8), halves(q_reg[it], q_sc[it]));
+            for (int it = 0; it < QN; ++it) {
+                const int x = it * 256 + p;
+                store_row(buf, 1, x / (DK / 8), x % (DK / 8), halves(q_reg[it], q_sc[it]));
+            }
+        };
+        auto store_f = [&](int c) {
+            uint8_t *buf = s_buf[c & 1];
 #pragma unroll
-        for (int it = 0; it < FN; ++it) {
-            const int x = it * PN + p < F_ITEMS ? it * PN + p : F_ITEMS - 1;
-            *reinterpret_cast<u32x4_t *>(buf + FR + x * 16) = f_reg[it];
-        }
+            for (int it = 0; it < FN; ++it)
+                if (it < 4 || p < 128) *reinterpret_cast<u32x4_t *>(buf + FR + (it * 256 + p) * 16) = f_reg[it];
 #pragma unroll
-        for (int it = 0; it < VN; ++it) {
-            const int x = it * PN + p < V_ITEMS ? it * PN + p : V_ITEMS - 1;
-            *reinterpret_cast<float *>(buf + VEC + x * 4) = v_reg[it];
-        }
-    };
+            for (int it = 0; it < VN; ++it)
+                if (it * 256 + p <= V_COUNT * CH) *reinterpret_cast<float *>(buf + VEC + (it * 256 + p) * 4) = v_reg[it];
+        };
+        // chunk c to LDS, and the loads of the one after it, in the four parts
+        // between the state waves' barriers (one part when they have one)
+        auto part = [&](int c, int i) {
+            if (c >= chunks) return;
+            const bool more = c + 1 < chunks;
+            if (i < KI) {
+                store_k(c, i);
+                if (more) load_k(c + 1, i);
+            }
+            if (i == 2) {
+                store_q(c);
+                if (more) load_q(c + 1);
+            }
+            if (i == 3) {
+                store_f(c);
+                if (more) load_f(c + 1);
+            }
+        };
         if (chunks > 0) {
-            load(0);
-            store(0);
-            if (chunks > 1) load(1);
+#pragma unroll
+            for (int it = 0; it < KI; ++it) load_k(0, it);
+            load_q(0);
+            load_f(0);
         }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) part(0, i);
         lds_barrier();
         for (int c = 0; c < chunks; ++c) {
-            if (c + 1 < chunks) {
-                store(c + 1);
-                if (c + 2 < chunks) load(c + 2);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                part(c + 1, i);
+                if (SPLIT || i == 3) lds_barrier();
             }
-            lds_barrier();
         }
         return;
     }
@@ -638,247 +667,411 @@ __global__ __launch_bounds__(64 * (COMP + PROD)) void delta_scan_kernel(DeltaArg
     // ---- the state's waves
     const int slot = a.state_idx ? a.state_idx[b] : b;
     const bool kept = slot >= 0 && slot < a.n_states;
-    const int col = col0 + 16 * wave + m;
-    const int64_t soff = ((int64_t)(kept ? slot : 0) * a.hv + h) * DK * a.dv + col;
-    f32x4_t S[NT];
-#pragma unroll
-    for (int t = 0; t < NT; ++t)
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-            S[t][e] = kept && a.s_in ? a.s_in[soff + (int64_t)(16 * t + 4 * g4 + e) * a.dv] : 0.f;
-    // rows 16 t + 4 g4 + e of v and o: a uniform base and the lane's offset
-    uint16_t v_next[16];
-    const uint32_t v_lane = ((uint32_t)(4 * g4) * (uint32_t)a.ldv + m) * 2;
-    const uint32_t o_lane = ((uint32_t)(4 * g4) * (uint32_t)a.ldo + m) * 2;
-    const int64_t head_col = (int64_t)h * a.dv + col0 + 16 * wave;
-    auto load_v = [&](int c) {
-        const int64_t r0 = t0 + (int64_t)c * CH;
-        const int len = t1 - r0 < CH ? (int)(t1 - r0) : CH;
-        const uint16_t *base = a.v + r0 * a.ldv + head_col;
-        if (len == CH) {
-#pragma unroll
-            for (int x = 0; x < 16; ++x)
-                v_next[x] = *reinterpret_cast<const uint16_t *>(
-                    reinterpret_cast<const uint8_t *>(base + (int64_t)(16 * (x / 4) + x % 4) * a.ldv) + v_lane);
-        } else {
-#pragma unroll
-            for (int x = 0; x < 16; ++x) {
-                const int row = 16 * (x / 4) + 4 * g4 + x % 4;
-                v_next[x] = base[(int64_t)(row < len ? row : len - 1) * a.ldv + m];
-            }
-        }
-    };
-    if (chunks > 0) load_v(0);
     const f32x4_t zero4 = {0.f, 0.f, 0.f, 0.f};
-    lds_barrier();
-    for (int c = 0; c < chunks; ++c) {
-        const uint8_t *buf = s_buf[c & 1];
-        auto frag = [&](int at) { return *reinterpret_cast<const u32x4_t *>(buf + at); };
-        auto vec4 = [&](int which, int t) {
-            return *reinterpret_cast<const f32x4_t *>(buf + VEC + (which * CH + 16 * t + 4 * g4) * 4);
+    if constexpr (SPLIT) {
+        constexpr int NTW = NT / 4;  // row tiles of the state per wave
+        const int w = wave, col = col0 + m;
+        const int64_t soff = ((int64_t)(kept ? slot : 0) * a.hv + h) * DK * a.dv + col;
+        f32x4_t S[NTW];
+        auto publish_max = [&] {
+            float mx = 0.f;
+#pragma unroll
+            for (int i = 0; i < NTW; ++i) mx = max_abs(S[i], mx);
+            mx = groups_max(mx);
+            if (g4 == 0) s_max[16 * w + m] = mx;
         };
-        float v[16];
 #pragma unroll
-        for (int x = 0; x < 16; ++x) v[x] = bf16_to_f32(v_next[x]);
-        load_v(c + 1 < chunks ? c + 1 : c);
-        const float gamma = *reinterpret_cast<const float *>(buf + VEC + V_COUNT * CH * 4);
+        for (int i = 0; i < NTW; ++i)
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                S[i][e] = kept && a.s_in ? a.s_in[soff + (int64_t)(16 * (NTW * w + i) + 4 * g4 + e) * a.dv] : 0.f;
+        publish_max();
+        const int64_t head_col = (int64_t)h * a.dv + col;
+        uint16_t v_next[4];
+        auto load_v = [&](int c) {
+            const int64_t r0 = t0 + (int64_t)c * CH;
+            const int len = t1 - r0 < CH ? (int)(t1 - r0) : CH;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const int row = 16 * w + 4 * g4 + e;
+                v_next[e] = a.v[(r0 + (row < len ? row : len - 1)) * a.ldv + head_col];
+            }
+        };
+        if (chunks > 0) load_v(0);
+        const int last_x = w / 2;  // inner blocks of 32 tokens up to this wave's own
+        lds_barrier();
+        for (int c = 0; c < chunks; ++c) {
+            const uint8_t *buf = s_buf[c & 1];
+            auto frag = [&](int at) { return *reinterpret_cast<const u32x4_t *>(buf + at); };
+            auto vec4 = [&](int which, int t) {
+                return *reinterpret_cast<const f32x4_t *>(buf + VEC + (which * CH + 16 * t + 4 * g4) * 4);
+            };
+            const int op0 = FR + (w < 2 ? w : 2 * w - 2) * 1024 + lane * 16;
+            // S as right operand, each wave its rows; and what this wave needs
+            // of the chunk
+            float mx = s_max[m];
+#pragma unroll
+            for (int i = 1; i < 4; ++i) mx = fmaxf(mx, s_max[16 * i + m]);
+            u32x4_t fk[NQ], fq[NQ];
+#pragma unroll
+            for (int q = 0; q < NQ; ++q) {
+                fk[q] = frag(row_at(0, 16 * w + m, 4 * q + g4));
+                fq[q] = frag(row_at(1, 16 * w + m, 4 * q + g4));
+            }
+            const f32x4_t fa = vec4(V_A, w), ft = vec4(V_T, w), fb = vec4(V_B, w), fp = vec4(V_P, w);
+            const float gamma = *reinterpret_cast<const float *>(buf + VEC + V_COUNT * CH * 4);
+            const RowScale ss = unit_scale(mx);
+            const float s_off = exp2i(-ss.s);
+#pragma unroll
+            for (int i = 0; i < NTW; ++i) {
+                const int t = NTW * w + i;
+                u32x4_t f, r;
+                split(S[i], ss.sc, f, r, 0);
+                uint8_t *d = s_S + (t / 2) * 1024 + lane * 16 + (t & 1) * 8;
+                *reinterpret_cast<uint2 *>(d) = make_uint2(f[0], f[1]);
+                *reinterpret_cast<uint2 *>(d + NQ * 1024) = make_uint2(r[0], r[1]);
+            }
+            float v[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) v[e] = bf16_to_f32(v_next[e]);
+            load_v(c + 1 < chunks ? c + 1 : c);
+            lds_barrier();
+            // K S and Q S of the wave's tokens, X = V - diag(e^G) K S
+            u32x4_t sh[NQ], sl[NQ];
+#pragma unroll
+            for (int q = 0; q < NQ; ++q) {
+                sh[q] = *reinterpret_cast<const u32x4_t *>(s_S + q * 1024 + lane * 16);
+                sl[q] = *reinterpret_cast<const u32x4_t *>(s_S + (NQ + q) * 1024 + lane * 16);
+            }
+            f32x4_t kh = zero4, kl = zero4, QS = zero4;
+#pragma unroll
+            for (int q = 0; q < NQ; ++q) {
+                kh = mfma_f16(fk[q], sh[q], kh);
+                kl = mfma_f16(fk[q], sl[q], kl);
+                QS = mfma_f16(fq[q], sh[q], QS);
+            }
+            f32x4_t X[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) X[0][e] = fmaf(-(kh[e] + kl[e]), fa[e] * s_off, v[e]);
+            s_X[64 * w + lane] = X[0];
+            u32x4_t th[2], tl[2], tp[2];
+#pragma unroll
+            for (int x = 0; x < 2; ++x)
+                if (x <= last_x) {
+                    th[x] = frag(op0 + x * 1024);
+                    tl[x] = frag(op0 + (6 + x) * 1024);
+                    tp[x] = frag(op0 + (12 + x) * 1024);
+                }
+            lds_barrier();
+            // U = T' X of the wave's tokens
+#pragma unroll
+            for (int t = 0; t < 4; ++t)
+                if (t / 2 <= last_x) X[t] = s_X[64 * t + lane];
+            mx = 0.f;
+#pragma unroll
+            for (int t = 0; t < 4; ++t)
+                if (t / 2 <= last_x) mx = max_abs(X[t], mx);
+            const RowScale xs = unit_scale(groups_max(mx));
+            const float x_off = exp2i(-xs.s);
+            f32x4_t uh = zero4, ul = zero4, um = zero4;
+#pragma unroll
+            for (int x = 0; x < 2; ++x)
+                if (x <= last_x) {
+                    u32x4_t xh, xl;
+                    split(X[2 * x], xs.sc, xh, xl, 0);
+                    split(X[2 * x + 1], xs.sc, xh, xl, 1);
+                    um = mfma_f16(tl[x], xh, um);
+                    ul = mfma_f16(th[x], xl, ul);
+                    uh = mfma_f16(th[x], xh, uh);
+                }
+            f32x4_t U[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) U[0][e] = (uh[e] + (ul[e] + um[e])) * (ft[e] * x_off);
+            s_U[64 * w + lane] = U[0];
+            u32x4_t kt[NTW][2];
+#pragma unroll
+            for (int i = 0; i < NTW; ++i)
+#pragma unroll
+                for (int x = 0; x < 2; ++x) kt[i][x] = frag(col_at(16 * (NTW * w + i) + m, 4 * x + g4));
+            f32x4_t fc[4];
+#pragma unroll
+            for (int t = 0; t < 4; ++t) fc[t] = vec4(V_C, t);
+            lds_barrier();
+            // S = e^{G_63} S + K^T diag(c) U, each wave its rows
+            f32x4_t W[4];
+            mx = 0.f;
+            float mw = 0.f;
+#pragma unroll
+            for (int t = 0; t < 4; ++t) {
+                U[t] = s_U[64 * t + lane];
+                W[t] = U[t] * fc[t];
+                mw = max_abs(W[t], mw);
+                if (t / 2 <= last_x) mx = max_abs(U[t], mx);
+            }
+            const RowScale wsc = unit_scale(groups_max(mw));
+            const float w_off = exp2i(-wsc.s);
+            f32x4_t dh[NTW], dl[NTW];
+#pragma unroll
+            for (int i = 0; i < NTW; ++i) dh[i] = dl[i] = zero4;
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+                u32x4_t wh, wl;
+                split(W[2 * x], wsc.sc, wh, wl, 0);
+                split(W[2 * x + 1], wsc.sc, wh, wl, 1);
+#pragma unroll
+                for (int i = 0; i < NTW; ++i) {
+                    dh[i] = mfma_f16(kt[i][x], wh, dh[i]);
+                    dl[i] = mfma_f16(kt[i][x], wl, dl[i]);
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < NTW; ++i)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) S[i][e] = fmaf(dh[i][e] + dl[i][e], w_off, gamma * S[i][e]);
+            publish_max();
+            // O = diag(b) Q S + P U of the wave's tokens
+            const RowScale us = unit_scale(groups_max(mx));
+            const float u_off = exp2i(-us.s);
+            f32x4_t o = zero4;
+#pragma unroll
+            for (int x = 0; x < 2; ++x)
+                if (x <= last_x) {
+                    u32x4_t f;
+#pragma unroll
+                    for (int t = 0; t < 2; ++t) {
+                        const f32x4_t u = U[2 * x + t];
+                        f[2 * t] = f16_pair(u[0] * us.sc, u[1] * us.sc);
+                        f[2 * t + 1] = f16_pair(u[2] * us.sc, u[3] * us.sc);
+                    }
+                    o = mfma_f16(tp[x], f, o);
+                }
+            const int64_t r0 = t0 + (int64_t)c * CH;
+            const int len = t1 - r0 < CH ? (int)(t1 - r0) : CH;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const int row = 16 * w + 4 * g4 + e;
+                const float z = fmaf(QS[e], fb[e] * s_off, o[e] * (fp[e] * u_off));
+                if (row < len) *reinterpret_cast<__bf16 *>(a.o + (r0 + row) * a.ldo + head_col) = (__bf16)z;
+            }
+            lds_barrier();
+        }
+        if (kept && a.s_out && !(chunks == 0 && a.s_in == a.s_out)) {
+#pragma unroll
+            for (int i = 0; i < NTW; ++i)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) a.s_out[soff + (int64_t)(16 * (NTW * w + i) + 4 * g4 + e) * a.dv] = S[i][e];
+        }
+    } else {
+        const int col = col0 + 16 * wave + m;
+        const int64_t soff = ((int64_t)(kept ? slot : 0) * a.hv + h) * DK * a.dv + col;
+        f32x4_t S[NT];
+#pragma unroll
+        for (int t = 0; t < NT; ++t)
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                S[t][e] = kept && a.s_in ? a.s_in[soff + (int64_t)(16 * t + 4 * g4 + e) * a.dv] : 0.f;
+        // rows 16 t + 4 g4 + e of v and o: a uniform base and the lane's offset
+        uint16_t v_next[16];
+        const uint32_t v_lane = ((uint32_t)(4 * g4) * (uint32_t)a.ldv + m) * 2;
+        const uint32_t o_lane = ((uint32_t)(4 * g4) * (uint32_t)a.ldo + m) * 2;
+        const int64_t head_col = (int64_t)h * a.dv + col0 + 16 * wave;
+        auto load_v = [&](int c) {
+            const int64_t r0 = t0 + (int64_t)c * CH;
+            const int len = t1 - r0 < CH ? (int)(t1 - r0) : CH;
+            const uint16_t *base = a.v + r0 * a.ldv + head_col;
+            if (len == CH) {
+#pragma unroll
+                for (int x = 0; x < 16; ++x)
+                    v_next[x] = *reinterpret_cast<const uint16_t *>(
+                        reinterpret_cast<const uint8_t *>(base + (int64_t)(16 * (x / 4) + x % 4) * a.ldv) + v_lane);
+            } else {
+#pragma unroll
+                for (int x = 0; x < 16; ++x) {
+                    const int row = 16 * (x / 4) + 4 * g4 + x % 4;
+                    v_next[x] = base[(int64_t)(row < len ? row : len - 1) * a.ldv + m];
+                }
+            }
+        };
+        if (chunks > 0) load_v(0);
+        lds_barrier();
+        for (int c = 0; c < chunks; ++c) {
+            const uint8_t *buf = s_buf[c & 1];
+            auto frag = [&](int at) { return *reinterpret_cast<const u32x4_t *>(buf + at); };
+            auto vec4 = [&](int which, int t) {
+                return *reinterpret_cast<const f32x4_t *>(buf + VEC + (which * CH + 16 * t + 4 * g4) * 4);
+            };
+            float v[16];
+#pragma unroll
+            for (int x = 0; x < 16; ++x) v[x] = bf16_to_f32(v_next[x]);
+            load_v(c + 1 < chunks ? c + 1 : c);
+            const float gamma = *reinterpret_cast<const float *>(buf + VEC + V_COUNT * CH * 4);
 
-        // Operands are read a phase ahead of their products where registers
-        // allow (one wave per SIMD has 512): a phase is short against an LDS
-        // read.
-        constexpr bool AHEAD_K = COMP == 1, AHEAD = COMP == 1;
-        auto k_frag = [&](int t, int q) { return frag(row_at(0, 16 * t + m, 4 * q + g4)); };
-        auto q_frag = [&](int t, int q) { return frag(row_at(1, 16 * t + m, 4 * q + g4)); };
-        auto kt_frag = [&](int t, int x) { return frag(col_at(16 * t + m, 4 * x + g4)); };
-        auto op_frag = [&](int which, int t, int x) { return frag(FR + (6 * which + frag_index(t, x)) * 1024 + lane * 16); };
-        u32x4_t ak[AHEAD_K ? NQ : 1][4], aq[AHEAD ? NQ : 1][4], at_[AHEAD ? 18 : 1], akt[AHEAD ? NT : 1][2];
-        if (AHEAD_K) {
+            auto k_frag = [&](int t, int q) { return frag(row_at(0, 16 * t + m, 4 * q + g4)); };
+            auto q_frag = [&](int t, int q) { return frag(row_at(1, 16 * t + m, 4 * q + g4)); };
+            auto kt_frag = [&](int t, int x) { return frag(col_at(16 * t + m, 4 * x + g4)); };
+            auto op = [&](int which, int t, int x) { return frag(FR + (6 * which + frag_index(t, x)) * 1024 + lane * 16); };
+            // the state as right operand
+            u32x4_t sh[NQ], sl[NQ];
+            float mx = 0.f;
+#pragma unroll
+            for (int t = 0; t < NT; ++t) mx = max_abs(S[t], mx);
+            const RowScale ss = unit_scale(groups_max(mx));
+            const float s_off = exp2i(-ss.s);
+#pragma unroll
+            for (int t = 0; t < NT; ++t) split(S[t], ss.sc, sh[t / 2], sl[t / 2], t & 1);
+            // K S, X = V - diag(e^G) K S (the remainders' products go into the same
+            // sums).  Here and below the inner index is the outer loop, so that
+            // products into one sum are four or more apart: one after another they
+            // wait for each other's result.
+            f32x4_t QS[4], X[4];
+#pragma unroll
+            for (int t = 0; t < 4; ++t) X[t] = QS[t] = zero4;
+#pragma unroll
+            for (int q = 0; q < NQ; ++q) {
+                u32x4_t fk[4];
+#pragma unroll
+                for (int t = 0; t < 4; ++t) fk[t] = k_frag(t, q);
+#pragma unroll
+                for (int t = 0; t < 4; ++t) X[t] = mfma_f16(fk[t], sl[q], X[t]);
+#pragma unroll
+                for (int t = 0; t < 4; ++t) X[t] = mfma_f16(fk[t], sh[q], X[t]);
+            }
+            mx = 0.f;
+#pragma unroll
+            for (int t = 0; t < 4; ++t) {
+                const f32x4_t fa = vec4(V_A, t);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) X[t][e] = fmaf(-X[t][e], fa[e] * s_off, v[4 * t + e]);
+                mx = max_abs(X[t], mx);
+            }
+            // U = T' X (in units of 2^-xs.s), W = diag(c) U
+            const RowScale xs = unit_scale(groups_max(mx));
+            const float x_off = exp2i(-xs.s);
+            u32x4_t xh[2], xl[2];
+#pragma unroll
+            for (int t = 0; t < 4; ++t) split(X[t], xs.sc, xh[t / 2], xl[t / 2], t & 1);
 #pragma unroll
             for (int q = 0; q < NQ; ++q)
 #pragma unroll
-                for (int t = 0; t < 4; ++t) ak[q][t] = k_frag(t, q);
-            __builtin_amdgcn_sched_barrier(0);
-        }
-        // the state as right operand
-        u32x4_t sh[NQ], sl[NQ];
-        float mx = 0.f;
+                for (int t = 0; t < 4; ++t) QS[t] = mfma_f16(q_frag(t, q), sh[q], QS[t]);
+            f32x4_t U[4], W[4];
 #pragma unroll
-        for (int t = 0; t < NT; ++t) mx = max_abs(S[t], mx);
-        const RowScale ss = unit_scale(groups_max(mx));
-        const float s_off = exp2i(-ss.s);
+            for (int t = 0; t < 4; ++t) U[t] = zero4;
 #pragma unroll
-        for (int t = 0; t < NT; ++t) split(S[t], ss.sc, sh[t / 2], sl[t / 2], t & 1);
-        // K S, X = V - diag(e^G) K S (the remainders' products go into the same
-        // sums).  Here and below the inner index is the outer loop, so that
-        // products into one sum are four or more apart: one after another they
-        // wait for each other's result.
-        f32x4_t QS[4], X[4];
+            for (int x = 0; x < 2; ++x) {
 #pragma unroll
-        for (int t = 0; t < 4; ++t) X[t] = QS[t] = zero4;
-        if (AHEAD) {
-            __builtin_amdgcn_sched_barrier(0);
+                for (int t = 2 * x; t < 4; ++t)
+                    U[t] = mfma_f16(op(1, t, x), xh[x], U[t]);
 #pragma unroll
-            for (int x = 0; x < 12; ++x) at_[x] = frag(FR + x * 1024 + lane * 16);
+                for (int t = 2 * x; t < 4; ++t) U[t] = mfma_f16(op(0, t, x), xl[x], U[t]);
 #pragma unroll
-            for (int q = 0; q < NQ; ++q)
+                for (int t = 2 * x; t < 4; ++t) U[t] = mfma_f16(op(0, t, x), xh[x], U[t]);
+            }
+            mx = 0.f;
+            float mw = 0.f;
 #pragma unroll
-                for (int t = 0; t < 4; ++t) aq[q][t] = q_frag(t, q);
-            __builtin_amdgcn_sched_barrier(0);
-        }
+            for (int t = 0; t < 4; ++t) {
+                const f32x4_t ft = vec4(V_T, t), fc = vec4(V_C, t);
 #pragma unroll
-        for (int q = 0; q < NQ; ++q) {
-            u32x4_t fk[4];
+                for (int e = 0; e < 4; ++e) {
+                    U[t][e] *= ft[e];
+                    W[t][e] = U[t][e] * fc[e];
+                }
+                mx = max_abs(U[t], mx);
+                mw = max_abs(W[t], mw);
+            }
+            // S = e^{G_63} S + K^T W first: the next chunk waits for it
+            const RowScale wsc = unit_scale(groups_max(mw));
+            const float w_off = exp2i(-wsc.s) * x_off;
+            u32x4_t wh[2], wl[2];
 #pragma unroll
-            for (int t = 0; t < 4; ++t) fk[t] = AHEAD_K ? ak[AHEAD_K ? q : 0][t] : k_frag(t, q);
+            for (int t = 0; t < 4; ++t) split(W[t], wsc.sc, wh[t / 2], wl[t / 2], t & 1);
+            f32x4_t D[NT];
 #pragma unroll
-            for (int t = 0; t < 4; ++t) X[t] = mfma_f16(fk[t], sl[q], X[t]);
+            for (int t = 0; t < NT; ++t) D[t] = zero4;
 #pragma unroll
-            for (int t = 0; t < 4; ++t) X[t] = mfma_f16(fk[t], sh[q], X[t]);
-        }
-        mx = 0.f;
+            for (int x = 0; x < 2; ++x)
 #pragma unroll
-        for (int t = 0; t < 4; ++t) {
-            const f32x4_t fa = vec4(V_A, t);
+                for (int t4 = 0; t4 < NT; t4 += 4) {
+                    u32x4_t fk[4];
 #pragma unroll
-            for (int e = 0; e < 4; ++e) X[t][e] = fmaf(-X[t][e], fa[e] * s_off, v[4 * t + e]);
-            mx = max_abs(X[t], mx);
-        }
-        // U = T' X (in units of 2^-xs.s), W = diag(c) U
-        const RowScale xs = unit_scale(groups_max(mx));
-        const float x_off = exp2i(-xs.s);
-        u32x4_t xh[2], xl[2];
+                    for (int t = 0; t < 4; ++t) fk[t] = kt_frag(t4 + t, x);
 #pragma unroll
-        for (int t = 0; t < 4; ++t) split(X[t], xs.sc, xh[t / 2], xl[t / 2], t & 1);
+                    for (int t = 0; t < 4; ++t) D[t4 + t] = mfma_f16(fk[t], wl[x], D[t4 + t]);
 #pragma unroll
-        for (int q = 0; q < NQ; ++q)
-#pragma unroll
-            for (int t = 0; t < 4; ++t) QS[t] = mfma_f16(AHEAD ? aq[AHEAD ? q : 0][t] : q_frag(t, q), sh[q], QS[t]);
-        f32x4_t U[4], W[4];
-#pragma unroll
-        for (int t = 0; t < 4; ++t) U[t] = zero4;
-        if (AHEAD) {
-            __builtin_amdgcn_sched_barrier(0);
+                    for (int t = 0; t < 4; ++t) D[t4 + t] = mfma_f16(fk[t], wh[x], D[t4 + t]);
+                }
 #pragma unroll
             for (int t = 0; t < NT; ++t)
 #pragma unroll
-                for (int x = 0; x < 2; ++x) akt[t][x] = kt_frag(t, x);
+                for (int e = 0; e < 4; ++e) S[t][e] = fmaf(D[t][e], w_off, gamma * S[t][e]);
+            // O = diag(b) Q S + P U
+            const RowScale us = unit_scale(groups_max(mx));
+            const float u_off = exp2i(-us.s) * x_off;
+            u32x4_t uh[2];
 #pragma unroll
-            for (int x = 12; x < 18; ++x) at_[x] = frag(FR + x * 1024 + lane * 16);
-            __builtin_amdgcn_sched_barrier(0);
-        }
-        auto op = [&](int which, int t, int x) { return AHEAD ? at_[AHEAD ? 6 * which + frag_index(t, x) : 0] : op_frag(which, t, x); };
+            for (int t = 0; t < 4; ++t)
 #pragma unroll
-        for (int x = 0; x < 2; ++x) {
+                for (int e = 0; e < 4; e += 2)
+                    uh[t / 2][2 * (t & 1) + e / 2] = f16_pair(U[t][e] * us.sc, U[t][e + 1] * us.sc);
+            f32x4_t O[4];
 #pragma unroll
-            for (int t = 2 * x; t < 4; ++t)
-                U[t] = mfma_f16(op(1, t, x), xh[x], U[t]);
+            for (int t = 0; t < 4; ++t) O[t] = zero4;
 #pragma unroll
-            for (int t = 2 * x; t < 4; ++t) U[t] = mfma_f16(op(0, t, x), xl[x], U[t]);
+            for (int x = 0; x < 2; ++x)
 #pragma unroll
-            for (int t = 2 * x; t < 4; ++t) U[t] = mfma_f16(op(0, t, x), xh[x], U[t]);
-        }
-        mx = 0.f;
-        float mw = 0.f;
+                for (int t = 2 * x; t < 4; ++t)
+                    O[t] = mfma_f16(op(2, t, x), uh[x], O[t]);
 #pragma unroll
-        for (int t = 0; t < 4; ++t) {
-            const f32x4_t ft = vec4(V_T, t), fc = vec4(V_C, t);
+            for (int t = 0; t < 4; ++t) {
+                const f32x4_t fb = vec4(V_B, t), fp = vec4(V_P, t);
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                U[t][e] *= ft[e];
-                W[t][e] = U[t][e] * fc[e];
+                for (int e = 0; e < 4; ++e) O[t][e] = fmaf(QS[t][e], fb[e] * s_off, O[t][e] * (fp[e] * u_off));
             }
-            mx = max_abs(U[t], mx);
-            mw = max_abs(W[t], mw);
-        }
-        // S = e^{G_63} S + K^T W first: the next chunk waits for it
-        const RowScale wsc = unit_scale(groups_max(mw));
-        const float w_off = exp2i(-wsc.s) * x_off;
-        u32x4_t wh[2], wl[2];
+            const int64_t r0 = t0 + (int64_t)c * CH;
+            const int len = t1 - r0 < CH ? (int)(t1 - r0) : CH;
+            uint16_t *ob = a.o + r0 * a.ldo + head_col;
+            if (len == CH) {
 #pragma unroll
-        for (int t = 0; t < 4; ++t) split(W[t], wsc.sc, wh[t / 2], wl[t / 2], t & 1);
-        f32x4_t D[NT];
+                for (int x = 0; x < 16; ++x)
+                    *reinterpret_cast<__bf16 *>(reinterpret_cast<uint8_t *>(ob + (int64_t)(16 * (x / 4) + x % 4) * a.ldo) +
+                                                o_lane) = (__bf16)O[x / 4][x % 4];
+            } else {
 #pragma unroll
-        for (int t = 0; t < NT; ++t) D[t] = zero4;
-#pragma unroll
-        for (int x = 0; x < 2; ++x)
-#pragma unroll
-            for (int t4 = 0; t4 < NT; t4 += 4) {
-                u32x4_t fk[4];
-#pragma unroll
-                for (int t = 0; t < 4; ++t) fk[t] = AHEAD ? akt[AHEAD ? t4 + t : 0][x] : kt_frag(t4 + t, x);
-#pragma unroll
-                for (int t = 0; t < 4; ++t) D[t4 + t] = mfma_f16(fk[t], wl[x], D[t4 + t]);
-#pragma unroll
-                for (int t = 0; t < 4; ++t) D[t4 + t] = mfma_f16(fk[t], wh[x], D[t4 + t]);
+                for (int x = 0; x < 16; ++x) {
+                    const int row = 16 * (x / 4) + 4 * g4 + x % 4;
+                    if (row < len) *reinterpret_cast<__bf16 *>(ob + (int64_t)row * a.ldo + m) = (__bf16)O[x / 4][x % 4];
+                }
             }
-#pragma unroll
-        for (int t = 0; t < NT; ++t)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) S[t][e] = fmaf(D[t][e], w_off, gamma * S[t][e]);
-        // O = diag(b) Q S + P U
-        const RowScale us = unit_scale(groups_max(mx));
-        const float u_off = exp2i(-us.s) * x_off;
-        u32x4_t uh[2];
-#pragma unroll
-        for (int t = 0; t < 4; ++t)
-#pragma unroll
-            for (int e = 0; e < 4; e += 2)
-                uh[t / 2][2 * (t & 1) + e / 2] = f16_pair(U[t][e] * us.sc, U[t][e + 1] * us.sc);
-        f32x4_t O[4];
-#pragma unroll
-        for (int t = 0; t < 4; ++t) O[t] = zero4;
-#pragma unroll
-        for (int x = 0; x < 2; ++x)
-#pragma unroll
-            for (int t = 2 * x; t < 4; ++t)
-                O[t] = mfma_f16(op(2, t, x), uh[x], O[t]);
-#pragma unroll
-        for (int t = 0; t < 4; ++t) {
-            const f32x4_t fb = vec4(V_B, t), fp = vec4(V_P, t);
-#pragma unroll
-            for (int e = 0; e < 4; ++e) O[t][e] = fmaf(QS[t][e], fb[e] * s_off, O[t][e] * (fp[e] * u_off));
+            lds_barrier();
         }
-        const int64_t r0 = t0 + (int64_t)c * CH;
-        const int len = t1 - r0 < CH ? (int)(t1 - r0) : CH;
-        uint16_t *ob = a.o + r0 * a.ldo + head_col;
-        if (len == CH) {
+        if (kept && a.s_out && !(chunks == 0 && a.s_in == a.s_out)) {
 #pragma unroll
-            for (int x = 0; x < 16; ++x)
-                *reinterpret_cast<__bf16 *>(reinterpret_cast<uint8_t *>(ob + (int64_t)(16 * (x / 4) + x % 4) * a.ldo) +
-                                            o_lane) = (__bf16)O[x / 4][x % 4];
-        } else {
+            for (int t = 0; t < NT; ++t)
 #pragma unroll
-            for (int x = 0; x < 16; ++x) {
-                const int row = 16 * (x / 4) + 4 * g4 + x % 4;
-                if (row < len) *reinterpret_cast<__bf16 *>(ob + (int64_t)row * a.ldo + m) = (__bf16)O[x / 4][x % 4];
-            }
+                for (int e = 0; e < 4; ++e) a.s_out[soff + (int64_t)(16 * t + 4 * g4 + e) * a.dv] = S[t][e];
         }
-        lds_barrier();
-    }
-    if (kept && a.s_out && !(chunks == 0 && a.s_in == a.s_out)) {
-#pragma unroll
-        for (int t = 0; t < NT; ++t)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) a.s_out[soff + (int64_t)(16 * t + 4 * g4 + e) * a.dv] = S[t][e];
     }
 }
+
+constexpr int SPLIT_TILES = 512;
 
 template <int DK>
 hipError_t launch_chunks(const DeltaArgs &a, void *ws, hipStream_t s) {
     if (a.T > 0)
         hipLaunchKernelGGL((delta_prep_kernel<DK>), dim3((unsigned)((a.T / CH + a.n_seq) * a.hv)), dim3(256), 0, s, a,
                            static_cast<uint8_t *>(ws));
-    // One column tile of 16 per compute unit: a wave of its own; more: four of
-    // them share what is brought to LDS.
+    // Workgroups of 16 columns while they fill the 256 compute units not much
+    // more than once; else of 64.
     const int64_t tiles = (int64_t)a.n_seq * a.hv * (a.dv / 16);
-    const int comp = tiles > 256 ? 4 : 1;
-    const int64_t groups = (int64_t)a.n_seq * a.hk, per = a.hv / a.hk * (a.dv / (16 * comp));
+    const bool split_rows = tiles <= SPLIT_TILES;
+    const int64_t groups = (int64_t)a.n_seq * a.hk, per = a.hv / a.hk * (a.dv / (split_rows ? 16 : 64));
     const dim3 grid((unsigned)((groups + 7) / 8 * 8 * per));
     const uint8_t *units = static_cast<const uint8_t *>(ws);
-    if (comp == 4)
-        hipLaunchKernelGGL((delta_scan_kernel<DK, 4, 4>), grid, dim3(512), 0, s, a, units);
+    if (split_rows)
+        hipLaunchKernelGGL((delta_scan_kernel<DK, true>), grid, dim3(512), 0, s, a, units);
     else
-        hipLaunchKernelGGL((delta_scan_kernel<DK, 1, 3>), grid, dim3(256), 0, s, a, units);
+        hipLaunchKernelGGL((delta_scan_kernel<DK, false>), grid, dim3(512), 0, s, a, units);
     return hipGetLastError();
 }
 

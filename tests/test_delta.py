@@ -142,6 +142,15 @@ def test_packed(kind, lens):
 
 
 @pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("lens,hk,hv,dk,dv", [([70] * 10, 4, 8, 128, 128), ([65, 3] * 16, 2, 8, 64, 64),
+                                              ([130, 1, 64, 63, 200, 0], 8, 16, 64, 128), ([100] * 9, 8, 16, 128, 64)])
+def test_many_columns(kind, lens, hk, hv, dk, dv):
+    """More state columns than workgroups of 16 of them are used for."""
+    assert len(lens) * hv * dv // 16 > 512
+    run(kind, lens, hk, hv, dk, dv, True, seed=hv)
+
+
+@pytest.mark.parametrize("kind", KINDS)
 @pytest.mark.parametrize("name,change", [
     ("no decay", dict(g=lambda g: g * 0)), ("full decay", dict(g=lambda g: g * 0 - 200)),
     ("infinite decay", dict(g=lambda g: torch.where(g < -0.3, float("-inf"), g))),
