@@ -242,8 +242,8 @@ __global__ __launch_bounds__(256) void delta_prep_kernel(DeltaArgs a, uint8_t *_
     constexpr int KQ = 2 * CH * DK * 2, TB = CH * LDA * 4;
     __shared__ __align__(16) uint8_t s_kq[KQ > TB ? KQ : TB];  // k, q as f16; then T
     __shared__ __align__(16) float s_A[CH * LDA];
-    __shared__ float s_f[2][CH];   // k and q: what takes a row's scale off and normalises it
-    __shared__ float s_sc[2][CH];  // and the scale
+    __shared__ float s_f[2][CH];   // k and q: sums of squares, then row factors
+    __shared__ float s_sc[2][CH];  // and the scales
     __shared__ __align__(16) float s_beta[CH];
     __shared__ double s_G[CH];
     const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6, m = lane & 15, g4 = lane >> 4;
@@ -330,47 +330,63 @@ __global__ __launch_bounds__(256) void delta_prep_kernel(DeltaArgs a, uint8_t *_
                 *reinterpret_cast<uint2 *>(s_kq + place(which, row, at / 8) + at % 8 * 2) = d;
             }
             if (m == 0) {
-                s_f[which][row] = (a.norm ? 1.0f / sqrtf(ss + 1e-6f) : 1.0f) * exp2i(-sc.s) * (which ? a.scale : 1.0f);
+                s_f[which][row] = ss;
                 s_sc[which][row] = sc.sc;
             }
         }
     }
     __syncthreads();
+    if (tid < 2 * CH) {
+        // what takes a row's scale off and normalises it (1 / sc: a power of two)
+        const int which = tid >> 6, row = lane;
+        const float off = __uint_as_float((uint32_t)(254 - (__float_as_uint(s_sc[which][row]) >> 23)) << 23);
+        s_f[which][row] = (a.norm ? off / sqrtf(s_f[which][row] + 1e-6f) : off) * (which ? a.scale : 1.0f);
+    }
+    __syncthreads();
 
-    // k_j.k_i and k_j.q_i, row j = 16 jt + 4 g4 + e, column i = 16 w + m
+    // k_j.k_i and k_j.q_i, row j = 16 jt + 4 g4 + e, column i; wave w takes the
+    // columns 16 w.. of P and 16 (3 - w).. of A, so that each has five tiles
     uint8_t *unit = ws + ((int64_t)id * a.hv + h) * UNIT;
     float *vec = reinterpret_cast<float *>(unit + UNIT_VEC);
     const int i = 16 * w + m;
     f32x4_t P[4];
     {
+        const int wa = 3 - w, ia = 16 * wa + m;
         u32x4_t bk[DK / 32], bq[DK / 32];
 #pragma unroll
         for (int ks = 0; ks < DK / 32; ++ks) {
-            bk[ks] = *reinterpret_cast<const u32x4_t *>(s_kq + place(0, i, 4 * ks + g4));
+            bk[ks] = *reinterpret_cast<const u32x4_t *>(s_kq + place(0, ia, 4 * ks + g4));
             bq[ks] = *reinterpret_cast<const u32x4_t *>(s_kq + place(1, i, 4 * ks + g4));
         }
-        const double Gi = s_G[i];
-        const float fi = s_f[0][i], fqi = s_f[1][i], bi = s_beta[i];
+        const double Gi = s_G[i], Ga = s_G[ia];
+        const float fq = s_f[1][i], fa = s_f[0][ia] * s_beta[ia];
 #pragma unroll
         for (int jt = 0; jt < 4; ++jt) {
             P[jt] = f32x4_t{0.f, 0.f, 0.f, 0.f};
-            if (jt <= w) {
-                f32x4_t kk = {0.f, 0.f, 0.f, 0.f}, kq = {0.f, 0.f, 0.f, 0.f};
+            u32x4_t ak[DK / 32];
 #pragma unroll
-                for (int ks = 0; ks < DK / 32; ++ks) {
-                    const u32x4_t ak = *reinterpret_cast<const u32x4_t *>(s_kq + place(0, 16 * jt + m, 4 * ks + g4));
-                    kk = mfma_f16(ak, bk[ks], kk);
-                    kq = mfma_f16(ak, bq[ks], kq);
-                }
-                f32x4_t A;
+            for (int ks = 0; ks < DK / 32; ++ks)
+                ak[ks] = *reinterpret_cast<const u32x4_t *>(s_kq + place(0, 16 * jt + m, 4 * ks + g4));
+            if (jt <= w) {
+                f32x4_t kq = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                for (int ks = 0; ks < DK / 32; ++ks) kq = mfma_f16(ak[ks], bq[ks], kq);
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
                     const int j = 16 * jt + 4 * g4 + e;
-                    const float d = j <= i ? exp_diff(Gi - s_G[j]) * s_f[0][j] : 0.f;
-                    A[e] = j < i ? kk[e] * fi * d * bi : 0.f;
-                    P[jt][e] = j <= i ? kq[e] * fqi * d : 0.f;
+                    P[jt][e] = j <= i ? kq[e] * fq * (exp_diff(Gi - s_G[j]) * s_f[0][j]) : 0.f;
                 }
-                *reinterpret_cast<f32x4_t *>(&s_A[i * LDA + 16 * jt + 4 * g4]) = A;
+            }
+            if (jt <= wa) {
+                f32x4_t kk = {0.f, 0.f, 0.f, 0.f}, A;
+#pragma unroll
+                for (int ks = 0; ks < DK / 32; ++ks) kk = mfma_f16(ak[ks], bk[ks], kk);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const int j = 16 * jt + 4 * g4 + e;
+                    A[e] = j < ia ? kk[e] * fa * (exp_diff(Ga - s_G[j]) * s_f[0][j]) : 0.f;
+                }
+                *reinterpret_cast<f32x4_t *>(&s_A[ia * LDA + 16 * jt + 4 * g4]) = A;
             }
         }
     }
