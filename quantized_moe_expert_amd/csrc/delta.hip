@@ -234,20 +234,21 @@ __device__ __forceinline__ float exp_diff(double d) {
     return __builtin_amdgcn_exp2f((float)(d * 1.4426950408889634));
 }
 
-// T', P and the row factors of one chunk and head.  Wave w owns row tile w.
-// Bound by latency chains (the 16 x 16 inversions) and the 20 KB it writes.
-template <int DK>
+// T', P and the row factors of one chunk and HP heads of one key head (k and q,
+// and their products, are read and formed once for them).  Bound by the vector
+// work: about 1500 instructions a wave and chunk with one head.
+template <int DK, int HP>
 __global__ __launch_bounds__(256) void delta_prep_kernel(DeltaArgs a, uint8_t *__restrict__ ws) {
     constexpr int LDA = 68, PL = DK / 16;  // elements per lane of a row's 16 lanes
     constexpr int KQ = 2 * CH * DK * 2, TB = CH * LDA * 4;
     __shared__ __align__(16) uint8_t s_kq[KQ > TB ? KQ : TB];  // k, q as f16; then T
     __shared__ __align__(16) float s_A[CH * LDA];
-    __shared__ float s_f[2][CH];   // k and q: sums of squares, then row factors
+    __shared__ __align__(16) float s_f[2][CH];   // k and q: sums of squares, then row factors
     __shared__ float s_sc[2][CH];  // and the scales
-    __shared__ __align__(16) float s_beta[CH];
-    __shared__ double s_G[CH];
+    __shared__ __align__(16) float s_beta[HP][CH];
+    __shared__ double s_G[HP][CH];
     const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6, m = lane & 15, g4 = lane >> 4;
-    const int h = blockIdx.x % a.hv, id = blockIdx.x / a.hv;
+    const int h0 = blockIdx.x % (a.hv / HP) * HP, id = blockIdx.x / (a.hv / HP);
     // the sequence: the last whose first chunk is at most id
     int lo = 0, hi = a.n_seq - 1;
     while (lo < hi) {
@@ -263,13 +264,13 @@ __global__ __launch_bounds__(256) void delta_prep_kernel(DeltaArgs a, uint8_t *_
     if (c < 0 || t0 + (int64_t)c * CH >= t1) return;
     t0 += c * CH;
     const int len = t1 - t0 < CH ? t1 - t0 : CH;
-    const int hk = h / (a.hv / a.hk);
+    const int hk = h0 / (a.hv / a.hk);
 
     // rows of k and q to f16: every load first (rows behind the last read the
     // last one's and are cleared)
     constexpr int MASK = DK / 8 - 1;
     auto place = [](int which, int row, int chunk) { return ((which * CH + row) * (DK / 8) + (chunk ^ (row & MASK))) * 16; };
-    const int64_t gate_at = (int64_t)(t0 + (lane < len ? lane : len - 1)) * a.hv + h;
+    const int64_t gate_at = (int64_t)(t0 + (lane < len ? lane : len - 1)) * a.hv + h0 + (w < HP ? w : 0);
     const float g_raw = a.g[gate_at], beta_raw = a.beta[gate_at];
     uint2 raw[2][4][PL / 4];
 #pragma unroll
@@ -287,14 +288,14 @@ __global__ __launch_bounds__(256) void delta_prep_kernel(DeltaArgs a, uint8_t *_
     {
         const float gl = lane < len ? g_raw : 0.f;
         double G = gl < -1000.f ? -1000.0 : (double)gl;  // e^-1000 is 0 too, and -inf - -inf is not
-        if (w == 0) {
+        if (w < HP) {  // wave w: head h0 + w
 #pragma unroll
             for (int o = 1; o < 64; o <<= 1) {
                 const double up = __shfl_up(G, o);
                 if (lane >= o) G += up;
             }
-            s_G[lane] = G;
-            s_beta[lane] = lane < len ? beta_raw : 0.f;
+            s_G[w][lane] = G;
+            s_beta[w][lane] = lane < len ? beta_raw : 0.f;
         }
     }
 #pragma unroll
@@ -346,156 +347,170 @@ __global__ __launch_bounds__(256) void delta_prep_kernel(DeltaArgs a, uint8_t *_
 
     // k_j.k_i and k_j.q_i, row j = 16 jt + 4 g4 + e, column i; wave w takes the
     // columns 16 w.. of P and 16 (3 - w).. of A, so that each has five tiles
-    uint8_t *unit = ws + ((int64_t)id * a.hv + h) * UNIT;
-    float *vec = reinterpret_cast<float *>(unit + UNIT_VEC);
-    const int i = 16 * w + m;
-    f32x4_t P[4];
+    const int i = 16 * w + m, wa = 3 - w, ia = 16 * wa + m;
+    f32x4_t kk[4], kq[4];
     {
-        const int wa = 3 - w, ia = 16 * wa + m;
         u32x4_t bk[DK / 32], bq[DK / 32];
 #pragma unroll
         for (int ks = 0; ks < DK / 32; ++ks) {
             bk[ks] = *reinterpret_cast<const u32x4_t *>(s_kq + place(0, ia, 4 * ks + g4));
             bq[ks] = *reinterpret_cast<const u32x4_t *>(s_kq + place(1, i, 4 * ks + g4));
         }
-        const double Gi = s_G[i], Ga = s_G[ia];
-        const float fq = s_f[1][i], fa = s_f[0][ia] * s_beta[ia];
 #pragma unroll
         for (int jt = 0; jt < 4; ++jt) {
-            P[jt] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+            kk[jt] = kq[jt] = f32x4_t{0.f, 0.f, 0.f, 0.f};
             u32x4_t ak[DK / 32];
 #pragma unroll
             for (int ks = 0; ks < DK / 32; ++ks)
                 ak[ks] = *reinterpret_cast<const u32x4_t *>(s_kq + place(0, 16 * jt + m, 4 * ks + g4));
-            if (jt <= w) {
-                f32x4_t kq = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-                for (int ks = 0; ks < DK / 32; ++ks) kq = mfma_f16(ak[ks], bq[ks], kq);
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const int j = 16 * jt + 4 * g4 + e;
-                    P[jt][e] = j <= i ? kq[e] * fq * (exp_diff(Gi - s_G[j]) * s_f[0][j]) : 0.f;
-                }
+            for (int ks = 0; ks < DK / 32; ++ks) {
+                if (jt <= w) kq[jt] = mfma_f16(ak[ks], bq[ks], kq[jt]);
+                if (jt <= wa) kk[jt] = mfma_f16(ak[ks], bk[ks], kk[jt]);
             }
-            if (jt <= wa) {
-                f32x4_t kk = {0.f, 0.f, 0.f, 0.f}, A;
-#pragma unroll
-                for (int ks = 0; ks < DK / 32; ++ks) kk = mfma_f16(ak[ks], bk[ks], kk);
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const int j = 16 * jt + 4 * g4 + e;
-                    A[e] = j < ia ? kk[e] * fa * (exp_diff(Ga - s_G[j]) * s_f[0][j]) : 0.f;
-                }
-                *reinterpret_cast<f32x4_t *>(&s_A[ia * LDA + 16 * jt + 4 * g4]) = A;
-            }
+            const f32x4_t f = *reinterpret_cast<const f32x4_t *>(&s_f[0][16 * jt + 4 * g4]);
+            kq[jt] *= f * s_f[1][i];
+            kk[jt] *= f * s_f[0][ia];
         }
     }
-    {
-        float mx = 0.f;
+#pragma unroll 1
+    for (int hh = 0; hh < HP; ++hh) {
+        uint8_t *unit = ws + ((int64_t)id * a.hv + h0 + hh) * UNIT;
+        float *vec = reinterpret_cast<float *>(unit + UNIT_VEC);
+        const double *sG = s_G[hh];
+        f32x4_t P[4];
+        {
+            const double Gi = sG[i], Ga = sG[ia];
+            const float ba = s_beta[hh][ia];
 #pragma unroll
-        for (int jt = 0; jt < 4; ++jt) mx = max_abs(P[jt], mx);
-        const RowScale sc = unit_scale(groups_max(mx));
-        if (g4 == 0) vec[V_P * CH + i] = exp2i(-sc.s);
+            for (int jt = 0; jt < 4; ++jt) {
+                P[jt] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+                if (jt <= w) {
 #pragma unroll
-        for (int ks = 0; ks < 2; ++ks)
-            if (ks <= w / 2) {
-                u32x4_t f;
-#pragma unroll
-                for (int t = 0; t < 2; ++t) {
-                    const f32x4_t p = P[2 * ks + t];
-                    f[2 * t] = f16_pair(p[0] * sc.sc, p[1] * sc.sc);
-                    f[2 * t + 1] = f16_pair(p[2] * sc.sc, p[3] * sc.sc);
+                    for (int e = 0; e < 4; ++e) {
+                        const int j = 16 * jt + 4 * g4 + e;
+                        P[jt][e] = j <= i ? kq[jt][e] * exp_diff(Gi - sG[j]) : 0.f;
+                    }
                 }
-                *reinterpret_cast<u32x4_t *>(unit + (12 + (w < 2 ? w : 2 * w - 2 + ks)) * 1024 + lane * 16) = f;
+                if (jt <= wa) {
+                    f32x4_t A;
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const int j = 16 * jt + 4 * g4 + e;
+                        A[e] = j < ia ? kk[jt][e] * (ba * exp_diff(Ga - sG[j])) : 0.f;
+                    }
+                    *reinterpret_cast<f32x4_t *>(&s_A[ia * LDA + 16 * jt + 4 * g4]) = A;
+                }
             }
-    }
-    __syncthreads();  // s_A is whole, k and q are used
+        }
+        {
+            float mx = 0.f;
+#pragma unroll
+            for (int jt = 0; jt < 4; ++jt) mx = max_abs(P[jt], mx);
+            const RowScale sc = unit_scale(groups_max(mx));
+            if (g4 == 0) vec[V_P * CH + i] = exp2i(-sc.s);
+#pragma unroll
+            for (int ks = 0; ks < 2; ++ks)
+                if (ks <= w / 2) {
+                    u32x4_t f;
+#pragma unroll
+                    for (int t = 0; t < 2; ++t) {
+                        const f32x4_t p = P[2 * ks + t];
+                        f[2 * t] = f16_pair(p[0] * sc.sc, p[1] * sc.sc);
+                        f[2 * t + 1] = f16_pair(p[2] * sc.sc, p[3] * sc.sc);
+                    }
+                    *reinterpret_cast<u32x4_t *>(unit + (12 + (w < 2 ? w : 2 * w - 2 + ks)) * 1024 + lane * 16) = f;
+                }
+        }
+        __syncthreads();  // s_A is whole, k and q are used up
 
-    // T = (I + A)^-1 by 16 x 16 tiles: the diagonal ones by substitution (a
-    // lane a column), then T_ij = -T_ii sum_k A_ik T_kj, one distance from the
-    // diagonal after another
-    float *T = reinterpret_cast<float *>(s_kq);
-    {
-        float col[16];
+        // T = (I + A)^-1 by 16 x 16 tiles: the diagonal ones by substitution (a
+        // lane a column), then T_ij = -T_ii sum_k A_ik T_kj, one distance from the
+        // diagonal after another
+        float *T = reinterpret_cast<float *>(s_kq);
+        {
+            float col[16];
 #pragma unroll
-        for (int r = 0; r < 16; ++r) {
-            float t = r == m ? 1.f : 0.f;
+            for (int r = 0; r < 16; ++r) {
+                float t = r == m ? 1.f : 0.f;
 #pragma unroll
-            for (int q = 0; q < (r + 3) / 4; ++q) {
-                const f32x4_t A = *reinterpret_cast<const f32x4_t *>(&s_A[(16 * w + r) * LDA + 16 * w + 4 * q]);
+                for (int q = 0; q < (r + 3) / 4; ++q) {
+                    const f32x4_t A = *reinterpret_cast<const f32x4_t *>(&s_A[(16 * w + r) * LDA + 16 * w + 4 * q]);
 #pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    if (4 * q + e < r) t = fmaf(-A[e], col[4 * q + e], t);
+                    for (int e = 0; e < 4; ++e)
+                        if (4 * q + e < r) t = fmaf(-A[e], col[4 * q + e], t);
+                }
+                col[r] = t;
             }
-            col[r] = t;
-        }
-        if (g4 == 0) {
+            if (g4 == 0) {
 #pragma unroll
-            for (int r = 0; r < 16; ++r) T[(16 * w + r) * LDA + 16 * w + m] = col[r];
-        }
-    }
-    __syncthreads();
-#pragma unroll
-    for (int d = 1; d < 4; ++d) {
-        if (w >= d) {
-            const int j = w - d;
-            f32x4_t M = {0.f, 0.f, 0.f, 0.f}, R = {0.f, 0.f, 0.f, 0.f};
-            for (int k = j; k < w; ++k) {
-                const f32x4_t A = *reinterpret_cast<const f32x4_t *>(&s_A[i * LDA + 16 * k + 4 * g4]);
-#pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    M = __builtin_amdgcn_mfma_f32_16x16x4f32(A[e], T[(16 * k + 4 * g4 + e) * LDA + 16 * j + m], M, 0, 0, 0);
+                for (int r = 0; r < 16; ++r) T[(16 * w + r) * LDA + 16 * w + m] = col[r];
             }
-            const f32x4_t D = *reinterpret_cast<const f32x4_t *>(&T[i * LDA + 16 * w + 4 * g4]);
-#pragma unroll
-            for (int e = 0; e < 4; ++e) R = __builtin_amdgcn_mfma_f32_16x16x4f32(-D[e], M[e], R, 0, 0, 0);
-#pragma unroll
-            for (int e = 0; e < 4; ++e) T[(16 * w + 4 * g4 + e) * LDA + 16 * j + m] = R[e];
         }
         __syncthreads();
-    }
-    {
-        f32x4_t t[4];
-        float mx = 0.f;
 #pragma unroll
-        for (int jt = 0; jt < 4; ++jt) {
-            t[jt] = f32x4_t{0.f, 0.f, 0.f, 0.f};
-            if (jt <= w) {
-                const f32x4_t x = *reinterpret_cast<const f32x4_t *>(&T[i * LDA + 16 * jt + 4 * g4]);
-                const f32x4_t be = *reinterpret_cast<const f32x4_t *>(&s_beta[16 * jt + 4 * g4]);
+        for (int d = 1; d < 4; ++d) {
+            if (w >= d) {
+                const int j = w - d;
+                f32x4_t M = {0.f, 0.f, 0.f, 0.f}, R = {0.f, 0.f, 0.f, 0.f};
+                for (int k = j; k < w; ++k) {
+                    const f32x4_t A = *reinterpret_cast<const f32x4_t *>(&s_A[i * LDA + 16 * k + 4 * g4]);
 #pragma unroll
-                for (int e = 0; e < 4; ++e) t[jt][e] = x[e] * be[e];
+                    for (int e = 0; e < 4; ++e)
+                        M = __builtin_amdgcn_mfma_f32_16x16x4f32(A[e], T[(16 * k + 4 * g4 + e) * LDA + 16 * j + m], M, 0, 0, 0);
+                }
+                const f32x4_t D = *reinterpret_cast<const f32x4_t *>(&T[i * LDA + 16 * w + 4 * g4]);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) R = __builtin_amdgcn_mfma_f32_16x16x4f32(-D[e], M[e], R, 0, 0, 0);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) T[(16 * w + 4 * g4 + e) * LDA + 16 * j + m] = R[e];
             }
-            mx = max_abs(t[jt], mx);
+            __syncthreads();
         }
-        const RowScale sc = unit_scale(groups_max(mx));
-        if (g4 == 0) vec[V_T * CH + i] = exp2i(-sc.s);
+        {
+            f32x4_t t[4];
+            float mx = 0.f;
 #pragma unroll
-        for (int ks = 0; ks < 2; ++ks)
-            if (ks <= w / 2) {
-                u32x4_t f, r;
+            for (int jt = 0; jt < 4; ++jt) {
+                t[jt] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+                if (jt <= w) {
+                    const f32x4_t x = *reinterpret_cast<const f32x4_t *>(&T[i * LDA + 16 * jt + 4 * g4]);
+                    const f32x4_t be = *reinterpret_cast<const f32x4_t *>(&s_beta[hh][16 * jt + 4 * g4]);
 #pragma unroll
-                for (int q = 0; q < 2; ++q)
-#pragma unroll
-                    for (int e = 0; e < 4; e += 2) {
-                        const float x = t[2 * ks + q][e] * sc.sc, y = t[2 * ks + q][e + 1] * sc.sc;
-                        f[2 * q + e / 2] = f16_pair(x, y);
-                        r[2 * q + e / 2] = f16_rest(x, y, f[2 * q + e / 2]);
-                    }
-                const int at = w < 2 ? w : 2 * w - 2 + ks;
-                *reinterpret_cast<u32x4_t *>(unit + at * 1024 + lane * 16) = f;
-                *reinterpret_cast<u32x4_t *>(unit + (6 + at) * 1024 + lane * 16) = r;
+                    for (int e = 0; e < 4; ++e) t[jt][e] = x[e] * be[e];
+                }
+                mx = max_abs(t[jt], mx);
             }
-    }
-    if (tid < CH) {
-        const double G = s_G[tid], last = s_G[CH - 1];
-        const float f = s_f[0][tid], eg = exp_diff(G);
-        vec[V_A * CH + tid] = eg * f;
-        vec[V_B * CH + tid] = eg * s_f[1][tid];
-        vec[V_C * CH + tid] = exp_diff(last - G) * f;
-        vec[V_SK * CH + tid] = s_sc[0][tid];
-        vec[V_SQ * CH + tid] = s_sc[1][tid];
-        if (tid == 0) *reinterpret_cast<float *>(unit + UNIT_GAMMA) = exp_diff(last);
+            const RowScale sc = unit_scale(groups_max(mx));
+            if (g4 == 0) vec[V_T * CH + i] = exp2i(-sc.s);
+#pragma unroll
+            for (int ks = 0; ks < 2; ++ks)
+                if (ks <= w / 2) {
+                    u32x4_t f, r;
+#pragma unroll
+                    for (int q = 0; q < 2; ++q)
+#pragma unroll
+                        for (int e = 0; e < 4; e += 2) {
+                            const float x = t[2 * ks + q][e] * sc.sc, y = t[2 * ks + q][e + 1] * sc.sc;
+                            f[2 * q + e / 2] = f16_pair(x, y);
+                            r[2 * q + e / 2] = f16_rest(x, y, f[2 * q + e / 2]);
+                        }
+                    const int at = w < 2 ? w : 2 * w - 2 + ks;
+                    *reinterpret_cast<u32x4_t *>(unit + at * 1024 + lane * 16) = f;
+                    *reinterpret_cast<u32x4_t *>(unit + (6 + at) * 1024 + lane * 16) = r;
+                }
+        }
+        if (tid < CH) {
+            const double G = sG[tid], last = sG[CH - 1];
+            const float f = s_f[0][tid], eg = exp_diff(G);
+            vec[V_A * CH + tid] = eg * f;
+            vec[V_B * CH + tid] = eg * s_f[1][tid];
+            vec[V_C * CH + tid] = exp_diff(last - G) * f;
+            vec[V_SK * CH + tid] = s_sc[0][tid];
+            vec[V_SQ * CH + tid] = s_sc[1][tid];
+            if (tid == 0) *reinterpret_cast<float *>(unit + UNIT_GAMMA) = exp_diff(last);
+        }
+        if (hh + 1 < HP) __syncthreads();  // T and s_A are used
     }
 }
 
@@ -1074,9 +1089,15 @@ constexpr int SPLIT_TILES = 512;
 
 template <int DK>
 hipError_t launch_chunks(const DeltaArgs &a, void *ws, hipStream_t s) {
-    if (a.T > 0)
-        hipLaunchKernelGGL((delta_prep_kernel<DK>), dim3((unsigned)((a.T / CH + a.n_seq) * a.hv)), dim3(256), 0, s, a,
-                           static_cast<uint8_t *>(ws));
+    if (a.T > 0) {
+        const int64_t chunks = a.T / CH + a.n_seq;
+        uint8_t *units = static_cast<uint8_t *>(ws);
+        // two heads of a key head together where that leaves enough workgroups
+        if (a.hv / a.hk % 2 == 0 && chunks * a.hv >= 2048)
+            hipLaunchKernelGGL((delta_prep_kernel<DK, 2>), dim3((unsigned)(chunks * (a.hv / 2))), dim3(256), 0, s, a, units);
+        else
+            hipLaunchKernelGGL((delta_prep_kernel<DK, 1>), dim3((unsigned)(chunks * a.hv)), dim3(256), 0, s, a, units);
+    }
     // Workgroups of 16 columns while they fill the 256 compute units not much
     // more than once; else of 64.
     const int64_t tiles = (int64_t)a.n_seq * a.hv * (a.dv / 16);

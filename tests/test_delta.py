@@ -150,6 +150,15 @@ def test_many_columns(kind, lens, hk, hv, dk, dv):
     run(kind, lens, hk, hv, dk, dv, True, seed=hv)
 
 
+@pytest.mark.parametrize("dk,dv", [(64, 64), (128, 64)])
+def test_many_chunks(dk, dv):
+    """Chunks and heads enough for the preparation to take two heads of a key
+    head at a time (2048 pairs)."""
+    lens = [64, 5] * 44 + [63, 65, 130]
+    assert (sum(lens) // 64 + len(lens)) * 16 >= 2048
+    run("prefill", lens, 4, 16, dk, dv, True, seed=dk)
+
+
 @pytest.mark.parametrize("kind", KINDS)
 @pytest.mark.parametrize("name,change", [
     ("no decay", dict(g=lambda g: g * 0)), ("full decay", dict(g=lambda g: g * 0 - 200)),
