@@ -75,7 +75,8 @@ typedef struct moe_q4_linear_weights {
  *   act       moe_q4_act
  *   residual  bf16 [T] rows of N at distance ldr, or NULL; may be y itself
  *             (same pointer and distance, y_dtype MOE_Q4_BF16)
- *   y         bf16 or float (y_dtype) [T] rows of N at distance ldy
+ *   y         bf16 or float (y_dtype) [T] rows of N at distance ldy; must not
+ *             overlap the inputs otherwise
  * T < 2^31, T * N < 2^40.
  */
 MOE_Q4_API int moe_q4_linear(const void *x, int64_t ldx, int64_t T, const moe_q4_linear_weights *w, int32_t act,

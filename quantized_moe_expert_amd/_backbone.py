@@ -152,7 +152,7 @@ def moe_q4_linear(x, weights, y, act=ACT_NONE, residual=None, stream=None):
     linear_struct, y bf16 or float32 [T, N], residual bf16 [T, N] (may be y)."""
     dev = _device()
     T, N = x.shape[0], weights.out_features
-    if weights.device != dev:
+    if getattr(weights, "device", dev) != dev:
         raise ValueError("moe_q4 takes device tensors of the current device")
     xp, ldx = _rows(x, "x", dev, (T, weights.in_features))
     f32 = y.dtype == torch.float32

@@ -9,7 +9,10 @@
 // them of one (sequence, head): 8 threads of 4 columns side by side, k_dim
 // spread over the rest, the state in registers from the first token to the
 // last.  Bound by the state's bytes (8 per element): each row's 32 columns
-// are one 128-byte line.
+// are one 128-byte line.  Measured: 64 sequences of one token, 32 heads of
+// 128 x 128 (268 MB of states): 42 us, 6.4 TB/s (a part of the states comes
+// from the last-level cache; a large copy moves 5.1 TB/s); one sequence: 4.8 us,
+// the latency of one load, reduction and store.
 #include "backbone.h"
 
 namespace moeq4 {
@@ -207,8 +210,8 @@ __device__ __forceinline__ float max_abs(f32x4_t v, float m) {
     return fmaxf(fmaxf(fmaxf(fabsf(v[0]), fabsf(v[1])), fmaxf(fabsf(v[2]), fabsf(v[3]))), m);
 }
 
-// Barrier that orders LDS only: loads and stores in flight stay in flight
-// (waiting for them at every chunk took 4.6 us a chunk).
+// Barrier that orders LDS only: loads of the next chunk and stores of outputs
+// stay in flight over it.
 __device__ __forceinline__ void lds_barrier() {
     asm volatile("" ::: "memory");
     __builtin_amdgcn_s_waitcnt(0xc07f);  // lgkmcnt(0)
@@ -236,7 +239,11 @@ __device__ __forceinline__ float exp_diff(double d) {
 
 // T', P and the row factors of one chunk and HP heads of one key head (k and q,
 // and their products, are read and formed once for them).  Bound by the vector
-// work: about 1500 instructions a wave and chunk with one head.
+// work: about 1500 instructions a wave and chunk with one head, 80% of the
+// vector units' time.  Measured: 16384 tokens, 32 heads of 128 x 128 on 16 key
+// heads: 103 us with two heads (1.7 TB/s of the 173 MB it writes), 122 us with
+// one; with the tiles of A and P on one wave each (up to eight a wave) 128 us;
+// with a row's load waiting for the one before it 171 us.
 template <int DK, int HP>
 __global__ __launch_bounds__(256) void delta_prep_kernel(DeltaArgs a, uint8_t *__restrict__ ws) {
     constexpr int LDA = 68, PL = DK / 16;  // elements per lane of a row's 16 lanes
@@ -519,10 +526,16 @@ __global__ __launch_bounds__(256) void delta_prep_kernel(DeltaArgs a, uint8_t *_
 // chunk to LDS meanwhile: k and q as f16 rows, k transposed, and the operands
 // of delta_prep_kernel.
 //   SPLIT false: 64 columns per workgroup, each state wave has 16 of them and
-//     works alone (its chain of products and vector work takes 4.2 us a chunk).
+//     works alone.  A chunk of a 128 x 128 head takes 4.4 us: about 600 vector
+//     instructions on each of the 8 waves (half of the vector units' time) and
+//     the products (18% of the matrix units').
 //   SPLIT true: 16 columns per workgroup, the state waves share their rows (of
 //     the state and of the chunk) and hand each other S, X and U through LDS:
-//     a shorter chain, more LDS traffic per column.  For few columns in all.
+//     a shorter chain (3.0 us a chunk, a third of it the last stage), more LDS
+//     traffic per column.  For few columns in all.
+// Measured: one prompt of 8192 tokens, 32 heads of 128 x 128: 385 us with SPLIT,
+// 540 us without; with one state wave of 512 registers and three others 440 us.
+// 8 prompts of 2048: 284 us without SPLIT.
 template <int DK, bool SPLIT>
 __global__ __launch_bounds__(512) void delta_scan_kernel(DeltaArgs a, const uint8_t *__restrict__ ws) {
     constexpr int COLS = SPLIT ? 16 : 64;

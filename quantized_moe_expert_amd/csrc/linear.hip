@@ -74,7 +74,9 @@ __device__ __forceinline__ void store_output(const LinearArgs &a, int64_t t, int
 // them of a row of x straight into the operands of 16x16x32 products: the
 // order of the inputs within a product is free as long as both operands have
 // the same, so lane group g = lane / 16 takes 16 consecutive codes and two
-// products the halves of them.
+// products the halves of them.  Measured: one token, 4097 x 2048 bf16 (17 MB):
+// 5.3 us (3.2 TB/s); 16 tokens, 12288 x 2048 int8 (26 MB): 12.8 us (2.0 TB/s),
+// where each workgroup reads x (64 KB) besides 32 KB of codes.
 template <bool INT8, int MT, int NT, int WAVES>
 __global__ __launch_bounds__(WAVES * 64) void linear_rows_kernel(LinearArgs a, int ntiles, int ttiles) {
     constexpr int LW = INT8 ? 2 : 4;  // 16-byte loads of a row of W per unit
@@ -226,6 +228,11 @@ hipError_t launch_rows(const LinearArgs &a, hipStream_t s) {
 // never used), so that the wait before a step is one constant count.  Past
 // the row's end chunks are read from its last one and masked where they are
 // used.
+//
+// Measured: 4096 tokens, N = 8192, K = 2048: bf16 167 us (824 TFLOP/s; the
+// library's product takes 98 us), int8 196 us (701 TFLOP/s; 32% of the matrix
+// units' time, half of the vector units': the conversion, 2.5 instructions a
+// code, and the rescaling, one per sum and group).
 constexpr int BLK = 32;   // inputs of a block
 constexpr int RING = 4;
 

@@ -6,14 +6,15 @@
 // thread held in registers: the row is read once, and the maximum, the sums
 // and the selection are passes over registers.  A segment's sums are relative
 // to its own maximum; a row of several segments has them joined by a second
-// launch, in segment order (no atomics: the same input gives the same bits).
+// launch, in segment order, so that the same input gives the same bits.
 //
 // The largest n of a segment (n <= 32): the n-th largest of the 64 lanes'
 // maxima of a wave bounds the n-th largest logit from below (found bit by bit
-// with ballots; the logit's index, inverted, decides ties, so keys are unique
-// and exactly n lanes reach the bound).  Logits at or above the largest of the
-// four waves' bounds, some n to 3 n of them, are collected in LDS, and each
-// one's rank is the number of larger ones.
+// with ballots; where many lanes share it, the logit's index, inverted, decides
+// ties).  Logits at or above the largest of the four waves' bounds, a few n of
+// them, are collected in LDS, and each one's rank is the number of larger ones
+// (keys of value and index are unique, so the order of collecting, by an LDS
+// counter, does not matter).
 #include "backbone.h"
 
 namespace moeq4 {
@@ -208,7 +209,12 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
 
 // One segment per workgroup.  DIRECT: the row has one segment and the outputs
 // are written here; otherwise its sums and keys go to part / part_top.
-// Measured (512 rows of 151939 bf16, n = 20): see launch_logprobs.
+// Bound by the vector work (620 instructions a wave with a top list, 32 of them
+// exponentials of four times the cost; without a list by the bytes).  Measured,
+// 512 rows of 151939 bf16 (156 MB): 62 us with n = 20 (2.5 TB/s) and 7 us for the
+// join, 34.5 us in all with n = 0 (4.5 TB/s).  Before the candidates were found
+// by the sign of a difference and reloaded by place: 82 us; ranked by one lane
+// each with one key after another: 128 us.  One row of 4097, n = 8: 4.8 us.
 template <bool F32, bool TOP, bool DIRECT>
 __global__ __launch_bounds__(THREADS) void logprobs_segment_kernel(LogprobsArgs a, int segs,
                                                                    Sums *__restrict__ part,

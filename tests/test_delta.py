@@ -322,6 +322,50 @@ def test_graph_replays_and_streams(kind):
         assert torch.equal(s, es) and torch.equal(o, eo), i
 
 
+@pytest.mark.parametrize("kind", KINDS)
+def test_far_rows_and_states(kind):
+    """Rows 2^22 elements apart and a state beyond 2^31 elements."""
+    lens, ld, n = [1040, 3], 1 << 22, 2 ** 31 // (4 * 64 * 64) + 2
+    T = sum(lens)
+    q, k, v, g, beta, s0, start = inputs(lens, 2, 4, 64, 64, True, 14)
+    far = torch.empty(T, ld, dtype=torch.bfloat16, device="cuda")
+    parts = [far[:, 0:128].unflatten(1, (2, 64)), far[:, 2 ** 21:2 ** 21 + 128].unflatten(1, (2, 64)),
+             far[:, ld - 256:].unflatten(1, (4, 64)), far[:, 1024:1024 + 256].unflatten(1, (4, 64))]
+    for a, b in zip(parts, (q, k, v)):
+        a.copy_(b)
+    pool = torch.empty(n, 4, 64, 64, device="cuda")
+    idx = torch.tensor([n - 1, n - 2], dtype=torch.int32, device="cuda")
+    pool[n - 1], pool[n - 2] = s0[0], s0[1]
+    call(kind, parts[0], parts[1], parts[2], g, beta, start, idx, pool, pool, parts[3], 0.1, True)
+    torch.cuda.synchronize()
+    check(parts[3].contiguous(), torch.stack([pool[n - 1], pool[n - 2]]), rule(q, k, v, g, beta, lens, s0, 0.1, True),
+          lens, 0.1, 64, f"{kind} far")
+
+
+@pytest.mark.parametrize("kind", KINDS)
+def test_two_streams(kind):
+    """Calls on two streams at once, each with buffers of its own."""
+    jobs = []
+    for seed, lens in enumerate(([70, 3], [200], [64] * 30, [1] * 9)):
+        q, k, v, g, beta, s0, start = inputs(lens, 2, 4, 128, 128, True, seed)
+        T = sum(lens)
+        need = m.delta_workspace_size(T, len(lens), 2, 4, 128, 128)
+        ws = torch.empty(need, dtype=torch.uint8, device="cuda")
+        o, s1 = torch.empty(T, 4, 128, dtype=torch.bfloat16, device="cuda"), torch.empty_like(s0)
+        args = [q, k, v, g, beta, start, None, s0, s1, o, 0.1, True] + ([ws] if kind == "prefill" else [])
+        fn = m.moe_q4_delta_prefill if kind == "prefill" else m.moe_q4_delta_decode
+        fn(*args)
+        jobs.append((fn, args, o, s1, o.clone(), s1.clone()))
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    torch.cuda.synchronize()
+    for _ in range(4):
+        for i, (fn, args, o, s1, _, _) in enumerate(jobs):
+            fn(*args, stream=streams[i % 2])
+    torch.cuda.synchronize()
+    for _, _, o, s1, want_o, want_s in jobs:
+        assert torch.equal(o, want_o) and torch.equal(s1, want_s)
+
+
 def test_refusals():
     q, k, v, g, beta, s0, start = inputs([5], 2, 4, 64, 64, True)
     o = torch.empty_like(v)

@@ -191,6 +191,41 @@ def test_graph_replays_and_streams():
             assert torch.equal(y, want), (T, i)
 
 
+@pytest.mark.parametrize("fmt", ["int8", "bf16"])
+def test_far_rows(fmt):
+    """Rows 2^22 elements apart: element offsets pass 2^32."""
+    T, K, N, ld = 1100, 256, 130, 1 << 22
+    gen = torch.Generator(device="cuda").manual_seed(1)
+    q, s, w = weights(fmt, N, K, gen)
+    x = torch.empty(T, ld, dtype=torch.bfloat16, device="cuda")[:, :K]
+    y = torch.empty(T, ld, dtype=torch.bfloat16, device="cuda")[:, 5:5 + N]
+    x.copy_(torch.randn(T, K, generator=gen, device="cuda"))
+    for rows in (slice(0, T), slice(T - 20, T)):
+        m.moe_q4_linear(x[rows], m.linear_struct(q, s), y[rows])
+        torch.cuda.synchronize()
+        check(y[rows], x[rows], w, None, 0, None, f"far rows {fmt}")
+        y[rows] = float("nan")
+
+
+def test_two_streams():
+    """Calls on two streams at once, each with buffers of its own."""
+    gen = torch.Generator(device="cuda").manual_seed(2)
+    jobs = []
+    for T in (5, 40, 300, 700):
+        q, s, _ = weights("int8", 700, 1024, gen)
+        x = torch.randn(T, 1024, generator=gen, device="cuda").bfloat16()
+        w, want = m.linear_struct(q, s), torch.empty(T, 700, device="cuda")
+        m.moe_q4_linear(x, w, want)
+        jobs.append((x, w, want, torch.empty_like(want), (q, s)))
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    torch.cuda.synchronize()
+    for _ in range(5):
+        for i, (x, w, _, y, _) in enumerate(jobs):
+            m.moe_q4_linear(x, w, y, stream=streams[i % 2])
+    torch.cuda.synchronize()
+    assert all(torch.equal(y, want) for _, _, want, y, _ in jobs)
+
+
 def test_refusals():
     x = torch.zeros(4, 256, dtype=torch.bfloat16, device="cuda")
     q, s = torch.zeros(32, 256, dtype=torch.int8, device="cuda"), torch.zeros(32, 2, dtype=torch.float16, device="cuda")

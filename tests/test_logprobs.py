@@ -194,6 +194,33 @@ def test_graph_replays_and_streams():
             assert all(torch.equal(a, b) for a, b in zip(out, want)), (V, i)
 
 
+def test_far_rows():
+    """Rows 2^23 elements apart (offsets beyond 2^32), of one and of several
+    segments."""
+    for V in (5000, 20000):
+        l, tok = rows(600, V, "bf16", 6)
+        far = torch.empty(600, 1 << 23, dtype=torch.bfloat16, device="cuda")[:, 3:3 + V]
+        far.copy_(l)
+        check(far, tok, 7, f"far rows V={V}")
+
+
+def test_two_streams():
+    """Calls on two streams at once, each with buffers of its own."""
+    jobs = []
+    for i, (T, V) in enumerate(((3, 4097), (5, 60001), (40, 9000), (7, 300))):
+        l, tok = rows(T, V, "bf16", i)
+        ws = torch.empty(max(m.logprobs_workspace_size(T, V, 9), 1), dtype=torch.uint8, device="cuda")
+        jobs.append((l, tok, ws, score(l, tok, 9), [torch.zeros_like(t) for t in score(l, tok, 9)]))
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    torch.cuda.synchronize()
+    for _ in range(5):
+        for i, (l, tok, ws, _, out) in enumerate(jobs):
+            m.moe_q4_logprobs(l, tok, *out, ws, stream=streams[i % 2])
+    torch.cuda.synchronize()
+    for _, _, _, want, out in jobs:
+        assert all(torch.equal(a, b) for a, b in zip(out, want))
+
+
 def test_refusals():
     l, tok = rows(4, 100, "bf16", 0)
     f, i = torch.zeros(4, device="cuda"), torch.zeros(4, 5, dtype=torch.int32, device="cuda")
