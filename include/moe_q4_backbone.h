@@ -77,7 +77,7 @@ typedef struct moe_q4_linear_weights {
  *             (same pointer and distance, y_dtype MOE_Q4_BF16)
  *   y         bf16 or float (y_dtype) [T] rows of N at distance ldy; must not
  *             overlap the inputs otherwise
- * T < 2^31, T * N < 2^40.
+ * T < 2^29, T * N < 2^38.
  */
 MOE_Q4_API int moe_q4_linear(const void *x, int64_t ldx, int64_t T, const moe_q4_linear_weights *w, int32_t act,
                              const void *residual, int64_t ldr, void *y, int64_t ldy, int32_t y_dtype,
@@ -124,8 +124,8 @@ typedef struct moe_q4_delta_shape {
  *   o          bf16 [T] rows of [v_heads][v_dim] at distance ldo, 16-byte
  *              aligned, ldo % 8 == 0; must not overlap the inputs
  * n_seq = 0 returns MOE_Q4_OK without launching anything.  With T = 0 the row
- * pointers may be NULL.  T < 2^31, n_seq < 2^20, n_seq * v_heads < 2^28,
- * (T / 64 + n_seq) * v_heads < 2^31.
+ * pointers may be NULL.  T < 2^31, n_seq < 2^20, n_seq * v_heads < 2^21,
+ * (T / 64 + n_seq) * v_heads < 2^24.
  *
  * moe_q4_delta_decode takes the tokens of a sequence one after another (tuned
  * for a few tokens per sequence); moe_q4_delta_prefill takes them in chunks of
@@ -166,7 +166,7 @@ MOE_Q4_API int moe_q4_delta_prefill(const void *q, int64_t ldq, const void *k, i
  *   top_logprob  float [T][n_top] out (n_top > 0): their log p
  *   ws           >= moe_q4_logprobs_workspace_size(T, V, n_top) bytes,
  *                16-byte aligned (may be NULL when that is 0)
- * T < 2^31, V < 2^31 - 2^16, ld < 2^40.  Sums are fp32, each over one part of a
+ * T * ceil(V / 8192) < 2^24, V < 2^31 - 2^16, ld < 2^40.  Sums are fp32, each over one part of a
  * row, joined in a fixed order: the same input gives the same bits.
  */
 MOE_Q4_API size_t moe_q4_logprobs_workspace_size(int64_t T, int64_t V, int32_t n_top);

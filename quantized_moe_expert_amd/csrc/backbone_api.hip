@@ -7,6 +7,7 @@ using namespace moeq4;
 
 namespace {
 
+// (The limits on products of sizes keep every launch below 2^32 threads.)
 constexpr int64_t LD_MAX = (int64_t)1 << 22;
 
 bool aligned(const void *p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
@@ -35,8 +36,8 @@ int delta_args(const void *q, int64_t ldq, const void *k, int64_t ldk, const voi
     int st = check_delta_shape(sh);
     if (st) return st;
     if (T < 0 || n_seq < 0 || n_states < 0) return MOE_Q4_ERR_INVALID_ARG;
-    if (T >= (int64_t)1 << 31 || n_seq >= 1 << 20 || (int64_t)n_seq * sh->v_heads >= 1 << 28 ||
-        (T / 64 + n_seq) * sh->v_heads >= (int64_t)1 << 31)
+    if (T >= (int64_t)1 << 31 || n_seq >= 1 << 20 || (int64_t)n_seq * sh->v_heads >= 1 << 21 ||
+        (T / 64 + n_seq) * sh->v_heads >= 1 << 24)
         return MOE_Q4_ERR_UNSUPPORTED;
     if (n_seq == 0) return MOE_Q4_OK;
     if (!seq_start || !aligned(seq_start, 4) || !aligned(state_idx, 4) || !aligned(state_in, 16) ||
@@ -68,7 +69,7 @@ int moe_q4_linear(const void *x, int64_t ldx, int64_t T, const moe_q4_linear_wei
     if (w->format != MOE_Q4_LINEAR_INT8 && w->format != MOE_Q4_LINEAR_BF16) return MOE_Q4_ERR_UNSUPPORTED;
     const bool int8 = w->format == MOE_Q4_LINEAR_INT8;
     if (int8 && (!w->scale || !aligned(w->scale, 2))) return MOE_Q4_ERR_INVALID_ARG;
-    if (K % (int8 ? 128 : 8) || K > 65536 || N >= 1 << 24 || T >= (int64_t)1 << 31 || T * N >= (int64_t)1 << 40)
+    if (K % (int8 ? 128 : 8) || K > 65536 || N >= 1 << 24 || T >= (int64_t)1 << 29 || T * N >= (int64_t)1 << 38)
         return MOE_Q4_ERR_UNSUPPORTED;
     if (act < MOE_Q4_ACT_NONE || act > MOE_Q4_ACT_GELU) return MOE_Q4_ERR_UNSUPPORTED;
     if (y_dtype != MOE_Q4_BF16 && y_dtype != MOE_Q4_F32) return MOE_Q4_ERR_UNSUPPORTED;
@@ -132,7 +133,7 @@ int moe_q4_logprobs(const void *logits, int32_t dtype, int64_t T, int64_t V, int
         return MOE_Q4_ERR_UNSUPPORTED;
     if (dtype != MOE_Q4_BF16 && dtype != MOE_Q4_F32) return MOE_Q4_ERR_UNSUPPORTED;
     if (T == 0) return MOE_Q4_OK;
-    if (T * logprobs_segments(V) >= (int64_t)1 << 31) return MOE_Q4_ERR_UNSUPPORTED;  // workgroups
+    if (T * logprobs_segments(V) >= 1 << 24) return MOE_Q4_ERR_UNSUPPORTED;
     if (!logits || !aligned(logits, dtype == MOE_Q4_F32 ? 4 : 2) || ld < V) return MOE_Q4_ERR_INVALID_ARG;
     if ((tokens && !logprob) || (n_top > 0 && (!top_idx || !top_logprob))) return MOE_Q4_ERR_INVALID_ARG;
     if (!aligned(tokens, 4) || !aligned(logprob, 4) || !aligned(entropy, 4) || !aligned(top_idx, 4) ||

@@ -126,7 +126,6 @@ __global__ __launch_bounds__(256) void delta_decode_kernel(DeltaArgs a) {
 template <int DK, int DV>
 hipError_t launch_decode(const DeltaArgs &a, hipStream_t s) {
     const int64_t blocks = (int64_t)a.n_seq * a.hv * (DV / DNB);
-    if (blocks >= (int64_t)1 << 31) return hipErrorInvalidValue;
     hipLaunchKernelGGL((delta_decode_kernel<DK, DV>), dim3((unsigned)blocks), dim3(256), 0, s, a);
     return hipGetLastError();
 }

@@ -197,7 +197,6 @@ template <bool INT8, int MT, int NT, int WAVES>
 hipError_t launch_rows(const LinearArgs &a, hipStream_t s) {
     const int ntiles = (a.N + 16 * NT - 1) / (16 * NT);
     const int64_t ttiles = (a.T + 16 * MT - 1) / (16 * MT);
-    if (ntiles * ttiles >= (int64_t)1 << 31) return hipErrorInvalidValue;
     hipLaunchKernelGGL((linear_rows_kernel<INT8, MT, NT, WAVES>), dim3((unsigned)(ntiles * ttiles)), dim3(WAVES * 64),
                        0, s, a, ntiles, (int)ttiles);
     return hipGetLastError();
@@ -561,7 +560,6 @@ __global__ __launch_bounds__((Tile<INT8, BM, BN, WM, WN, WK>::THREADS)) void lin
 template <bool INT8, int BM, int BN, int WM, int WN, int WK>
 hipError_t launch_tile(const LinearArgs &a, hipStream_t s) {
     const int64_t ttiles = (a.T + BM - 1) / BM, ntiles = (a.N + BN - 1) / BN;
-    if (ntiles * ttiles >= (int64_t)1 << 28) return hipErrorInvalidValue;
     hipLaunchKernelGGL((linear_tile_kernel<INT8, BM, BN, WM, WN, WK>), dim3((unsigned)(ntiles * ttiles)),
                        dim3(Tile<INT8, BM, BN, WM, WN, WK>::THREADS), 0, s, a, (int)ntiles, (int)ttiles);
     return hipGetLastError();

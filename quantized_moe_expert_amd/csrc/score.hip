@@ -447,7 +447,6 @@ template <bool F32>
 hipError_t launch(const LogprobsArgs &a, void *ws, hipStream_t s) {
     const int segs = logprobs_segments(a.V);
     const int64_t blocks = a.T * segs;
-    if (blocks >= (int64_t)1 << 31) return hipErrorInvalidValue;
     const dim3 grid((unsigned)blocks), block(THREADS);
     Sums *part = nullptr;
     uint64_t *part_top = static_cast<uint64_t *>(ws);

@@ -54,6 +54,7 @@ def _linear(K=256, N=100, fmt=m.LINEAR_INT8, q=FAKE, scale=FAKE, bias=None, x=FA
     (UNSUPPORTED, dict(ydt=2)),
     (UNSUPPORTED, dict(K=192)), (UNSUPPORTED, dict(K=65664)), (UNSUPPORTED, dict(fmt=1, K=100)),
     (UNSUPPORTED, dict(N=1 << 24)), (UNSUPPORTED, dict(T=1 << 31)), (UNSUPPORTED, dict(T=1 << 20, N=1 << 20)),
+    (UNSUPPORTED, dict(T=1 << 29, N=1)), (UNSUPPORTED, dict(T=1 << 16, N=1 << 22)),  # launches of 2^32 threads
     (INVALID, dict(ldx=248)), (INVALID, dict(ldx=260)), (UNSUPPORTED, dict(ldx=(1 << 22) + 8)),
     (INVALID, dict(ldy=99)), (UNSUPPORTED, dict(ldy=(1 << 22) + 1)),
     (INVALID, dict(res=FAKE + 64, ldr=99)), (UNSUPPORTED, dict(res=FAKE + 64, ldr=(1 << 22) + 1)),
@@ -90,6 +91,7 @@ def _delta(prefill, hk=2, hv=4, dk=128, dv=128, T=10, n_seq=2, n_states=2, q=FAK
     (INVALID, dict(T=-1)), (INVALID, dict(n_seq=-1)), (INVALID, dict(n_states=-1)),
     (UNSUPPORTED, dict(T=1 << 31)), (UNSUPPORTED, dict(n_seq=1 << 20)),
     (UNSUPPORTED, dict(n_seq=1 << 19, hk=1, hv=512)),
+    (UNSUPPORTED, dict(n_seq=1 << 19)), (UNSUPPORTED, dict(T=1 << 28)),  # launches of 2^32 threads
     (INVALID, dict(q=None)), (INVALID, dict(k=None)), (INVALID, dict(v=None)), (INVALID, dict(o=None)),
     (INVALID, dict(g=None)), (INVALID, dict(beta=None)), (INVALID, dict(start=None)),
     (INVALID, dict(q=FAKE + 8)), (INVALID, dict(o=FAKE + 8)), (INVALID, dict(g=FAKE + 2)),
@@ -124,6 +126,7 @@ def _scores(logits=FAKE, dtype=0, T=4, V=100, ld=100, tokens=FAKE, logprob=FAKE,
     (INVALID, dict(tokens=FAKE + 2)), (INVALID, dict(entropy=FAKE + 2)), (INVALID, dict(idx=FAKE + 2)),
     (UNSUPPORTED, dict(n=33)), (UNSUPPORTED, dict(dtype=2)), (UNSUPPORTED, dict(T=1 << 31)),
     (UNSUPPORTED, dict(V=1 << 31, ld=1 << 31)), (UNSUPPORTED, dict(ld=1 << 40)),
+    (UNSUPPORTED, dict(T=1 << 24)), (UNSUPPORTED, dict(T=1 << 23, V=10000, ld=10000)),  # launches of 2^32 threads
     (OK, dict(T=0)), (OK, dict(T=0, logits=None)),
     (OK, dict(tokens=None, logprob=None, entropy=None, n=0, idx=None, top=None)),
 ])
