@@ -38,6 +38,16 @@ __device__ __forceinline__ uint32_t upper_pair(float a, float b) {
 __device__ __forceinline__ float code(uint32_t w, int j, float f) {
     return fmaf((float)(w >> (8 * j) & 0xffu), f, -128.0f * f);
 }
+// The same with f = 1.
+__device__ __forceinline__ float code1(uint32_t w, int j) { return (float)(int8_t)(w >> (8 * j)); }
+__device__ __forceinline__ u32x4_t codes_bf16(uint32_t lo, uint32_t hi) {
+    u32x4_t r;
+    r.x = upper_pair(code1(lo, 0), code1(lo, 1));
+    r.y = upper_pair(code1(lo, 2), code1(lo, 3));
+    r.z = upper_pair(code1(hi, 0), code1(hi, 1));
+    r.w = upper_pair(code1(hi, 2), code1(hi, 3));
+    return r;
+}
 // 8 codes (two dwords) times f, a power of two or 0, as 8 bf16 (exact).
 __device__ __forceinline__ u32x4_t codes_bf16(uint32_t lo, uint32_t hi, float f) {
     lo ^= 0x80808080u;
@@ -143,8 +153,8 @@ __global__ __launch_bounds__(WAVES * 64) void linear_rows_kernel(LinearArgs a, i
                 u32x4_t b[4];
 #pragma unroll
                 for (int l = 0; l < 4; ++l)
-                    b[l] = (l & 1) ? codes_bf16(d.w[j][l >> 1].z, d.w[j][l >> 1].w, 1.0f)
-                                   : codes_bf16(d.w[j][l >> 1].x, d.w[j][l >> 1].y, 1.0f);
+                    b[l] = (l & 1) ? codes_bf16(d.w[j][l >> 1].z, d.w[j][l >> 1].w)
+                                   : codes_bf16(d.w[j][l >> 1].x, d.w[j][l >> 1].y);
                 const float s = f16_to_f32(d.s[j]);
 #pragma unroll
                 for (int i = 0; i < MT; ++i) {
@@ -211,10 +221,18 @@ hipError_t launch_rows(const LinearArgs &a, hipStream_t s) {
 // quarter).  A stage is 32 WK inputs: WK blocks of rows of 32 bf16 (64 bytes),
 // 16-byte chunk c of row r at place c ^ (r / 2 & 3), so that the lanes of a
 // read spread over the banks.  x and bf16 weights go to LDS by direct loads
-// (the source address carries the swizzle); int8 codes go there the same way
-// and are converted, LDS to LDS, once for all waves.
+// (the source address carries the swizzle); int8 codes go there the same way.
 //
-// A group's scale s = m 2^e, 1 <= |m| < 2: 2^e goes into the converted codes
+// Codes that several waves use are converted, LDS to LDS, once for all of
+// them.  Codes that one wave uses alone (WM = 1, the small tiles) it converts
+// in its registers, 1.5 instructions a code; a stage is a group then, whose
+// products start from 0 and are scaled and added under the next stage's.
+// Measured: 300 tokens, N = 2048, K = 4096: 24.7 us so, 35 us by way of LDS
+// (a step costs 0.75 us however few the tiles: the chain from barrier to
+// barrier, with two waves on a SIMD; bf16 19 us); its scales read by each wave
+// for itself, 64 bytes a row apart, cost 6 us more.
+//
+// Else a group's scale s = m 2^e, 1 <= |m| < 2: 2^e goes into the converted codes
 // (exact in bf16), and the sums are kept in units of the current group's m,
 // i.e. multiplied by m_g / m_(g+1) between groups and by the last m at the
 // end.  A zero scale has codes 0 and m = 1.
@@ -234,6 +252,7 @@ hipError_t launch_rows(const LinearArgs &a, hipStream_t s) {
 // code, and the rescaling, one per sum and group).
 constexpr int BLK = 32;   // inputs of a block
 constexpr int RING = 4;
+constexpr int OWN_GROUPS = 64;  // groups whose scales are in LDS at a time (OWN)
 
 // m and 2^e of a group's scale (f16 bits).
 __device__ __forceinline__ float scale_pow2(uint16_t s) {
@@ -275,6 +294,10 @@ struct Tile {
     static constexpr int A_ITEMS = BM * 4 * WK / THREADS;  // 16-byte chunks per thread
     static constexpr int B_ITEMS = BN * (INT8 ? 2 : 4) * WK / THREADS;
     static constexpr int OPS = A_ITEMS + B_ITEMS;  // loads per stage and thread
+    // codes that one wave uses alone are converted in its registers; a stage is
+    // a group then
+    static constexpr bool OWN = INT8 && WM == 1;
+    static_assert(!OWN || WK == 4, "a stage is a group");
     static_assert(BM * 4 * WK % THREADS == 0 && BN * 2 * WK % THREADS == 0, "whole chunks");
 };
 
@@ -284,10 +307,12 @@ __global__ __launch_bounds__((Tile<INT8, BM, BN, WM, WN, WK>::THREADS)) void lin
                                                                                               int ttiles) {
     using C = Tile<INT8, BM, BN, WM, WN, WK>;
     constexpr int TM = C::TM, TN = C::TN;
+    constexpr bool OWN = C::OWN;
     // a slot: x, weights as bf16, codes (and, once they are converted, the m of
     // the weight rows in their place)
-    constexpr int A_BYTES = WK * BM * 64, B_BYTES = WK * BN * 64, C_BYTES = INT8 ? WK * BN * 32 : 0;
-    constexpr int SLOT = A_BYTES + B_BYTES + C_BYTES;
+    constexpr int A_BYTES = WK * BM * 64, B_BYTES = OWN ? 0 : WK * BN * 64, C_BYTES = INT8 ? WK * BN * 32 : 0;
+    constexpr int S_BYTES = OWN ? BN * (OWN_GROUPS / RING) * 2 : 0;
+    constexpr int SLOT = A_BYTES + B_BYTES + C_BYTES + S_BYTES;
     __shared__ __align__(16) uint8_t s_0[SLOT], s_1[SLOT], s_2[SLOT], s_3[SLOT];
     // The compiler waits for all direct loads in flight before an LDS access
     // that it cannot tell to be in another array, or whose own stage's loads it
@@ -344,20 +369,22 @@ __global__ __launch_bounds__((Tile<INT8, BM, BN, WM, WN, WK>::THREADS)) void lin
     typedef __attribute__((address_space(3))) void lds_void;
     auto load = [&](int step, int u) {
         const int k0 = (step < steps ? step : steps - 1) * C::BK;
+        // (int8 rows are whole stages)
+        const uint8_t *xk0 = xb + (INT8 ? 2 * (int64_t)k0 : 0), *wk0 = wb + (INT8 ? k0 : 0);
 #pragma unroll
         for (int i = 0; i < C::A_ITEMS; ++i) {
-            int k = k0 + xk[i];
-            k = k < K ? k : K - 8;
-            __builtin_amdgcn_global_load_lds((const void *)(xb + (xo[i] + 2u * (uint32_t)k)),
+            int k = INT8 ? xk[i] : k0 + xk[i];
+            if (!INT8) k = k < K ? k : K - 8;
+            __builtin_amdgcn_global_load_lds((const void *)(xk0 + (xo[i] + 2u * (uint32_t)k)),
                                              (lds_void *)(slot_a(u) + (i * C::THREADS + wave * 64) * 16), 16, 0,
                                              0);
         }
 #pragma unroll
         for (int i = 0; i < C::B_ITEMS; ++i) {
-            int k = k0 + wkk[i];
-            k = k < K ? k : K - (INT8 ? 16 : 8);
+            int k = INT8 ? wkk[i] : k0 + wkk[i];
+            if (!INT8) k = k < K ? k : K - 8;
             const int at = (i * C::THREADS + wave * 64) * 16;
-            __builtin_amdgcn_global_load_lds((const void *)(wb + (wo[i] + (INT8 ? 1u : 2u) * (uint32_t)k)),
+            __builtin_amdgcn_global_load_lds((const void *)(wk0 + (wo[i] + (INT8 ? 1u : 2u) * (uint32_t)k)),
                                              (lds_void *)(INT8 ? slot_c(u, at) : slot_b(u, at)), 16, 0, 0);
         }
     };
@@ -413,6 +440,7 @@ __global__ __launch_bounds__((Tile<INT8, BM, BN, WM, WN, WK>::THREADS)) void lin
     const int place = col >> 1 & 3;  // rows of a lane differ by multiples of 32
     struct Frags {
         u32x4_t a[TM], b[TN];
+        uint2 c[TN];  // OWN: codes in place of b
     };
     // operands of half `kk` of the wave's block of a stage
     auto read = [&](int step, int u, int kk, Frags &f) {
@@ -421,14 +449,21 @@ __global__ __launch_bounds__((Tile<INT8, BM, BN, WM, WN, WK>::THREADS)) void lin
 #pragma unroll
         for (int i = 0; i < TM; ++i) f.a[i] = *reinterpret_cast<const u32x4_t *>(slot_a(u) + (oa + i * 32 * 64));
 #pragma unroll
-        for (int j = 0; j < TN; ++j) f.b[j] = *reinterpret_cast<const u32x4_t *>(slot_b(u, ob + j * 32 * 64));
+        for (int j = 0; j < TN; ++j) {
+            if (OWN)
+                f.c[j] = *reinterpret_cast<const uint2 *>(
+                    slot_c(u, (wk * BN + row_b + 32 * j) * 32 + (2 * kk + half) * 8));
+            else
+                f.b[j] = *reinterpret_cast<const u32x4_t *>(slot_b(u, ob + j * 32 * 64));
+        }
         if ((step + 1) * C::BK > K) {
             const bool in = step * C::BK + wk * BLK + (2 * kk + half) * 8 < K;
             const u32x4_t zero = {0, 0, 0, 0};
 #pragma unroll
             for (int i = 0; i < TM; ++i) f.a[i] = in ? f.a[i] : zero;
 #pragma unroll
-            for (int j = 0; j < TN; ++j) f.b[j] = in ? f.b[j] : zero;
+            for (int j = 0; j < TN; ++j)
+                if (!OWN) f.b[j] = in ? f.b[j] : zero;  // (codes are finite)
         }
     };
     auto multiply = [&](const Frags &f) {
@@ -454,54 +489,147 @@ __global__ __launch_bounds__((Tile<INT8, BM, BN, WM, WN, WK>::THREADS)) void lin
         }
     };
 
-    // step s: the second half's operands are read under the products of the
-    // first, the next step's first half under those of the second; between
-    // them stage s + 1 is waited for, and stage s + RING takes the slot that
-    // every wave has read by then.  Steps behind the last one, up to a
-    // multiple of RING, multiply zeros.
-#pragma unroll
-    for (int u = 0; u < RING; ++u) {
-        load(u, u);
-        FENCE();
-    }
-    if (INT8) {
-        WAIT_VM((RING - 1) * C::OPS);
-        convert(0, 0);
-    }
-    WAIT_VM_LDS((RING - 1) * C::OPS);
-    lds_barrier();
-    Frags f0, f1;
-    read(0, 0, 0, f0);
-    if (INT8) {
-#pragma unroll
-        for (int j = 0; j < TN; ++j) m_now[j] = read_m(0, j);
-    }
-    for (int base = 0; base < steps; base += RING) {
+    // OWN: scales of groups first .. first + 63, group g in slot g % RING: a wave
+    // takes one slot, 16 lanes a row
+    auto store_scales = [&](int first) {
+        static_assert(OWN_GROUPS / RING == 16, "lanes of a row");
+        constexpr int WAVES = C::THREADS / 64;
+        int l = lane;
+        asm volatile("" : "+v"(l));  // (addresses formed here, not held in registers over the products)
+        const int i = l & 15, r0 = wave / RING * 4 + (l >> 4);
 #pragma unroll
         for (int u = 0; u < RING; ++u) {
-            const int step = base + u;
-            read(step, u, 1, f1);
-            if (INT8) {
-                WAIT_VM((RING - 2) * C::OPS);
-                convert(step + 1, (u + 1) % RING);
-                // a group is four blocks
-                if (WK == 4 ? step > 0 : u == 0 && step > 0) rescale(u);
-            }
-            multiply(f0);
-            WAIT_VM_LDS((RING - 2) * C::OPS);
-            lds_barrier();
-            load(step + RING, u);
-            read(step + 1, (u + 1) % RING, 0, f0);
-            multiply(f1);
-        }
-    }
-    if (INT8) {
+            if (wave % RING != u) continue;
+            const int g = first + i * RING + u;
 #pragma unroll
-        for (int j = 0; j < TN; ++j)
+            for (int it = 0; it < BN / WAVES; ++it) {
+                const int r = r0 + it * WAVES, n = n0 + r < a.N ? n0 + r : a.N - 1;
+                *reinterpret_cast<uint16_t *>(slot_c(u, C_BYTES + (r * 16 + i) * 2)) =
+                    g < groups ? a.scale[(int64_t)n * groups + g] : 0;  // 0 for the steps behind the last
+            }
+        }
+    };
+    if constexpr (OWN) {
+        // A step's products start from 0; they are scaled and summed one step
+        // later, under the next products.
+        f32x16_t p[2][TM][TN];
+        float s_now[TN], s_last[TN];
+        auto multiply_own = [&](const Frags &f, f32x16_t (&q)[TM][TN], bool first) {
+#pragma unroll
+            for (int j = 0; j < TN; ++j) {
+                const u32x4_t b = codes_bf16(f.c[j].x, f.c[j].y);
+#pragma unroll
+                for (int i = 0; i < TM; ++i) {
+                    f32x16_t c;
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) c[e] = 0.f;
+                    q[i][j] = mfma32(f.a[i], b, first ? c : q[i][j]);
+                }
+            }
+        };
+        auto add_last = [&](const f32x16_t (&q)[TM][TN]) {
+#pragma unroll
+            for (int j = 0; j < TN; ++j)
+#pragma unroll
+                for (int i = 0; i < TM; ++i)
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) acc[i][j][e] = fmaf(q[i][j][e], s_last[j], acc[i][j][e]);
+        };
+        auto read_scales = [&](int step, int u) {
+#pragma unroll
+            for (int j = 0; j < TN; ++j)
+                s_now[j] = f16_to_f32(*reinterpret_cast<const uint16_t *>(
+                    slot_c(u, C_BYTES + ((row_b + 32 * j) * 16 + step % OWN_GROUPS / RING) * 2)));
+        };
+#pragma unroll
+        for (int j = 0; j < TN; ++j) {
+            s_last[j] = 0.f;
 #pragma unroll
             for (int i = 0; i < TM; ++i)
 #pragma unroll
-                for (int e = 0; e < 16; ++e) acc[i][j][e] *= m_now[j];
+                for (int e = 0; e < 16; ++e) p[1][i][j][e] = 0.f;
+        }
+#pragma unroll
+        for (int u = 0; u < RING; ++u) {
+            load(u, u);
+            FENCE();
+        }
+        Frags f0, f1;
+        for (int base = 0; base < steps; base += RING) {
+            // (every wave has read the last scales before the last barrier)
+            if (base % OWN_GROUPS == 0) {
+                store_scales(base);
+                WAIT_VM_LDS(0);
+                lds_barrier();
+                if (base == 0) read(0, 0, 0, f0);
+            }
+#pragma unroll
+            for (int u = 0; u < RING; ++u) {
+                const int step = base + u;
+                read(step, u, 1, f1);
+                read_scales(step, u);
+                multiply_own(f0, p[u & 1], true);
+                add_last(p[(u + 1) & 1]);
+#pragma unroll
+                for (int j = 0; j < TN; ++j) s_last[j] = s_now[j];
+                WAIT_VM_LDS((RING - 2) * C::OPS);
+                lds_barrier();
+                load(step + RING, u);
+                read(step + 1, (u + 1) % RING, 0, f0);
+                multiply_own(f1, p[u & 1], false);
+            }
+        }
+        add_last(p[1]);
+    } else {
+        // step s: the second half's operands are read under the products of the
+        // first, the next step's first half under those of the second; between
+        // them stage s + 1 is waited for, and stage s + RING takes the slot that
+        // every wave has read by then.  Steps behind the last one, up to a
+        // multiple of RING, multiply zeros.
+#pragma unroll
+        for (int u = 0; u < RING; ++u) {
+            load(u, u);
+            FENCE();
+        }
+        if (INT8) {
+            WAIT_VM((RING - 1) * C::OPS);
+            convert(0, 0);
+        }
+        WAIT_VM_LDS((RING - 1) * C::OPS);
+        lds_barrier();
+        Frags f0, f1;
+        read(0, 0, 0, f0);
+        if (INT8) {
+#pragma unroll
+            for (int j = 0; j < TN; ++j) m_now[j] = read_m(0, j);
+        }
+        for (int base = 0; base < steps; base += RING) {
+#pragma unroll
+            for (int u = 0; u < RING; ++u) {
+                const int step = base + u;
+                read(step, u, 1, f1);
+                if (INT8) {
+                    WAIT_VM((RING - 2) * C::OPS);
+                    convert(step + 1, (u + 1) % RING);
+                    // a group is four blocks
+                    if (WK == 4 ? step > 0 : u == 0 && step > 0) rescale(u);
+                }
+                multiply(f0);
+                WAIT_VM_LDS((RING - 2) * C::OPS);
+                lds_barrier();
+                load(step + RING, u);
+                read(step + 1, (u + 1) % RING, 0, f0);
+                multiply(f1);
+            }
+        }
+        if (INT8) {
+#pragma unroll
+            for (int j = 0; j < TN; ++j)
+#pragma unroll
+                for (int i = 0; i < TM; ++i)
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) acc[i][j][e] *= m_now[j];
+        }
     }
     WAIT_VM_LDS(0);
     lds_barrier();  // every wave is done with the slots
@@ -568,13 +696,17 @@ hipError_t launch_tile(const LinearArgs &a, hipStream_t s) {
 // Which kernel and tile.  Measured (us, int8 / bf16, MI355X):
 //   16 tokens, N = 12288, K = 2048: rows<1,1,8> 12.8 / 16.3, <1,2,8> 14.2 / 17.6, <1,4,4> 12.9 / 15.6;
 //   N = 2048, K = 4096: 9.3 / 10.3, 12.6 / 13.7, 19.5 / 21.7
-//   64 tokens, N = 2048, K = 4096: rows<2,1,4> 13.4 / 15.4, <2,2,4> 17.4 / 18.5, 64x64 tiles 35 / 19;
+//   64 tokens, N = 2048, K = 4096: rows<2,1,4> 13.1 / 15.4, <2,2,4> 17.4 / 18.5, 64x32 tiles 19.8 / 12.9;
 //   N = 12288, K = 2048: <2,1,4> 32.4 / 36.2, <2,2,4> 24.5 / 29.4
-//   300 tokens, N = 2048, K = 4096: 64x64 35 / 19, 128x128 83 / 39; N = 8192, K = 2048: 53 / 33, 49 / 28
-//   1000 tokens, N = 4097, K = 2048: 64x64 86 / 53, 128x128 59 / 42, 128x256 58 / 40, 256x256 85 / 63
+//   128 tokens, N = 2048, K = 4096: rows<2,2,4> 17.8 / 20.3, 64x32 19.8 / 13.1, 64x64 24.4 / 18.4;
+//   N = 8192, K = 2048: 30.5 / 33.8, 27.8 / 17.6, 17.3 / 13.9
+//   300 tokens, N = 2048, K = 4096: 64x32 40 / 25, 64x64 24.7 / 19, 128x128 83 / 39;
+//   N = 8192, K = 2048: 64x64 44 / 33, 128x128 48 / 28
+//   1000 tokens, N = 4097, K = 2048: 64x64 72 / 53, 128x128 59 / 42, 128x256 58 / 40, 256x256 85 / 63
 //   4096 tokens, N = 2048, K = 4096: 128x128 125 / 97, 128x256 119 / 84, 256x256 148 / 107;
 //   N = 8192, K = 2048: 250 / 203, 247 / 199, 196 / 167
-// so: the largest tile that leaves the 256 compute units enough of them.
+// so: the largest tile that leaves the 256 compute units enough of them, and the
+// smallest while it gives each unit one at most.
 template <bool INT8>
 hipError_t launch_any(const LinearArgs &a, hipStream_t s) {
     if (a.T <= 16) return launch_rows<INT8, 1, 1, 8>(a, s);
@@ -583,6 +715,7 @@ hipError_t launch_any(const LinearArgs &a, hipStream_t s) {
     if (tiles(256, 256) >= 400) return launch_tile<INT8, 256, 256, 2, 4, 1>(a, s);
     if (tiles(128, 256) >= 128) return launch_tile<INT8, 128, 256, 2, 4, 1>(a, s);
     if (tiles(128, 128) >= 160) return launch_tile<INT8, 128, 128, 2, 2, 1>(a, s);
+    if (tiles(64, 32) <= 256) return launch_tile<INT8, 64, 32, 1, 1, 4>(a, s);
     return launch_tile<INT8, 64, 64, 1, 2, 4>(a, s);
 }
 

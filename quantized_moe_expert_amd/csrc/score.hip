@@ -156,11 +156,6 @@ __device__ __forceinline__ uint64_t wave_bound(uint32_t hi, int n, F lo_of) {
     return ((uint64_t)v << 32) | w;
 }
 
-// Lanes of a ballot below this one.
-__device__ __forceinline__ int lanes_below(uint64_t ballot) {
-    return __builtin_amdgcn_mbcnt_hi((uint32_t)(ballot >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)ballot, 0));
-}
-
 // Bit 31 - i: l[i] < limit, for a finite limit: the sign of the difference,
 // shifted in (two instructions a logit; a compare and a select would wait for
 // each other).

@@ -102,6 +102,18 @@ def test_zero_and_tiny_scales(T):
     run("int8", T, 1024, 200, out=torch.float32, seed=T, zero_scales=True)
 
 
+@pytest.mark.parametrize("fmt,K", [("int8", 128), ("int8", 640), ("int8", 8192), ("int8", 8320), ("int8", 16512),
+                                   ("bf16", 392), ("bf16", 8200)])
+@pytest.mark.parametrize("T,N", [(70, 100), (300, 2050), (449, 1441)])
+def test_small_tiles(fmt, K, T, N):
+    """Rows of one group to more than two fills of the scales; one workgroup per tile row to more than the card has."""
+    run(fmt, T, K, N, out=torch.float32, seed=K)
+
+
+def test_small_tiles_zero_scales():
+    run("int8", 300, 1024, 2050, residual=True, seed=3, zero_scales=True)
+
+
 @pytest.mark.parametrize("fmt,T,N,K", [("int8", 2050, 2100, 640), ("bf16", 2050, 2100, 648), ("int8", 600, 4097, 2048),
                                        ("bf16", 1000, 1025, 512), ("int8", 1000, 513, 1024)])
 def test_large(fmt, T, N, K):
