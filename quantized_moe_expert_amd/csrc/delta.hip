@@ -1097,21 +1097,26 @@ __global__ __launch_bounds__(512) void delta_scan_kernel(DeltaArgs a, const uint
     }
 }
 
-constexpr int SPLIT_TILES = 512;
+constexpr int SPLIT_TILES = 256;
 
 template <int DK>
 hipError_t launch_chunks(const DeltaArgs &a, void *ws, hipStream_t s) {
     if (a.T > 0) {
         const int64_t chunks = a.T / CH + a.n_seq;
         uint8_t *units = static_cast<uint8_t *>(ws);
-        // two heads of a key head together where that leaves enough workgroups
-        if (a.hv / a.hk % 2 == 0 && chunks * a.hv >= 2048)
+        // Two heads of a key head together where that leaves enough workgroups.
+        // Measured (whole calls, us, one head / two): k_dim 128, 792 chunks and
+        // heads 110.6 / 113.8, 1056 119.3 / 115.1, 1632 97.5 / 93.2; k_dim 64 (less
+        // to share): 2560 66.1 / 68.1, 4160 160 / 161, 8448 195 / 190.
+        if (a.hv / a.hk % 2 == 0 && chunks * a.hv >= (DK == 128 ? 1024 : 4096))
             hipLaunchKernelGGL((delta_prep_kernel<DK, 2>), dim3((unsigned)(chunks * (a.hv / 2))), dim3(256), 0, s, a, units);
         else
             hipLaunchKernelGGL((delta_prep_kernel<DK, 1>), dim3((unsigned)(chunks * a.hv)), dim3(256), 0, s, a, units);
     }
-    // Workgroups of 16 columns while they fill the 256 compute units not much
-    // more than once; else of 64.
+    // Workgroups of 16 columns while there are no more than compute units (a unit
+    // holds one); else of 64.  Measured (whole calls, us, 16 / 64): 256 tiles of 16
+    // columns, k_dim 128: 4096 tokens 214 / 270; 512: 2 x 1024 121 / 92; k_dim 64,
+    // 256: 8 x 256 26.3 / 28.5; 512: 16 x 256 42.7 / 34.3.
     const int64_t tiles = (int64_t)a.n_seq * a.hv * (a.dv / 16);
     const bool split_rows = tiles <= SPLIT_TILES;
     const int64_t groups = (int64_t)a.n_seq * a.hk, per = a.hv / a.hk * (a.dv / (split_rows ? 16 : 64));

@@ -159,6 +159,25 @@ def test_many_chunks(dk, dv):
     run("prefill", lens, 4, 16, dk, dv, True, seed=dk)
 
 
+@pytest.mark.parametrize("dk,dv", [(64, 128), (128, 128)])
+@pytest.mark.parametrize("extra", [0, 1])
+def test_chunks_about_the_paired_heads(dk, dv, extra):
+    """Just below and at the 1024 or 4096 chunks and heads from which two heads
+    of a key head share their preparation; the scan at and above 256 tiles of 16
+    columns."""
+    limit = 1024 if dk == 128 else 4096
+    hv = 32
+    lens = [limit // hv // 2 * 64 - 64, 63, 1 + 64 * extra]
+    lens[0] -= 64 * (sum(lens) // 64 + len(lens) - limit // hv - extra + 1)
+    assert (sum(lens) // 64 + len(lens)) * hv == limit + (extra - 1) * hv
+    run("prefill", lens, 16, hv, dk, dv, False, seed=dk + extra)
+
+
+@pytest.mark.parametrize("n", [16, 17])
+def test_columns_about_the_shared_rows(n):
+    run("prefill", [130] * n, 2, 4, 64, 64, True, seed=n)
+
+
 @pytest.mark.parametrize("kind", KINDS)
 @pytest.mark.parametrize("name,change", [
     ("no decay", dict(g=lambda g: g * 0)), ("full decay", dict(g=lambda g: g * 0 - 200)),
