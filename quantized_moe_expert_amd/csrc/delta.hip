@@ -144,9 +144,10 @@ hipError_t launch_decode(const DeltaArgs &a, hipStream_t s) {
 //
 // Operands are f16: k, q rows, T', P rows and the columns of S, X, U are
 // scaled by a power of two each, taken off again in fp32 (so f16's range
-// limits none of them).  Products that reach the state take a second f16 with
-// the remainder of each operand (22 bits; k needs none, its 8 bits fit), those
-// that reach only o take one (12 bits against o's 8).  Sums are fp32.  G is
+// limits none of them).  All but k and q, whose 8 bits fit, have a second f16
+// with the remainder (22 bits; the product of two remainders is left out).
+// With one f16 the error of o was 2^-13 of the state, 1.1e-3 of o's norm in bf16
+// roundings that fell to the other side.  Sums are fp32.  G is
 // summed in double: e^{G_i - G_j} of neighbours is then right behind a strong
 // decay.
 //
@@ -159,10 +160,11 @@ typedef __attribute__((__vector_size__(4 * sizeof(float)))) float f32x4_t;
 typedef _Float16 f16x2_t __attribute__((ext_vector_type(2)));
 
 constexpr int CH = 64;
-// Per (chunk, head): 18 operands of 1 KB (T' first f16: 6, remainder: 6, P: 6;
-// row tile 0: inner tiles 0-1; 1: 0-1; 2: 0-1, 2-3; 3: 0-1, 2-3), then vectors
-// of 64 floats, then e^{G_63}.
-constexpr int UNIT = 20480, UNIT_VEC = 18432;
+// Per (chunk, head): 24 operands of 1 KB (T' first f16: 6, remainder: 6, P the
+// same; row tile 0: inner tiles 0-1; 1: 0-1; 2: 0-1, 2-3; 3: 0-1, 2-3), then
+// vectors of 64 floats, then e^{G_63}.
+constexpr int OPS = 24;
+constexpr int UNIT = 26624, UNIT_VEC = OPS * 1024;
 enum { V_A, V_B, V_C, V_T, V_P, V_SK, V_SQ, V_COUNT };
 constexpr int UNIT_GAMMA = UNIT_VEC + V_COUNT * CH * 4;
 __device__ __forceinline__ constexpr int frag_index(int it, int ks) { return it < 2 ? it : 2 * it - 2 + ks; }
@@ -240,9 +242,10 @@ __device__ __forceinline__ float exp_diff(double d) {
 // and their products, are read and formed once for them).  Bound by the vector
 // work: about 1500 instructions a wave and chunk with one head, 80% of the
 // vector units' time.  Measured: 16384 tokens, 32 heads of 128 x 128 on 16 key
-// heads: 103 us with two heads (1.7 TB/s of the 173 MB it writes), 122 us with
-// one; with the tiles of A and P on one wave each (up to eight a wave) 128 us;
-// with a row's load waiting for the one before it 171 us.
+// heads: 108 us with two heads (2.0 TB/s of the 216 MB it writes).  Without P's
+// remainders 103 us, and then 122 us with one head, 128 us with the tiles of A and
+// P on one wave each (up to eight a wave), 171 us with a row's load waiting for the
+// one before it.
 template <int DK, int HP>
 __global__ __launch_bounds__(256) void delta_prep_kernel(DeltaArgs a, uint8_t *__restrict__ ws) {
     constexpr int LDA = 68, PL = DK / 16;  // elements per lane of a row's 16 lanes
@@ -418,14 +421,12 @@ __global__ __launch_bounds__(256) void delta_prep_kernel(DeltaArgs a, uint8_t *_
 #pragma unroll
             for (int ks = 0; ks < 2; ++ks)
                 if (ks <= w / 2) {
-                    u32x4_t f;
-#pragma unroll
-                    for (int t = 0; t < 2; ++t) {
-                        const f32x4_t p = P[2 * ks + t];
-                        f[2 * t] = f16_pair(p[0] * sc.sc, p[1] * sc.sc);
-                        f[2 * t + 1] = f16_pair(p[2] * sc.sc, p[3] * sc.sc);
-                    }
-                    *reinterpret_cast<u32x4_t *>(unit + (12 + (w < 2 ? w : 2 * w - 2 + ks)) * 1024 + lane * 16) = f;
+                    u32x4_t f, r;
+                    split(P[2 * ks], sc.sc, f, r, 0);
+                    split(P[2 * ks + 1], sc.sc, f, r, 1);
+                    const int at = w < 2 ? w : 2 * w - 2 + ks;
+                    *reinterpret_cast<u32x4_t *>(unit + (12 + at) * 1024 + lane * 16) = f;
+                    *reinterpret_cast<u32x4_t *>(unit + (18 + at) * 1024 + lane * 16) = r;
                 }
         }
         __syncthreads();  // s_A is whole, k and q are used up
@@ -525,27 +526,31 @@ __global__ __launch_bounds__(256) void delta_prep_kernel(DeltaArgs a, uint8_t *_
 // chunk to LDS meanwhile: k and q as f16 rows, k transposed, and the operands
 // of delta_prep_kernel.
 //   SPLIT false: 64 columns per workgroup, each state wave has 16 of them and
-//     works alone.  A chunk of a 128 x 128 head takes 4.4 us: about 600 vector
+//     works alone.  A chunk of a 128 x 128 head takes 4.6 us: about 600 vector
 //     instructions on each of the 8 waves (half of the vector units' time) and
-//     the products (18% of the matrix units').
+//     the products (a fifth of the matrix units').
 //   SPLIT true: 16 columns per workgroup, the state waves share their rows (of
 //     the state and of the chunk) and hand each other S, X and U through LDS:
-//     a shorter chain (3.0 us a chunk, a third of it the last stage), more LDS
+//     a shorter chain (3.2 us a chunk, a third of it the last stage), more LDS
 //     traffic per column.  For few columns in all.
-// Measured: one prompt of 8192 tokens, 32 heads of 128 x 128: 385 us with SPLIT,
-// 540 us without; with one state wave of 512 registers and three others 440 us.
-// 8 prompts of 2048: 284 us without SPLIT.
+// Measured: one prompt of 8192 tokens, 32 heads of 128 x 128: 410 us with SPLIT;
+// 8 prompts of 2048: 296 us without.  (With one f16 for what only o sees 385 and
+// 284 us, and then 540 us for the first without SPLIT, 440 us with one state wave
+// of 512 registers and three others.)
 template <int DK, bool SPLIT>
 __global__ __launch_bounds__(512) void delta_scan_kernel(DeltaArgs a, const uint8_t *__restrict__ ws) {
     constexpr int COLS = SPLIT ? 16 : 64;
     constexpr int NT = DK / 16, NQ = DK / 32;
     constexpr int ROWS = CH * DK * 2;                              // bytes of k, of q, of k transposed
-    constexpr int FR = 3 * ROWS, VEC = FR + 18 * 1024, BUF = VEC + V_COUNT * CH * 4 + 16;
+    constexpr int FR = 3 * ROWS, VEC = FR + OPS * 1024, BUF = VEC + V_COUNT * CH * 4 + 16;
     __shared__ __align__(16) uint8_t s_buf[2][BUF];
-    // SPLIT: S as right operands (f16 and remainders), X and U tiles, largest
+    // SPLIT: S as right operands (f16 and remainders; their place takes the U
+    // tiles, which are written behind the barrier after S's last read and read
+    // before the one that the next S is written behind), X tiles, largest
     // magnitude of each column of S in each wave's rows
     __shared__ __align__(16) uint8_t s_S[SPLIT ? 2 * NQ * 1024 : 16];
-    __shared__ f32x4_t s_X[SPLIT ? 4 * 64 : 1], s_U[SPLIT ? 4 * 64 : 1];
+    __shared__ f32x4_t s_X[SPLIT ? 4 * 64 : 1];
+    f32x4_t *const s_U = reinterpret_cast<f32x4_t *>(s_S);
     __shared__ float s_max[SPLIT ? 64 : 1];
     const int tid = threadIdx.x, lane = tid & 63, m = lane & 15, g4 = lane >> 4;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -569,10 +574,9 @@ __global__ __launch_bounds__(512) void delta_scan_kernel(DeltaArgs a, const uint
 
     if (wave >= 4) {
         // ---- bringing chunks to LDS.  Items of a thread: KI pairs of rows x 8
-        // of k, QN rows x 8 of q, FN 16-byte pieces of operands (the last only
-        // for half of the threads), VN floats
+        // of k, QN rows x 8 of q, FN 16-byte pieces of operands, VN floats
         const int p = tid - 256;
-        constexpr int KI = 32 * (DK / 8) / 256, QN = CH * (DK / 8) / 256, FN = 5, VN = 2;
+        constexpr int KI = 32 * (DK / 8) / 256, QN = CH * (DK / 8) / 256, FN = OPS * 64 / 256, VN = 2;
         u32x4_t k_reg[KI][2], q_reg[QN], f_reg[FN];
         float v_reg[VN], k_sc[KI][2], q_sc[QN];
         // byte offsets from the chunk's first row (64 rows of at most 2^22
@@ -618,7 +622,7 @@ __global__ __launch_bounds__(512) void delta_scan_kernel(DeltaArgs a, const uint
             const uint8_t *unit = units + c * unit_step;
 #pragma unroll
             for (int it = 0; it < FN; ++it)
-                if (it < 4 || p < 128) f_reg[it] = *reinterpret_cast<const u32x4_t *>(unit + (uint32_t)((it * 256 + p) * 16));
+                f_reg[it] = *reinterpret_cast<const u32x4_t *>(unit + (uint32_t)((it * 256 + p) * 16));
 #pragma unroll
             for (int it = 0; it < VN; ++it)
                 if (it * 256 + p <= V_COUNT * CH)
@@ -665,7 +669,7 @@ __global__ __launch_bounds__(512) void delta_scan_kernel(DeltaArgs a, const uint
             uint8_t *buf = s_buf[c & 1];
 #pragma unroll
             for (int it = 0; it < FN; ++it)
-                if (it < 4 || p < 128) *reinterpret_cast<u32x4_t *>(buf + FR + (it * 256 + p) * 16) = f_reg[it];
+                *reinterpret_cast<u32x4_t *>(buf + FR + (it * 256 + p) * 16) = f_reg[it];
 #pragma unroll
             for (int it = 0; it < VN; ++it)
                 if (it * 256 + p <= V_COUNT * CH) *reinterpret_cast<float *>(buf + VEC + (it * 256 + p) * 4) = v_reg[it];
@@ -786,24 +790,27 @@ __global__ __launch_bounds__(512) void delta_scan_kernel(DeltaArgs a, const uint
                 sh[q] = *reinterpret_cast<const u32x4_t *>(s_S + q * 1024 + lane * 16);
                 sl[q] = *reinterpret_cast<const u32x4_t *>(s_S + (NQ + q) * 1024 + lane * 16);
             }
-            f32x4_t kh = zero4, kl = zero4, QS = zero4;
+            f32x4_t kh = zero4, kl = zero4, QS = zero4, ql = zero4;
 #pragma unroll
             for (int q = 0; q < NQ; ++q) {
                 kh = mfma_f16(fk[q], sh[q], kh);
                 kl = mfma_f16(fk[q], sl[q], kl);
                 QS = mfma_f16(fq[q], sh[q], QS);
+                ql = mfma_f16(fq[q], sl[q], ql);
             }
+            QS += ql;
             f32x4_t X[4];
 #pragma unroll
             for (int e = 0; e < 4; ++e) X[0][e] = fmaf(-(kh[e] + kl[e]), fa[e] * s_off, v[e]);
             s_X[64 * w + lane] = X[0];
-            u32x4_t th[2], tl[2], tp[2];
+            u32x4_t th[2], tl[2], tp[2], tr[2];
 #pragma unroll
             for (int x = 0; x < 2; ++x)
                 if (x <= last_x) {
                     th[x] = frag(op0 + x * 1024);
                     tl[x] = frag(op0 + (6 + x) * 1024);
                     tp[x] = frag(op0 + (12 + x) * 1024);
+                    tr[x] = frag(op0 + (18 + x) * 1024);
                 }
             lds_barrier();
             // U = T' X of the wave's tokens
@@ -875,19 +882,18 @@ __global__ __launch_bounds__(512) void delta_scan_kernel(DeltaArgs a, const uint
             // O = diag(b) Q S + P U of the wave's tokens
             const RowScale us = unit_scale(groups_max(mx));
             const float u_off = exp2i(-us.s);
-            f32x4_t o = zero4;
+            f32x4_t o = zero4, ol = zero4, om = zero4;
 #pragma unroll
             for (int x = 0; x < 2; ++x)
                 if (x <= last_x) {
-                    u32x4_t f;
-#pragma unroll
-                    for (int t = 0; t < 2; ++t) {
-                        const f32x4_t u = U[2 * x + t];
-                        f[2 * t] = f16_pair(u[0] * us.sc, u[1] * us.sc);
-                        f[2 * t + 1] = f16_pair(u[2] * us.sc, u[3] * us.sc);
-                    }
+                    u32x4_t f, r;
+                    split(U[2 * x], us.sc, f, r, 0);
+                    split(U[2 * x + 1], us.sc, f, r, 1);
+                    om = mfma_f16(tr[x], f, om);
+                    ol = mfma_f16(tp[x], r, ol);
                     o = mfma_f16(tp[x], f, o);
                 }
+            o += ol + om;
             const int64_t r0 = t0 + (int64_t)c * CH;
             const int len = t1 - r0 < CH ? (int)(t1 - r0) : CH;
 #pragma unroll
@@ -978,6 +984,10 @@ __global__ __launch_bounds__(512) void delta_scan_kernel(DeltaArgs a, const uint
                 for (int t = 0; t < 4; ++t) X[t] = mfma_f16(fk[t], sl[q], X[t]);
 #pragma unroll
                 for (int t = 0; t < 4; ++t) X[t] = mfma_f16(fk[t], sh[q], X[t]);
+#pragma unroll
+                for (int t = 0; t < 4; ++t) QS[t] = mfma_f16(q_frag(t, q), sl[q], QS[t]);
+#pragma unroll
+                for (int t = 0; t < 4; ++t) QS[t] = mfma_f16(q_frag(t, q), sh[q], QS[t]);
             }
             mx = 0.f;
 #pragma unroll
@@ -993,10 +1003,6 @@ __global__ __launch_bounds__(512) void delta_scan_kernel(DeltaArgs a, const uint
             u32x4_t xh[2], xl[2];
 #pragma unroll
             for (int t = 0; t < 4; ++t) split(X[t], xs.sc, xh[t / 2], xl[t / 2], t & 1);
-#pragma unroll
-            for (int q = 0; q < NQ; ++q)
-#pragma unroll
-                for (int t = 0; t < 4; ++t) QS[t] = mfma_f16(q_frag(t, q), sh[q], QS[t]);
             f32x4_t U[4], W[4];
 #pragma unroll
             for (int t = 0; t < 4; ++t) U[t] = zero4;
@@ -1023,7 +1029,9 @@ __global__ __launch_bounds__(512) void delta_scan_kernel(DeltaArgs a, const uint
                 mx = max_abs(U[t], mx);
                 mw = max_abs(W[t], mw);
             }
-            // S = e^{G_63} S + K^T W first: the next chunk waits for it
+            // S = e^{G_63} S + K^T W first: the next chunk waits for it.  (Nothing is
+            // moved over this line: else 8 registers are spilled in the loop.)
+            __builtin_amdgcn_sched_barrier(0);
             const RowScale wsc = unit_scale(groups_max(mw));
             const float w_off = exp2i(-wsc.s) * x_off;
             u32x4_t wh[2], wl[2];
@@ -1051,20 +1059,21 @@ __global__ __launch_bounds__(512) void delta_scan_kernel(DeltaArgs a, const uint
             // O = diag(b) Q S + P U
             const RowScale us = unit_scale(groups_max(mx));
             const float u_off = exp2i(-us.s) * x_off;
-            u32x4_t uh[2];
+            u32x4_t uh[2], ul[2];
 #pragma unroll
-            for (int t = 0; t < 4; ++t)
-#pragma unroll
-                for (int e = 0; e < 4; e += 2)
-                    uh[t / 2][2 * (t & 1) + e / 2] = f16_pair(U[t][e] * us.sc, U[t][e + 1] * us.sc);
+            for (int t = 0; t < 4; ++t) split(U[t], us.sc, uh[t / 2], ul[t / 2], t & 1);
             f32x4_t O[4];
 #pragma unroll
             for (int t = 0; t < 4; ++t) O[t] = zero4;
 #pragma unroll
-            for (int x = 0; x < 2; ++x)
+            for (int x = 0; x < 2; ++x) {
 #pragma unroll
-                for (int t = 2 * x; t < 4; ++t)
-                    O[t] = mfma_f16(op(2, t, x), uh[x], O[t]);
+                for (int t = 2 * x; t < 4; ++t) O[t] = mfma_f16(op(3, t, x), uh[x], O[t]);
+#pragma unroll
+                for (int t = 2 * x; t < 4; ++t) O[t] = mfma_f16(op(2, t, x), ul[x], O[t]);
+#pragma unroll
+                for (int t = 2 * x; t < 4; ++t) O[t] = mfma_f16(op(2, t, x), uh[x], O[t]);
+            }
 #pragma unroll
             for (int t = 0; t < 4; ++t) {
                 const f32x4_t fb = vec4(V_B, t), fp = vec4(V_P, t);
@@ -1115,8 +1124,8 @@ hipError_t launch_chunks(const DeltaArgs &a, void *ws, hipStream_t s) {
     }
     // Workgroups of 16 columns while there are no more than compute units (a unit
     // holds one); else of 64.  Measured (whole calls, us, 16 / 64): 256 tiles of 16
-    // columns, k_dim 128: 4096 tokens 214 / 270; 512: 2 x 1024 121 / 92; k_dim 64,
-    // 256: 8 x 256 26.3 / 28.5; 512: 16 x 256 42.7 / 34.3.
+    // columns, k_dim 128: 4096 tokens 225 / 260; 512: 2 x 1024 119 / 87; k_dim 64,
+    // 256: 8 x 256 28.2 / 30.3; 512: 16 x 256 44.7 / 36.3.
     const int64_t tiles = (int64_t)a.n_seq * a.hv * (a.dv / 16);
     const bool split_rows = tiles <= SPLIT_TILES;
     const int64_t groups = (int64_t)a.n_seq * a.hk, per = a.hv / a.hk * (a.dv / (split_rows ? 16 : 64));

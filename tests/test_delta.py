@@ -401,3 +401,41 @@ def test_refusals():
     if m.delta_workspace_size(5, 1, 2, 4, 64, 64):
         with pytest.raises(m.MoeQ4Error):
             m.moe_q4_delta_prefill(**args)
+
+
+@pytest.mark.parametrize("n_seq", [1, 9])
+@pytest.mark.parametrize("L", [1, 2, 17, 63, 64, 65, 129])
+@pytest.mark.parametrize("dk,dv", [(64, 64), (128, 128)])
+def test_prefill_operands_have_22_bits(dk, dv, L, n_seq):
+    """States and outputs as near as operands of two f16 make them, on both
+    layouts of the scan (few columns and many).
+
+    A chunk takes the state through three products after one another (K S,
+    T' X, K^T W).  Each has operands of 22 bits (2^-22 for either, of what is
+    multiplied) and fp32 sums of 64 or k_dim + 64 terms, whose roundings are
+    taken as independent (14 x 2^-24 < 2^-20): 3 (2^-21 + 2^-20) < 5 x 2^-20 of
+    M, and the chunks' errors add.  An output's two products (with q.k_j of
+    random directions, whose norm over a chunk is below 2) add at most
+    2 x 3 x 2^-20 of scale |q| M before it is rounded, by at most half a bf16
+    step.  (The file's own bound allows the output's operands 12 bits.)  The
+    same algorithm in fp32 on the CPU is within 0.05 of either bound; without
+    the remainder of one operand it is, at the worst of these lengths, 13 (S),
+    52 (T'), 62 (X) and 75 (W) times the state's and, where only the output
+    sees it, 5 times the output's (S in Q S, P, U).
+    """
+    lens = [L] * n_seq
+    q, k, v, g, beta, s0, start = inputs(lens, 4, 8, dk, dv, True, seed=L)
+    scale = dk ** -0.5
+    o = torch.full((sum(lens), 8, dv), float("nan"), dtype=torch.bfloat16, device="cuda")
+    s1 = torch.full_like(s0, float("nan"))
+    call("prefill", q, k, v, g, beta, start, None, s0, s1, o, scale, True)
+    torch.cuda.synchronize()
+    want_o, want_s, big, qn = rule(q, k, v, g, beta, lens, s0, scale, True)
+    chunks = (L + 63) // 64
+    off_s = (s1.cpu().double() - want_s).norm(dim=2).amax(-1) / (5 * chunks * 2.0 ** -20 * big)
+    half = torch.ldexp(torch.ones_like(want_o), torch.frexp(want_o).exponent - 9)
+    tol = (5 * chunks + 6) * 2.0 ** -20 * scale * qn.norm(dim=-1) * big.repeat_interleave(L, 0)
+    off_o = ((o.cpu().double() - want_o).abs() - half) / tol[..., None]
+    print(f"{n_seq} x {L}, {dk}x{dv}: largest error / bound: o {float(off_o.max()):.4f}, state {float(off_s.max()):.4f}",
+          flush=True)
+    assert float(off_o.max()) <= 1 and float(off_s.max()) <= 1
