@@ -62,7 +62,9 @@ __device__ __forceinline__ u32x4_t codes_bf16(uint32_t lo, uint32_t hi, float f)
 
 __device__ __forceinline__ float activate(float z, int act) {
     if (act == 1) return z / (1.0f + expf(-z));
-    if (act == 2) return 0.5f * z * (1.0f + erff(z * 0.70710678118654752f));
+    // 1 + erf(x) = erfc(-x), which keeps its digits where erf nears -1 (4096 tokens,
+    // 2048 -> 8192: 220 us, 212 with erf)
+    if (act == 2) return 0.5f * z * erfcf(z * -0.70710678118654752f);
     return z;
 }
 

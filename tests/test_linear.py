@@ -254,3 +254,28 @@ def test_refusals():
     with pytest.raises(m.MoeQ4Error):
         m.moe_q4_linear(x, w, y, 7)
     m.moe_q4_linear(x[:0], w, y[:0])
+
+
+@pytest.mark.parametrize("T,N", [(1, 300), (40, 70), (100, 70), (1100, 2400)])
+@pytest.mark.parametrize("out", [torch.bfloat16, torch.float32])
+def test_gelu_keeps_its_relative_accuracy(T, N, out):
+    """z (1 + erf(z / sqrt 2)) / 2 for z in [-12, 9], far into the tail where
+    the parenthesis cancels.  One input per output, so that z is exact; the
+    argument of the error function takes two roundings (2^-24 each), which its
+    slope makes at most 2 z^2 2^-24 of the value, the function itself up to 16
+    steps (32 x 2^-24), the products 8 x 2^-24."""
+    gen = torch.Generator(device="cuda").manual_seed(T)
+    x, w = torch.zeros(T, 8, device="cuda"), torch.zeros(N, 8, device="cuda")
+    x[:, 5] = torch.rand(T, generator=gen, device="cuda") * 6 - 4
+    w[:, 5] = torch.rand(N, generator=gen, device="cuda") * 2 + 1
+    x[0, 5] = -4.0
+    x, w = x.bfloat16(), w.bfloat16()
+    y = torch.empty(T, N, dtype=out, device="cuda")
+    m.moe_q4_linear(x, m.linear_struct(w), y, m.ACT_GELU)
+    torch.cuda.synchronize()
+    z = (x[:, 5:6].double() * w[None, :, 5].double()).cpu()
+    want = z * torch.special.erfc(-z * 0.5 ** 0.5) / 2
+    rel = (2 * z * z + 40) * 2.0 ** -24 + (2.0 ** -8 if out == torch.bfloat16 else 2.0 ** -24)
+    worst = float(((y.cpu().double() - want).abs() / (rel * want.abs() + 1e-44)).max())
+    print(f"gelu T={T} N={N} {out}: largest error / tolerance {worst:.3f}, z from {float(z.min()):.2f}", flush=True)
+    assert worst <= 1
