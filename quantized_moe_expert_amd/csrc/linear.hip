@@ -300,6 +300,7 @@ struct Tile {
     // a group then
     static constexpr bool OWN = INT8 && WM == 1;
     static_assert(!OWN || WK == 4, "a stage is a group");
+    static_assert(!INT8 || OWN || WK == 1, "a stage is a quarter of a group");
     static_assert(BM * 4 * WK % THREADS == 0 && BN * 2 * WK % THREADS == 0, "whole chunks");
 };
 
@@ -407,11 +408,11 @@ __global__ __launch_bounds__((Tile<INT8, BM, BN, WM, WN, WK>::THREADS)) void lin
             asm volatile("" : "+v"(scale8[i]));
         }
     };
-    // codes of stage `step` (each thread's own) to bf16; a stage of WK = 4 is
-    // a group, of WK = 1 a quarter
+    // codes of stage `step` (each thread's own) to bf16; a stage is a quarter
+    // of a group
     auto convert = [&](int step, int u) {
-        int group = WK == 4 ? step : step >> 2;
-        if ((group & 7) == 0 && (WK == 4 || (step & 3) == 0)) load_scales(group);
+        int group = step >> 2;
+        if ((group & 7) == 0 && (step & 3) == 0) load_scales(group);
         group = group < groups ? group : groups - 1;  // behind the row: the last scale again
         const int pair = group >> 1 & 3;
 #pragma unroll
@@ -613,8 +614,7 @@ __global__ __launch_bounds__((Tile<INT8, BM, BN, WM, WN, WK>::THREADS)) void lin
                 if (INT8) {
                     WAIT_VM((RING - 2) * C::OPS);
                     convert(step + 1, (u + 1) % RING);
-                    // a group is four blocks
-                    if (WK == 4 ? step > 0 : u == 0 && step > 0) rescale(u);
+                    if (u == 0 && step > 0) rescale(u);  // a group is four stages
                 }
                 multiply(f0);
                 WAIT_VM_LDS((RING - 2) * C::OPS);
