@@ -279,3 +279,86 @@ def test_gelu_keeps_its_relative_accuracy(T, N, out):
     worst = float(((y.cpu().double() - want).abs() / (rel * want.abs() + 1e-44)).max())
     print(f"gelu T={T} N={N} {out}: largest error / tolerance {worst:.3f}, z from {float(z.min()):.2f}", flush=True)
     assert worst <= 1
+
+
+# (T, N) of the three large tiles: 128 x 128 (165 of them), 128 x 256 (153), 256 x 256 (400)
+LARGE = [(600, 4097), (2050, 2100), (5000, 5100)]
+
+
+def mixed_scales(N, K, gen):
+    """Scales of either sign over 2^-24 .. 2^5, a third of them 0 (or -0), whole
+    rows of 0 and of the smallest f16 among them."""
+    s = torch.exp2(torch.randint(-24, 6, (N, K // 128), generator=gen, device="cuda").float())
+    s = s * (1 + torch.rand(s.shape, generator=gen, device="cuda")) * torch.randn(s.shape, generator=gen, device="cuda").sign()
+    s[torch.rand(s.shape, generator=gen, device="cuda") < 0.33] = 0
+    s[3], s[5], s[-1, -1] = 0, 2.0 ** -24, -(2.0 ** -24)
+    s[7, 0] = -0.0
+    return s.half()
+
+
+@pytest.mark.parametrize("T,N", LARGE)
+@pytest.mark.parametrize("fmt,K", [("int8", 128), ("int8", 256), ("int8", 1280), ("bf16", 8), ("bf16", 264), ("bf16", 1000)])
+def test_large_tiles(fmt, K, T, N):
+    """Every large tile with float outputs at odd offsets of wider rows, x and
+    residual rows in wider ones, and scales of any size and sign.  (A change of
+    a group's unit takes up to six roundings of the sums: K / 16 in all.)"""
+    gen = torch.Generator(device="cuda").manual_seed(K)
+    q, s, w = weights(fmt, N, K, gen)
+    if fmt == "int8":
+        s = mixed_scales(N, K, gen)
+        w = q.double() * s.double().repeat_interleave(128, 1)
+    x = torch.randn(T, K + 24, generator=gen, device="cuda").bfloat16()[:, 8:8 + K]
+    b = torch.randn(N, generator=gen, device="cuda")
+    r = torch.randn(T, N + 3, generator=gen, device="cuda").bfloat16()[:, 1:1 + N]
+    whole = torch.full((T, N + 6), 5.0, device="cuda")
+    y = whole[:, 3:3 + N]
+    m.moe_q4_linear(x, m.linear_struct(q, s, b), y, m.ACT_NONE, r)
+    torch.cuda.synchronize()
+    ref = expect(x, w, b, 0, r)
+    parts = x.double().abs() @ w.abs().t().contiguous() + b.double().abs() + r.double().abs()
+    tol = 2.0 ** -24 * (ref.abs() + (K + K / 16 + 8) * parts)
+    worst = float(((y.double() - ref).abs() / tol).max())
+    print(f"{fmt} T={T} K={K} N={N}: largest error / tolerance {worst:.3f}", flush=True)
+    assert torch.isfinite(y).all() and worst <= 1
+    assert (whole[:, :3] == 5).all() and (whole[:, 3 + N:] == 5).all()
+
+
+@pytest.mark.parametrize("T,N", LARGE)
+@pytest.mark.parametrize("fmt,K", [("int8", 384), ("bf16", 392)])
+@pytest.mark.parametrize("act", [0, 1, 2])
+def test_large_tiles_in_place(fmt, K, T, N, act):
+    gen = torch.Generator(device="cuda").manual_seed(act)
+    q, s, w = weights(fmt, N, K, gen, zero_scales=True)
+    x = torch.randn(T, K, generator=gen, device="cuda").bfloat16()
+    b = torch.randn(N, generator=gen, device="cuda")
+    y = torch.randn(T, N, generator=gen, device="cuda").bfloat16()
+    r = y.clone()
+    m.moe_q4_linear(x, m.linear_struct(q, s, b), y, act, y)
+    torch.cuda.synchronize()
+    check(y, x, w, b, act, r, f"in place {fmt} T={T} N={N} act={act}")
+
+
+@pytest.mark.parametrize("T,N", LARGE)
+@pytest.mark.parametrize("fmt,K", [("int8", 384), ("bf16", 392)])
+def test_large_tiles_keep_infinities_and_nan_apart(fmt, K, T, N):
+    """Tokens with an infinity or a NaN, and bf16 weight rows with one, change
+    no other outputs; the same input gives the same bits."""
+    gen = torch.Generator(device="cuda").manual_seed(K)
+    q, s, _ = weights(fmt, N, K, gen)
+    x = torch.randn(T, K, generator=gen, device="cuda").bfloat16()
+    w = m.linear_struct(q, s)
+    ref, again, y = (torch.empty(T, N, device="cuda") for _ in range(3))
+    m.moe_q4_linear(x, w, ref)
+    m.moe_q4_linear(x, w, again)
+    bad = torch.zeros(T, N, dtype=torch.bool, device="cuda")
+    for t in (0, T // 2, T - 1):
+        x[t, K - 1], x[t, 100] = float("inf"), float("nan")
+        bad[t] = True
+    if fmt == "bf16":
+        for n in (1, N - 1):
+            q[n, K - 1] = float("nan")
+            bad[:, n] = True
+    m.moe_q4_linear(x, w, y)
+    torch.cuda.synchronize()
+    assert torch.equal(ref, again)
+    assert torch.isnan(y[bad]).all() and torch.equal(y[~bad], ref[~bad])
