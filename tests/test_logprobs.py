@@ -241,3 +241,35 @@ def test_refusals():
     with pytest.raises(m.MoeQ4Error):
         m.moe_q4_logprobs(l, tok, f, f, i, None, ws)
     m.moe_q4_logprobs(l[:0], tok[:0], f[:0], f[:0], i[:0], top[:0], ws)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("V", [262144 + 5, 2200000])
+def test_many_segments(dtype, V):
+    """Top lists of more keys than the joining workgroup holds at once (33 and
+    269 segments of 32 keys), and more segments than it has threads: ordinary
+    rows, few distinct values (ties across the segments), the largest all in the
+    last segments, all in the first, one left."""
+    l, tok = rows(5, V, "f32", 11)
+    l[1] = l[1].round()
+    l[2, -20000:] += 40
+    l[3, :9000] += 40
+    l[4] = -INF
+    l[4, V - 1] = 2.0
+    tok[2], tok[4] = V - 3, V - 1
+    check(l.bfloat16() if dtype == "bf16" else l, tok, 32, f"many segments {dtype} V={V}")
+
+
+@pytest.mark.parametrize("V", [300, 20001])
+def test_signalling_nan_counts_as_minus_infinity(V):
+    l, tok = rows(4, V, "bf16", 12)
+    want = l.clone()
+    want[:, 5::3] = -INF
+    bits = l.view(torch.int16)
+    bits[:, 5::3] = 0x7f81  # a NaN whose quiet bit is clear
+    bits[1, 5::3] = -0x7f  # 0xff81
+    for a, b in ((l, want), (bits, want)):
+        assert all(torch.equal(p, q) for p, q in zip(score(a, tok, 20), score(b, tok, 20)))
+    f = want.float()
+    f.view(torch.int32)[:, 5::3] = 0x7f800001
+    assert all(torch.equal(p, q) for p, q in zip(score(f, tok, 20), score(want.float(), tok, 20)))
