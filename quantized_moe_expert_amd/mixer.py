@@ -1,9 +1,15 @@
-"""Convenience wrapper: buffers for one gated delta rule mixer of the backbone.
+"""Convenience wrapper: buffers for a plain gated delta rule mixer.
 
-The half of a backbone layer that stands before the experts (MoeQ4Layer): the
-fused q | k | v projection, the gated delta rule and the output projection
-added to the stream.  Allocates the buffers and the workspace once (torch
-device memory) and calls the C ABI; the computation itself is the library's.
+A fused q | k | v projection, the gated delta rule and an output projection
+added to the stream, one after another.  Allocates the buffers and the
+workspace once (torch device memory) and calls the C ABI; the computation
+itself is the library's.
+
+This is the rule between its two linears and nothing else.  The backbone's own
+gated DeltaNet layers have more around it, which the library does not offer:
+a short causal convolution and SiLU behind the input projection, a gated norm
+before the output projection, and g and beta computed from the stream.  A layer
+with those makes the three calls itself, with its own steps between.
 """
 from __future__ import annotations
 
@@ -21,6 +27,10 @@ class DeltaMixer:
     from [v_heads, v_dim] back to the stream.  The structs' tensors are the
     caller's to keep.  q and k are normalised per head; scale 1 / sqrt(k_dim).
     ``mode``: "decode" (token by token) or "prefill" (chunks of 64 tokens).
+
+    The buffers are the mixer's, one set for all of its calls: a call must be
+    ordered after the one before, so that streams or threads that run at the
+    same time need a mixer each (they may share the weights).
     """
 
     def __init__(self, w_in, w_out, k_heads: int, v_heads: int, k_dim: int, v_dim: int, max_tokens: int,
@@ -43,8 +53,9 @@ class DeltaMixer:
 
     def forward(self, x, g, beta, seq_start, state_in, state_out, y, state_idx=None):
         """y (bf16 [T, hidden], may be x) = x + mixer(x).  g, beta, seq_start
-        and the states as moe_q4_delta_decode; every one of the T rows must
-        belong to a sequence."""
+        and the states as moe_q4_delta_decode.  Every one of the T rows must
+        belong to a sequence: one that only fills up the batch is a sequence of
+        its own whose ``state_idx`` is -1 (no state is read or written)."""
         T = x.shape[0]
         if T > self.max_tokens or seq_start.numel() - 1 > self.max_seqs:
             raise ValueError(f"{T} tokens of {seq_start.numel() - 1} sequences do not fit in the buffers")

@@ -183,3 +183,73 @@ def test_mixer_refusals():
     start = torch.tensor([0, 9], dtype=torch.int32, device="cuda")
     with pytest.raises(ValueError):
         mx.forward(x, torch.zeros(9, HV, device="cuda"), torch.zeros(9, HV, device="cuda"), start, None, None, x)
+
+
+@pytest.mark.parametrize("mode", ["prefill", "decode"])
+def test_mixer_rows_that_fill_up_the_batch(mode):
+    """A batch of a fixed size, captured, of which a part is in use: the other
+    rows are sequences without a state.  Outputs and states of those in use are
+    the bits of a call with them alone, and no other state changes."""
+    T, used = 6, 4
+    bb = Backbone(T, T, 2)
+    mixer = bb.mixers[mode]
+    gen = torch.Generator(device="cuda").manual_seed(5)
+    start = torch.arange(T + 1, dtype=torch.int32, device="cuda")
+    idx = torch.tensor([7, 2, 5, 0, -1, -1], dtype=torch.int32, device="cuda")
+    x, y = (torch.zeros(T, H, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    g, beta = torch.zeros(T, HV, device="cuda"), torch.zeros(T, HV, device="cuda")
+    states = torch.randn(8, HV, DK, DV, generator=gen, device="cuda") * 0.1
+    s0 = states.clone()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        mixer.forward(x, g, beta, start, states, states, y, idx)
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        mixer.forward(x, g, beta, start, states, states, y, idx)
+    states.copy_(s0)
+    eager = s0.clone()
+    for i in range(3):
+        x.copy_(torch.randn(T, H, generator=gen, device="cuda"))
+        x[used:] = float("nan")  # whatever the unused rows hold
+        gi, bi = gates(T, gen)
+        g.copy_(gi)
+        beta.copy_(bi)
+        graph.replay()
+        torch.cuda.synchronize()
+        want = torch.empty(used, H, dtype=torch.bfloat16, device="cuda")
+        mixer.forward(x[:used], g[:used], beta[:used], start[:used + 1], eager, eager, want, idx[:used])
+        torch.cuda.synchronize()
+        assert torch.equal(y[:used], want) and torch.equal(states, eager), i
+    for unnamed in (1, 3, 4, 6):
+        assert torch.equal(states[unnamed], s0[unnamed])
+    assert not torch.equal(states[7], s0[7])
+
+
+@pytest.mark.parametrize("mode", ["prefill", "decode"])
+def test_mixers_on_two_streams(mode):
+    """A mixer for each stream, with the same weights."""
+    lens = [70, 66] if mode == "prefill" else [1, 2]
+    T, B = sum(lens), len(lens)
+    bb = Backbone(T, B, 3)
+    win, wout = m.linear_struct(*bb.win), m.linear_struct(*bb.wout)
+    start = torch.tensor([sum(lens[:i]) for i in range(B + 1)], dtype=torch.int32, device="cuda")
+    jobs = []
+    for seed in (1, 2):
+        gen = torch.Generator(device="cuda").manual_seed(seed)
+        mixer = m.DeltaMixer(win, wout, HK, HV, DK, DV, T, B, mode)
+        x = torch.randn(T, H, generator=gen, device="cuda").bfloat16()
+        s0 = torch.randn(B, HV, DK, DV, generator=gen, device="cuda") * 0.1
+        args = (x, *gates(T, gen), start, s0)
+        s1, y = torch.empty_like(s0), torch.empty_like(x)
+        mixer.forward(*args, s1, y)
+        jobs.append((mixer, args, s1.clone(), y.clone(), s1, y, torch.cuda.Stream()))
+    torch.cuda.synchronize()
+    for _ in range(5):
+        for mixer, args, _, _, s1, y, stream in jobs:
+            with torch.cuda.stream(stream):
+                mixer.forward(*args, s1, y)
+    torch.cuda.synchronize()
+    for _, _, want_s, want_y, s1, y, _ in jobs:
+        assert torch.equal(s1, want_s) and torch.equal(y, want_y)
