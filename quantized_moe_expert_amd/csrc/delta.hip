@@ -1114,9 +1114,10 @@ hipError_t launch_chunks(const DeltaArgs &a, void *ws, hipStream_t s) {
         const int64_t chunks = a.T / CH + a.n_seq;
         uint8_t *units = static_cast<uint8_t *>(ws);
         // Two heads of a key head together where that leaves enough workgroups.
-        // Measured (whole calls, us, one head / two): k_dim 128, 792 chunks and
-        // heads 110.6 / 113.8, 1056 119.3 / 115.1, 1632 97.5 / 93.2; k_dim 64 (less
-        // to share): 2560 66.1 / 68.1, 4160 160 / 161, 8448 195 / 190.
+        // Measured (whole calls, us, one head / two, 32 heads): k_dim 128, 768 chunks
+        // and heads 94 / 96, 832 56.6 / 58.7, 1056 121 / 118, 8448 427 / 404; k_dim 64
+        // (less to share): 2112 78 / 78, 4160 334 / 335, 8448 of eight prompts
+        // 212 / 208, of one (its chain of chunks is the time) 704 / 715.
         if (a.hv / a.hk % 2 == 0 && chunks * a.hv >= (DK == 128 ? 1024 : 4096))
             hipLaunchKernelGGL((delta_prep_kernel<DK, 2>), dim3((unsigned)(chunks * (a.hv / 2))), dim3(256), 0, s, a, units);
         else
@@ -1125,7 +1126,11 @@ hipError_t launch_chunks(const DeltaArgs &a, void *ws, hipStream_t s) {
     // Workgroups of 16 columns while there are no more than compute units (a unit
     // holds one); else of 64.  Measured (whole calls, us, 16 / 64): 256 tiles of 16
     // columns, k_dim 128: 4096 tokens 225 / 260; 512: 2 x 1024 119 / 87; k_dim 64,
-    // 256: 8 x 256 28.2 / 30.3; 512: 16 x 256 44.7 / 36.3.
+    // 256: 8 x 256 28.2 / 30.3; 512: 16 x 256 44.7 / 36.3.  (The count is of all
+    // units.  The kernel keeps the workgroups of a sequence and key head on one XCD
+    // of 32 units, so with few such pairs and many columns for each they take turns
+    // there while other XCDs have none: 4096 tokens of 32 value heads on 16, 4, 2
+    // and 1 key heads take 223, 399, 758 and 1474 us.  Nothing here avoids that.)
     const int64_t tiles = (int64_t)a.n_seq * a.hv * (a.dv / 16);
     const bool split_rows = tiles <= SPLIT_TILES;
     const int64_t groups = (int64_t)a.n_seq * a.hk, per = a.hv / a.hk * (a.dv / (split_rows ? 16 : 64));

@@ -695,20 +695,29 @@ hipError_t launch_tile(const LinearArgs &a, hipStream_t s) {
     return hipGetLastError();
 }
 
-// Which kernel and tile.  Measured (us, int8 / bf16, MI355X):
-//   16 tokens, N = 12288, K = 2048: rows<1,1,8> 12.8 / 16.3, <1,2,8> 14.2 / 17.6, <1,4,4> 12.9 / 15.6;
-//   N = 2048, K = 4096: 9.3 / 10.3, 12.6 / 13.7, 19.5 / 21.7
-//   64 tokens, N = 2048, K = 4096: rows<2,1,4> 13.1 / 15.4, <2,2,4> 17.4 / 18.5, 64x32 tiles 19.8 / 12.9;
-//   N = 12288, K = 2048: <2,1,4> 32.4 / 36.2, <2,2,4> 24.5 / 29.4
-//   128 tokens, N = 2048, K = 4096: rows<2,2,4> 17.8 / 20.3, 64x32 19.8 / 13.1, 64x64 24.4 / 18.4;
-//   N = 8192, K = 2048: 30.5 / 33.8, 27.8 / 17.6, 17.3 / 13.9
-//   300 tokens, N = 2048, K = 4096: 64x32 40 / 25, 64x64 24.7 / 19, 128x128 83 / 39;
-//   N = 8192, K = 2048: 64x64 44 / 33, 128x128 48 / 28
-//   1000 tokens, N = 4097, K = 2048: 64x64 72 / 53, 128x128 59 / 42, 128x256 58 / 40, 256x256 85 / 63
-//   4096 tokens, N = 2048, K = 4096: 128x128 125 / 97, 128x256 119 / 84, 256x256 148 / 107;
-//   N = 8192, K = 2048: 250 / 203, 247 / 199, 196 / 167
-// so: the largest tile that leaves the 256 compute units enough of them, and the
-// smallest while it gives each unit one at most.
+// Which kernel and tile.  Measured (us, int8 / bf16, in a graph, MI355X; rows<MT,NT,WAVES>):
+//   16 tokens, N = 12288, K = 2048: rows<1,1,8> 13.3 / 15.3, <1,2,8> 14.4 / 15.9, <1,4,4> 12.5 / 14.2;
+//   N = 2048, K = 4096: 9.9 / 10.8, 12.6 / 14.0, 19.2 / 21.7
+//   17 tokens, N = 2048, K = 4096: rows<2,1,4> 11.0 / 12.9, <2,2,4> 14.1 / 16.3, 64x32 tiles 18.6 / 12.8;
+//   N = 4097, K = 2048: 9.9 / 10.4, 9.5 / 10.6, 12.6 / 9.1; N = 12288: 15.4 / 16.7, 14.5 / 16.9, 22.7 / 16.0,
+//   64x64 14.6 / 13.3
+//   64 tokens, N = 2048, K = 4096: rows<2,1,4> 13.6 / 16.0, <2,2,4> 17.3 / 19.3, 64x32 19.2 / 13.6;
+//   N = 4097, K = 2048: 17.6 / 18.6, 15.0 / 17.1, 13.4 / 10.0; N = 12288: 34.1 / 36.3, 24.5 / 28.9, 24.8 / 18.6,
+//   64x64 16.2 / 15.4
+//   128 tokens, N = 2048, K = 4096: rows<2,2,4> 17.5 / 21.3, 64x32 19.5 / 13.8, 64x64 22.7 / 15.8;
+//   N = 8192, K = 2048: 31.0 / 34.6, 25.0 / 18.6, 17.0 / 14.7
+//   300 tokens, N = 2048, K = 4096: 64x32 35.9 / 25.3, 64x64 23.2 / 20.0, 128x128 82 / 40;
+//   N = 8192, K = 2048: 64x64 43.2 / 33.2, 128x128 48.7 / 28.9
+//   1000 tokens, N = 4097, K = 2048: 64x64 73 / 55, 128x128 59 / 42, 128x256 57.5 / 39.9, 256x256 85 / 64
+//   4096 tokens, N = 2048, K = 4096: 128x128 117 / 88, 128x256 109 / 79, 256x256 150 / 102;
+//   N = 8192, K = 2048: 248 / 184, 240 / 185, 195 / 161
+// The rule: rows up to 64 tokens; then the largest tile that leaves the 256 compute
+// units enough of them, and the smallest while it gives each unit one at most.  It is
+// one rule for both types, by tokens and tiles alone, and not the best of the above
+// everywhere: at 33 to 64 tokens tiles are 1.2 to 1.9 times as fast where N is large
+// (12288: 16.2 / 15.4 against 24.5 / 28.9), and with bf16 also at N = 2048 (13.6
+// against 16.0); with int8 64x64 is 11% faster at 300 tokens and N = 8192, rows 10%
+// at 128 tokens and N = 2048; <1,4,4> is 6 to 7% faster at 16 tokens and N = 12288.
 template <bool INT8>
 hipError_t launch_any(const LinearArgs &a, hipStream_t s) {
     if (a.T <= 16) return launch_rows<INT8, 1, 1, 8>(a, s);
