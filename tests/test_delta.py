@@ -439,3 +439,97 @@ def test_prefill_operands_have_22_bits(dk, dv, L, n_seq):
     print(f"{n_seq} x {L}, {dk}x{dv}: largest error / bound: o {float(off_o.max()):.4f}, state {float(off_s.max()):.4f}",
           flush=True)
     assert float(off_o.max()) <= 1 and float(off_s.max()) <= 1
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("n_seq", [1, 9])
+@pytest.mark.parametrize("power", [-40, 60])
+def test_powers_of_two_pass_through(kind, n_seq, power):
+    """The rule is linear in v and the state: a power of two on both comes out
+    of every output, bit for bit."""
+    lens = [130] * n_seq
+    q, k, v, g, beta, s0, start = inputs(lens, 2, 8, 64, 128, True, 15)
+    got = []
+    for f in (1.0, 2.0 ** power):
+        o, s1 = torch.zeros(v.shape, dtype=torch.bfloat16, device="cuda"), torch.zeros_like(s0)
+        call(kind, q, k, (v.float() * f).bfloat16(), g, beta, start, None, s0 * f, s1, o, 0.1, True)
+        got.append((o.float(), s1))
+    torch.cuda.synchronize()
+    assert torch.equal(got[0][0] * 2.0 ** power, got[1][0]) and torch.equal(got[0][1] * 2.0 ** power, got[1][1])
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("n_seq", [1, 9])
+def test_large_values_behind_a_token(kind, n_seq):
+    """Tokens whose values are 2^16 times larger, in the same chunk, leave the
+    outputs before them as near as the 22 bits (test above) make them; the bound
+    is doubled for the operands' absolute step there (2^-39 of the largest, 2^-23
+    of the smaller ones)."""
+    L, cut = 64, 40
+    lens = [L] * n_seq
+    q, k, v, g, beta, s0, start = inputs(lens, 2, 8, 64, 128, True, 16)
+    v = v.unflatten(0, (n_seq, L)).clone()
+    v[:, cut:] *= 2.0 ** 16
+    v = v.flatten(0, 1)
+    o, s1 = torch.zeros(v.shape, dtype=torch.bfloat16, device="cuda"), torch.zeros_like(s0)
+    call(kind, q, k, v, g, beta, start, None, s0, s1, o, 0.1, True)
+    torch.cuda.synchronize()
+    before = lambda t: t.unflatten(0, (n_seq, L))[:, :cut].flatten(0, 1)
+    want, _, big, qn = rule(*(before(t) for t in (q, k, v, g, beta)), [cut] * n_seq, s0, 0.1, True)
+    half = torch.ldexp(torch.ones_like(want), torch.frexp(want).exponent - 9)
+    tol = 2 * 11 * 2.0 ** -20 * 0.1 * qn.norm(dim=-1) * big.repeat_interleave(cut, 0)
+    worst = float((((before(o).cpu().double() - want).abs() - half) / tol[..., None]).max())
+    print(f"{kind} {n_seq}: largest error / bound {worst:.4f}", flush=True)
+    assert worst <= 1
+
+
+@pytest.mark.parametrize("kind", KINDS)
+def test_long_sequence(kind):
+    """2^17 tokens.  With 0.1 of decay a token, what lies 1000 tokens back is
+    gone (e^-100): the last ones are those of the last 1064 tokens alone."""
+    T, tail = 2 ** 17 + 5, 1064
+    q, k, v, g, beta, s0, start = inputs([T], 1, 2, 64, 64, True, 17)
+    g = g * 0 - 0.1
+    o, s1 = torch.zeros(v.shape, dtype=torch.bfloat16, device="cuda"), torch.zeros_like(s0)
+    call(kind, q, k, v, g, beta, start, None, s0, s1, o, 0.1, True)
+    torch.cuda.synchronize()
+    ref = rule(*(t[-tail:] for t in (q, k, v, g, beta)), [tail], s0 * 0, 0.1, True)
+    want_o, want_s, big, qn = ref
+    check(o[-64:], s1, (want_o[-64:], want_s, big, qn[-64:]), [64], 0.1, 64, f"{kind} {T} tokens")
+
+
+@pytest.mark.parametrize("kind", KINDS)
+def test_many_sequences(kind):
+    gen = torch.Generator().manual_seed(1)
+    run(kind, torch.randint(0, 4, (3000,), generator=gen).tolist(), 1, 1, 64, 64, True, seed=18)
+
+
+@pytest.mark.parametrize("kind", KINDS)
+def test_most_heads(kind):
+    run(kind, [3, 65], 2, 1024, 64, 64, True, seed=19)
+
+
+def test_graphs_that_share_a_workspace():
+    """Two captured prompts with one workspace, replayed in turn."""
+    ws, jobs = None, []
+    for seed, lens in ((20, [70, 3]), (21, [200])):
+        q, k, v, g, beta, s0, start = inputs(lens, 2, 4, 128, 128, True, seed)
+        need = m.delta_workspace_size(sum(lens), len(lens), 2, 4, 128, 128)
+        ws = torch.empty(1 << 20 if need < 1 << 20 else need, dtype=torch.uint8, device="cuda") if ws is None else ws
+        assert need <= ws.numel()
+        o, s1 = torch.zeros(v.shape, dtype=torch.bfloat16, device="cuda"), torch.zeros_like(s0)
+        args = (q, k, v, g, beta, start, None, s0, s1, o, 0.1, True, ws)
+        m.moe_q4_delta_prefill(*args)
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            m.moe_q4_delta_prefill(*args)
+        jobs.append((graph, o, s1, o.clone(), s1.clone(), args))
+    for _ in range(3):
+        for graph, o, s1, *_ in jobs:
+            o.zero_()
+            s1.zero_()
+            graph.replay()
+    torch.cuda.synchronize()
+    for _, o, s1, want_o, want_s, _ in jobs:
+        assert torch.equal(o, want_o) and torch.equal(s1, want_s)

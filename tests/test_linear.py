@@ -362,3 +362,25 @@ def test_large_tiles_keep_infinities_and_nan_apart(fmt, K, T, N):
     torch.cuda.synchronize()
     assert torch.equal(ref, again)
     assert torch.isnan(y[bad]).all() and torch.equal(y[~bad], ref[~bad])
+
+
+@pytest.mark.parametrize("fmt", ["int8", "bf16"])
+@pytest.mark.parametrize("T,N", [(2, 130), (40, 70), (100, 130), (600, 4097)])
+def test_most_inputs(fmt, T, N):
+    """65536 inputs."""
+    run(fmt, T, 65536, N, out=torch.float32, seed=N)
+
+
+@pytest.mark.parametrize("T,N", [(1, 1 << 22), (20, (1 << 22) - 3), (70, 1 << 22), ((1 << 22) + 3, 17), ((1 << 22) + 3, 100)])
+def test_most_outputs_and_tokens(T, N):
+    """2^22 outputs (the longest rows) and more than 2^22 tokens, compared part by part."""
+    gen = torch.Generator(device="cuda").manual_seed(N)
+    q, s, w = weights("int8", N, 128, gen)
+    x = torch.randn(T, 128, generator=gen, device="cuda").bfloat16()
+    y = torch.full((T, N), float("nan"), device="cuda")
+    m.moe_q4_linear(x, m.linear_struct(q, s), y)
+    torch.cuda.synchronize()
+    step = 1 << 20
+    for t in range(0, T, step):
+        for n in range(0, N, step):
+            check(y[t:t + step, n:n + step], x[t:t + step], w[n:n + step], None, 0, None, f"T={T} N={N} at {t}, {n}")

@@ -273,3 +273,33 @@ def test_signalling_nan_counts_as_minus_infinity(V):
     f = want.float()
     f.view(torch.int32)[:, 5::3] = 0x7f800001
     assert all(torch.equal(p, q) for p, q in zip(score(f, tok, 20), score(want.float(), tok, 20)))
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_many_rows(dtype):
+    l, tok = rows((1 << 20) + 3, 5, dtype, 13)
+    check(l, tok, 2, f"many rows {dtype}")
+
+
+def test_graphs_that_share_a_workspace():
+    """Two captured calls with one workspace, replayed in turn."""
+    shapes = ((3, 60001), (5, 20001))
+    ws = torch.empty(max(m.logprobs_workspace_size(T, V, 8) for T, V in shapes), dtype=torch.uint8, device="cuda")
+    jobs = []
+    for i, (T, V) in enumerate(shapes):
+        l, tok = rows(T, V, "bf16", 30 + i)
+        want = score(l, tok, 8)
+        out = [torch.zeros_like(t) for t in want]
+        m.moe_q4_logprobs(l, tok, *out, ws)
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            m.moe_q4_logprobs(l, tok, *out, ws)
+        jobs.append((graph, out, want, l, tok))
+    for _ in range(3):
+        for graph, out, *_ in jobs:
+            for t in out:
+                t.zero_()
+            graph.replay()
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for _, out, want, *_ in jobs for a, b in zip(out, want))
