@@ -54,7 +54,7 @@ typedef enum {
  *   scale  f16 bit patterns [N][K/128], 2-byte aligned (int8; NULL for bf16).
  *          Scales must be finite.
  *   bias   float [N] or NULL
- * int8 needs K % 128 == 0, bf16 K % 8 == 0; K <= 65536, N < 2^24.
+ * int8 needs K % 128 == 0, bf16 K % 8 == 0; K <= 65536, N <= 2^22 (a row of y).
  */
 typedef struct moe_q4_linear_weights {
     int32_t in_features;    /* K */
@@ -131,6 +131,9 @@ typedef struct moe_q4_delta_shape {
  * for a few tokens per sequence); moe_q4_delta_prefill takes them in chunks of
  * 64 on the matrix cores (tuned for prompts) and needs
  *   ws  >= moe_q4_delta_workspace_size(T, n_seq, shape) bytes, 256-byte aligned.
+ * The operands of prefill's products hold 22 bits of every value down to 2^-16 of
+ * the largest beside it (in a column of the state, or of a chunk's values and
+ * updates) and steps of 2^-39 of that one below; decode works in fp32.
  * A NaN or an infinity in a token's inputs makes the outputs of its sequence
  * from that token on (prefill: from its chunk on) undefined numbers.
  */

@@ -8,8 +8,8 @@
 //   linear_rows_kernel  few tokens, or too few tiles for the other: no LDS in
 //       the main loop.  Bound by the weights' bytes (T small) or by what the
 //       caches deliver of x and W.
-//   linear_tile_kernel  many tokens: tiles staged through LDS, bound by the
-//       matrix cores.
+//   linear_tile_kernel  many tokens: tiles staged through LDS, bound by what LDS
+//       delivers to the matrix cores and, with few tiles, by the chain of steps.
 #include "backbone.h"
 
 namespace moeq4 {
@@ -229,7 +229,7 @@ hipError_t launch_rows(const LinearArgs &a, hipStream_t s) {
 // them.  Codes that one wave uses alone (WM = 1, the small tiles) it converts
 // in its registers, 1.5 instructions a code; a stage is a group then, whose
 // products start from 0 and are scaled and added under the next stage's.
-// Measured: 300 tokens, N = 2048, K = 4096: 24.7 us so, 35 us by way of LDS
+// Measured: 300 tokens, N = 2048, K = 4096: 23 to 25 us so, 35 us by way of LDS
 // (a step costs 0.75 us however few the tiles: the chain from barrier to
 // barrier, with two waves on a SIMD; bf16 19 us); its scales read by each wave
 // for itself, 64 bytes a row apart, cost 6 us more.
@@ -248,8 +248,8 @@ hipError_t launch_rows(const LinearArgs &a, hipStream_t s) {
 // the row's end chunks are read from its last one and masked where they are
 // used.
 //
-// Measured: 4096 tokens, N = 8192, K = 2048: bf16 167 us (824 TFLOP/s; the
-// library's product takes 98 us), int8 196 us (701 TFLOP/s; 32% of the matrix
+// Measured: 4096 tokens, N = 8192, K = 2048: bf16 161 us (853 TFLOP/s; torch's
+// product takes 98 us), int8 195 us (705 TFLOP/s; 32% of the matrix
 // units' time, half of the vector units': the conversion, 2.5 instructions a
 // code, and the rescaling, one per sum and group).
 constexpr int BLK = 32;   // inputs of a block

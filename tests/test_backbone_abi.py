@@ -142,3 +142,10 @@ def test_logprobs_workspace():
         assert _scores(**big, ws=None) == WORKSPACE
         assert _scores(**big, nb=need - 1) == WORKSPACE
         assert _scores(**big, ws=FAKE + 8, nb=need) == INVALID
+
+
+@pytest.mark.parametrize("T", [1, 2])
+def test_linear_outputs_are_at_most_a_row_of_y(T):
+    """2^22 outputs, the longest distance of rows, whatever the number of tokens."""
+    assert _linear(N=(1 << 22) + 1, T=T) == UNSUPPORTED
+    assert _linear(N=1 << 22, T=0) == OK
