@@ -10,8 +10,8 @@
 // spread over the rest, the state in registers from the first token to the
 // last.  Bound by the state's bytes (8 per element): each row's 32 columns
 // are one 128-byte line.  Measured: 64 sequences of one token, 32 heads of
-// 128 x 128 (268 MB of states): 42 us, 6.4 TB/s (a part of the states comes
-// from the last-level cache; a large copy moves 5.1 TB/s); one sequence: 4.8 us,
+// 128 x 128 (268 MB of states): 43 us, 6.2 TB/s (a part of the states comes
+// from the last-level cache; a large copy moves 5.1 TB/s); one sequence: 5.0 us,
 // the latency of one load, reduction and store.
 #include "backbone.h"
 
@@ -242,7 +242,7 @@ __device__ __forceinline__ float exp_diff(double d) {
 // and their products, are read and formed once for them).  Bound by the vector
 // work: about 1500 instructions a wave and chunk with one head, 80% of the
 // vector units' time.  Measured: 16384 tokens, 32 heads of 128 x 128 on 16 key
-// heads: 108 us with two heads (2.0 TB/s of the 216 MB it writes).  Without P's
+// heads: 108 to 114 us with two heads (2.0 TB/s of the 216 MB it writes).  Without P's
 // remainders 103 us, and then 122 us with one head, 128 us with the tiles of A and
 // P on one wave each (up to eight a wave), 171 us with a row's load waiting for the
 // one before it.
@@ -534,7 +534,7 @@ __global__ __launch_bounds__(256) void delta_prep_kernel(DeltaArgs a, uint8_t *_
 //     a shorter chain (3.2 us a chunk, a third of it the last stage), more LDS
 //     traffic per column.  For few columns in all.
 // Measured: one prompt of 8192 tokens, 32 heads of 128 x 128: 410 us with SPLIT;
-// 8 prompts of 2048: 296 us without.  (With one f16 for what only o sees 385 and
+// 8 prompts of 2048: 296 to 302 us without.  (With one f16 for what only o sees 385 and
 // 284 us, and then 540 us for the first without SPLIT, 440 us with one state wave
 // of 512 registers and three others.)
 template <int DK, bool SPLIT>

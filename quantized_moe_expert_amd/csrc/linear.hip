@@ -87,7 +87,7 @@ __device__ __forceinline__ void store_output(const LinearArgs &a, int64_t t, int
 // order of the inputs within a product is free as long as both operands have
 // the same, so lane group g = lane / 16 takes 16 consecutive codes and two
 // products the halves of them.  Measured: one token, 4097 x 2048 bf16 (17 MB):
-// 5.3 us (3.2 TB/s); 16 tokens, 12288 x 2048 int8 (26 MB): 12.8 us (2.0 TB/s),
+// 5.5 us (3.1 TB/s); 16 tokens, 12288 x 2048 int8 (26 MB): 13.3 us (2.0 TB/s),
 // where each workgroup reads x (64 KB) besides 32 KB of codes.
 template <bool INT8, int MT, int NT, int WAVES>
 __global__ __launch_bounds__(WAVES * 64) void linear_rows_kernel(LinearArgs a, int ntiles, int ttiles) {

@@ -209,7 +209,7 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
 // 512 rows of 151939 bf16 (156 MB): 62 us with n = 20 (2.5 TB/s) and 7 us for the
 // join, 34.5 us in all with n = 0 (4.5 TB/s).  Before the candidates were found
 // by the sign of a difference and reloaded by place: 82 us; ranked by one lane
-// each with one key after another: 128 us.  One row of 4097, n = 8: 4.8 us.
+// each with one key after another: 128 us.  One row of 4097, n = 8: 4.9 us.
 template <bool F32, bool TOP, bool DIRECT>
 __global__ __launch_bounds__(THREADS) void logprobs_segment_kernel(LogprobsArgs a, int segs,
                                                                    Sums *__restrict__ part,
