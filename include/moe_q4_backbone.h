@@ -9,6 +9,12 @@
  *   - moe_q4_delta_decode, moe_q4_delta_prefill: the gated delta rule, the
  *     mixer of three layers in four (drama-rs page, first paragraph and
  *     "Layout": gated DeltaNet);
+ *   - moe_q4_kv_append, moe_q4_attention: the paged cache of the attention
+ *     layers, one layer in four (drama-rs page, first paragraph: full attention
+ *     every 4th layer), and the attention of prompts, single tokens and trees of
+ *     drafted tokens over it;
+ *   - moe_q4_add_norm: what lies between two blocks: norm of a block's output,
+ *     gate, residual, norm before the next block;
  *   - moe_q4_logprobs: log probabilities of given tokens, entropy and the most
  *     likely tokens from the head's logits.
  *
@@ -45,7 +51,8 @@ typedef enum {
 typedef enum {
     MOE_Q4_ACT_NONE = 0,
     MOE_Q4_ACT_SILU = 1,      /* z / (1 + exp(-z)) */
-    MOE_Q4_ACT_GELU = 2       /* z (1 + erf(z / sqrt 2)) / 2 */
+    MOE_Q4_ACT_GELU = 2,      /* z (1 + erf(z / sqrt 2)) / 2 */
+    MOE_Q4_ACT_SIGMOID = 3    /* 1 / (1 + exp(-z)): gates of moe_q4_add_norm only */
 } moe_q4_act;
 
 /*
@@ -72,7 +79,7 @@ typedef struct moe_q4_linear_weights {
  * of the bf16 weights) with x are exact; a group's scale multiplies its
  * partial sum.
  *   x         bf16 [T] rows of K at distance ldx (16-byte aligned, ldx % 8 == 0)
- *   act       moe_q4_act
+ *   act       moe_q4_act, but for MOE_Q4_ACT_SIGMOID
  *   residual  bf16 [T] rows of N at distance ldr, or NULL; may be y itself
  *             (same pointer and distance, y_dtype MOE_Q4_BF16)
  *   y         bf16 or float (y_dtype) [T] rows of N at distance ldy; must not
@@ -150,6 +157,131 @@ MOE_Q4_API int moe_q4_delta_prefill(const void *q, int64_t ldq, const void *k, i
                                     int32_t n_states, const moe_q4_delta_shape *shape, float scale, int32_t norm_qk,
                                     const float *state_in, float *state_out, void *o, int64_t ldo, void *ws,
                                     size_t ws_bytes, moe_q4_stream stream);
+
+/*
+ * Keys and values of n_seq sequences in pages of a pool.  Token i of sequence
+ * b (its cache index, from 0) lies in page p = page_table[b][i / page_size],
+ * at k and v [p][head][i % page_size].
+ *   k, v        bf16 [n_pages][kv_heads][page_size][head_dim], 16-byte aligned
+ *   page_table  int32 [n_seq][max_pages].  An entry outside [0, n_pages) is a
+ *               page that is not there: its keys are seen by nobody and nothing
+ *               is stored in it.  Entries behind a sequence's last token are not
+ *               used.  Sequences may share pages that they only read.
+ *   kv_len      int32 [n_seq]: tokens of each sequence, the call's own (the
+ *               rows of seq_start) the last among them: row i of the call's n
+ *               rows of sequence b has cache index kv_len[b] - n + i.  Tokens
+ *               with an index below 0 or behind the table are not stored; keys
+ *               behind the table are seen by nobody.
+ * head_dim 64, 128 or 256; page_size a multiple of 16, max_pages * page_size
+ * < 2^31; kv_heads at most 1024.
+ */
+typedef struct moe_q4_kv_cache {
+    int32_t kv_heads, head_dim;
+    int32_t page_size;          /* tokens per page */
+    int32_t max_pages;          /* entries per sequence of page_table */
+    int64_t n_pages;            /* pages of the pool, below 2^31 */
+    void *k, *v;
+    const int32_t *page_table;
+    const int32_t *kv_len;
+} moe_q4_kv_cache;
+
+/*
+ * Heads of T packed tokens into the cache.  Per head of q and k, in fp32 and
+ * rounded once:
+ *   x <- x / sqrt(mean(x^2) + eps) * norm      (with q_norm, k_norm)
+ *   the first rot_dim entries turned in pairs by position * inv_freq[j]:
+ *   (a, b) <- (a cos - b sin, b cos + a sin)
+ * The angle is computed in 64 bits, so that it is right for every position.
+ *   q, k, v      bf16 [T] rows of [q_heads or kv_heads][head_dim] at distances
+ *                ldq, ldk, ldv (16-byte aligned, distances % 8 == 0).  q may be
+ *                NULL: keys and values alone.
+ *   seq_start    int32 [n_seq + 1] as of moe_q4_delta_decode.  Rows behind the
+ *                last sequence are neither read nor written.
+ *   positions    int32 [T] or NULL: a token's position is its cache index
+ *   inv_freq     float [rot_dim / 2]; NULL with rot_dim = 0: no rotation.
+ *                rot_dim % 16 == 0, at most head_dim.
+ *   interleaved  0: pair j is entries j and j + rot_dim / 2; else 2j and 2j + 1
+ *   q_norm, k_norm  float [head_dim] or NULL
+ *   q_out        bf16 [T] rows of [q_heads][head_dim] at distance ldqo; may be q
+ *                itself (same pointer and distance), must not overlap the inputs
+ *                otherwise.
+ * Two tokens of one call must not share a place in the cache (its contents would
+ * be undefined).  q_heads at most 1024; T < 2^24, n_seq < 2^20.
+ */
+MOE_Q4_API int moe_q4_kv_append(const void *q, int64_t ldq, int32_t q_heads, const void *k, int64_t ldk,
+                                const void *v, int64_t ldv, int64_t T, const int32_t *seq_start, int32_t n_seq,
+                                const moe_q4_kv_cache *cache, const int32_t *positions, const float *inv_freq,
+                                int32_t rot_dim, int32_t interleaved, const float *q_norm, const float *k_norm,
+                                float eps, void *q_out, int64_t ldqo, moe_q4_stream stream);
+
+/*
+ * Attention of T packed query rows over the cache.  Query head h reads head
+ * h * kv_heads / q_heads of the cache.  For a query and a key that it sees
+ *   s = scale q . k,  then s = cap tanh(s / cap)     (cap > 0)
+ *                     then s -= slopes[h] * |distance|  (with slopes)
+ *   o = sum softmax(s) v
+ * with scores, softmax and sums in fp32; the weights may be rounded to bf16 for
+ * their products with v.  A query that sees no key gets o = 0.  The distance is
+ * the query's position less the key's; positions are cache indices.  A query sees
+ *   - the keys up to its own index, with window > 0 only those at a distance
+ *     below window,
+ *   - and the first prefix[b] keys of its sequence, wherever it stands,
+ * of its own sequence alone.
+ * With a tree the rows of a sequence are drafted tokens, at most 64: bit j of
+ * tree[t] says that row t sees row j of its sequence (itself, as a rule, and
+ * those that it follows).  Cached tokens before the rows are seen as above; a
+ * row's position is the number of those plus the number of other rows that it
+ * sees, and distances (window, slopes) go by it.  Rows behind the 64th of a
+ * sequence are seen by nobody.  prefix must be NULL with a tree.
+ *   q          bf16 [T] rows of [q_heads][head_dim] at distance ldq (as
+ *              moe_q4_kv_append leaves them)
+ *   seq_start  int32 [n_seq + 1] as of moe_q4_delta_decode; the keys of the rows
+ *              themselves are read from the cache
+ *   slopes     float [q_heads] or NULL
+ *   prefix     int32 [n_seq] or NULL
+ *   tree       uint64 [T], 8-byte aligned, or NULL
+ *   o          bf16 [T] rows of [q_heads][head_dim] at distance ldo; must not
+ *              overlap the inputs.  (q and o 16-byte aligned, distances % 8 == 0)
+ *   ws         >= moe_q4_attention_workspace_size(T, n_seq, q_heads, cache)
+ *              bytes, 256-byte aligned (may be NULL when that is 0)
+ * scale, cap and the slopes must be finite, cap and window at least 0; q_heads a
+ * multiple of kv_heads, at most 1024; T * q_heads < 2^26, n_seq < 2^20.
+ * Rows behind the last sequence are neither read nor written.  Parts of a row's
+ * keys are joined in a fixed order: the same input gives the same bits.  A NaN or
+ * an infinity in a key or value reaches the queries that see it (some of their
+ * outputs are NaN or infinite) and no others.
+ */
+MOE_Q4_API size_t moe_q4_attention_workspace_size(int64_t T, int32_t n_seq, int32_t q_heads,
+                                                  const moe_q4_kv_cache *cache);
+MOE_Q4_API int moe_q4_attention(const void *q, int64_t ldq, int32_t q_heads, int64_t T, const int32_t *seq_start,
+                                int32_t n_seq, const moe_q4_kv_cache *cache, float scale, float cap, int32_t window,
+                                const float *slopes, const int32_t *prefix, const uint64_t *tree, void *o, int64_t ldo,
+                                void *ws, size_t ws_bytes, moe_q4_stream stream);
+
+/*
+ * Between two blocks, over T rows of H values, in fp32:
+ *   r = u, then r = r / sqrt(mean(r^2) + eps) * post_norm   (with post_norm)
+ *          then r = r * act(gate)                           (with gate)
+ *   x_out = x + scale r                                     (rounded to bf16)
+ *   y     = x_out / sqrt(mean(x_out^2) + eps) * pre_norm    (with pre_norm; of the rounded x_out)
+ *   x          bf16 rows at distance ldx, or NULL: nothing is added (x_out = scale r)
+ *   u          bf16 or float (u_dtype) rows at distance ldu (the experts' float
+ *              output, a linear layer's), or NULL: a plain norm of x (x_out = x; post_norm
+ *              and gate must be NULL)
+ *   gate       bf16 rows at distance ldg, or NULL; ldg = 0: one row for all tokens
+ *   gate_act   MOE_Q4_ACT_NONE, MOE_Q4_ACT_SILU or MOE_Q4_ACT_SIGMOID
+ *   post_norm, pre_norm  float [H], 16-byte aligned, or NULL
+ *   x_out      bf16 rows at distance ldxo, or NULL: not wanted (pre_norm is given);
+ *              may be x itself (same pointer and distance)
+ *   y          bf16 rows at distance ldy (with pre_norm)
+ * Rows are 16-byte aligned with distances % 8 == 0; H % 8 == 0, H <= 65536;
+ * T < 2^26, T * H < 2^33.  The outputs must not overlap each other or, but for x_out,
+ * the inputs; u, gate and x may be the same memory.
+ */
+MOE_Q4_API int moe_q4_add_norm(const void *x, int64_t ldx, const void *u, int64_t ldu, int32_t u_dtype, int64_t T,
+                               int32_t H, const float *post_norm, const void *gate, int64_t ldg, int32_t gate_act,
+                               float scale, const float *pre_norm, float eps, void *x_out, int64_t ldxo, void *y,
+                               int64_t ldy, moe_q4_stream stream);
 
 #define MOE_Q4_MAX_TOP 32
 /*

@@ -6,7 +6,8 @@ SwiGLU experts (fused-dequant GEMVs for decode, matrix-core grouped GEMMs for
 prefill), the gate-weighted combine and the int8 shared expert.  This package is its thin Python
 binding: ``_lib`` mirrors the C entry points, ``layer`` holds buffers;
 ``_backbone`` mirrors the entry points beside the experts (linear layers, the
-gated delta rule, token scores).
+gated delta rule, attention over a paged cache, norms between blocks, token
+scores).
 """
 from ._lib import (ASYM_G64, SYM_G128, FP8_B128, NVFP4, WS_DECODE, WS_GROUP, WS_PREFILL, WS_ROUTE, EXPORTS, MoeQ4Error,
                    error_string, layer_struct, lib, moe_q4_decode, moe_q4_dequant, moe_q4_group,
@@ -17,9 +18,10 @@ from ._lib import (ASYM_G64, SYM_G128, FP8_B128, NVFP4, WS_DECODE, WS_GROUP, WS_
                    moe_q4_prefill_pack_size, moe_q4_prefill_pack, prefill_pack,
                    moe_q4_forward_noalloc, NOALLOC_SCRATCH_BYTES, moe_q4_forward_det, WS_FORWARD_DET,
                    FRAME_MAX_LANES, frame_workspace_size, moe_q4_frame)
-from ._backbone import (ACT_GELU, ACT_NONE, ACT_SILU, BACKBONE_EXPORTS, LINEAR_BF16, LINEAR_INT8, MAX_TOP, DeltaShape,
-                        LinearWeights, delta_workspace_size, linear_struct, logprobs_workspace_size,
-                        moe_q4_delta_decode, moe_q4_delta_prefill, moe_q4_linear, moe_q4_logprobs)
+from ._backbone import (ACT_GELU, ACT_NONE, ACT_SIGMOID, ACT_SILU, BACKBONE_EXPORTS, LINEAR_BF16, LINEAR_INT8, MAX_TOP,
+                        DeltaShape, KVCache, LinearWeights, attention_workspace_size, delta_workspace_size,
+                        kv_cache_struct, linear_struct, logprobs_workspace_size, moe_q4_add_norm, moe_q4_attention,
+                        moe_q4_delta_decode, moe_q4_delta_prefill, moe_q4_kv_append, moe_q4_linear, moe_q4_logprobs)
 from .layer import MoeQ4Layer
 from .mixer import DeltaMixer
 
@@ -34,4 +36,6 @@ __all__ = ["ASYM_G64", "SYM_G128", "FP8_B128", "NVFP4", "WS_DECODE", "WS_GROUP",
            "FRAME_MAX_LANES", "frame_workspace_size", "moe_q4_frame",
            "ACT_GELU", "ACT_NONE", "ACT_SILU", "BACKBONE_EXPORTS", "LINEAR_BF16", "LINEAR_INT8", "MAX_TOP", "DeltaShape",
            "LinearWeights", "delta_workspace_size", "linear_struct", "logprobs_workspace_size",
-           "moe_q4_delta_decode", "moe_q4_delta_prefill", "moe_q4_linear", "moe_q4_logprobs", "DeltaMixer"]
+           "moe_q4_delta_decode", "moe_q4_delta_prefill", "moe_q4_linear", "moe_q4_logprobs", "DeltaMixer",
+           "ACT_SIGMOID", "KVCache", "attention_workspace_size", "kv_cache_struct", "moe_q4_add_norm", "moe_q4_attention",
+           "moe_q4_kv_append"]

@@ -15,13 +15,14 @@ import torch
 from . import _lib
 
 LINEAR_INT8, LINEAR_BF16 = 0, 1
-ACT_NONE, ACT_SILU, ACT_GELU = 0, 1, 2
+ACT_NONE, ACT_SILU, ACT_GELU, ACT_SIGMOID = 0, 1, 2, 3
 BF16, F32 = 0, 1
 MAX_TOP = 32       # MOE_Q4_MAX_TOP
 LINEAR_GROUP = 128  # inputs per int8 weight scale
 
 # every entry point declared in include/moe_q4_backbone.h
 BACKBONE_EXPORTS = ("moe_q4_linear", "moe_q4_delta_workspace_size", "moe_q4_delta_decode", "moe_q4_delta_prefill",
+                    "moe_q4_kv_append", "moe_q4_attention_workspace_size", "moe_q4_attention", "moe_q4_add_norm",
                     "moe_q4_logprobs_workspace_size", "moe_q4_logprobs")
 
 
@@ -35,6 +36,13 @@ class DeltaShape(ctypes.Structure):
     """struct moe_q4_delta_shape"""
     _fields_ = [("k_heads", ctypes.c_int32), ("v_heads", ctypes.c_int32), ("k_dim", ctypes.c_int32),
                 ("v_dim", ctypes.c_int32)]
+
+
+class KVCache(ctypes.Structure):
+    """struct moe_q4_kv_cache"""
+    _fields_ = [("kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32), ("page_size", ctypes.c_int32),
+                ("max_pages", ctypes.c_int32), ("n_pages", ctypes.c_int64), ("k", ctypes.c_void_p),
+                ("v", ctypes.c_void_p), ("page_table", ctypes.c_void_p), ("kv_len", ctypes.c_void_p)]
 
 
 _ready = None
@@ -55,6 +63,16 @@ def lib() -> ctypes.CDLL:
         L.moe_q4_delta_decode.argtypes = delta + [P]
         L.moe_q4_delta_prefill.restype = ctypes.c_int
         L.moe_q4_delta_prefill.argtypes = delta + [P, sz, P]
+        cache = ctypes.POINTER(KVCache)
+        L.moe_q4_kv_append.restype = ctypes.c_int
+        L.moe_q4_kv_append.argtypes = [P, i64, i32, P, i64, P, i64, i64, P, i32, cache, P, P, i32, i32, P, P, f32, P,
+                                       i64, P]
+        L.moe_q4_attention_workspace_size.restype = sz
+        L.moe_q4_attention_workspace_size.argtypes = [i64, i32, i32, cache]
+        L.moe_q4_attention.restype = ctypes.c_int
+        L.moe_q4_attention.argtypes = [P, i64, i32, i64, P, i32, cache, f32, f32, i32, P, P, P, P, i64, P, sz, P]
+        L.moe_q4_add_norm.restype = ctypes.c_int
+        L.moe_q4_add_norm.argtypes = [P, i64, P, i64, i32, i64, i32, P, P, i64, i32, f32, P, f32, P, i64, P, i64, P]
         L.moe_q4_logprobs_workspace_size.restype = sz
         L.moe_q4_logprobs_workspace_size.argtypes = [i64, i64, i32]
         L.moe_q4_logprobs.restype = ctypes.c_int
@@ -210,6 +228,118 @@ def moe_q4_delta_prefill(q, k, v, g, beta, seq_start, state_idx, state_in, state
     memory of delta_workspace_size bytes."""
     _delta("moe_q4_delta_prefill", q, k, v, g, beta, seq_start, state_idx, state_in, state_out, o, scale, norm_qk,
            ws, stream)
+
+
+def kv_cache_struct(k, v, page_table, kv_len) -> KVCache:
+    """struct moe_q4_kv_cache from the pool's pages k, v bf16 [n_pages,
+    kv_heads, page_size, head_dim], page_table int32 [n_seq, max_pages] and
+    kv_len int32 [n_seq].  The caller keeps the tensors alive; their contents
+    are read when a call runs."""
+    dev = k.get_device()
+    if dev < 0:
+        raise ValueError("moe_q4 takes device tensors")
+    if k.dim() != 4 or k.dtype not in _SIXTEEN:
+        raise ValueError("k: expected bf16 pages [n_pages, kv_heads, page_size, head_dim]")
+    if page_table.dim() != 2:
+        raise ValueError("page_table: expected [n_seq, max_pages]")
+    n_pages, heads, page, d = k.shape
+    n_seq, cols = page_table.shape
+    c = KVCache(heads, d, page, cols, n_pages, _flat(k, "k", dev, k.shape, k.dtype),
+                _flat(v, "v", dev, k.shape, k.dtype), _flat(page_table, "page_table", dev, (n_seq, cols), torch.int32),
+                _flat(kv_len, "kv_len", dev, (n_seq,), torch.int32))
+    c.device, c.n_seq = dev, n_seq
+    return c
+
+
+def _cached(cache, seq_start, dev):
+    """(pointer, n_seq) of the starts of the cache's sequences."""
+    if cache.device != dev:
+        raise ValueError("moe_q4 takes device tensors of the current device")
+    return _flat(seq_start, "seq_start", dev, (cache.n_seq + 1,), torch.int32), cache.n_seq
+
+
+def moe_q4_kv_append(q, k, v, seq_start, cache, q_out, inv_freq=None, positions=None, q_norm=None, k_norm=None,
+                     eps=1e-6, interleaved=False, stream=None):
+    """q bf16 [T, Hq, d] (or None), k, v bf16 [T, Hkv, d] (rows may lie in
+    wider ones): heads of q and k normed (q_norm, k_norm float32 [d]) and
+    turned by position * inv_freq (float32 [rot / 2]; positions int32 [T],
+    None: the cache index), q into q_out (may be q), k and v into the cache of
+    kv_cache_struct behind the tokens that it has of their sequences."""
+    dev = _device()
+    start, n_seq = _cached(cache, seq_start, dev)
+    T, d = k.shape[0], cache.head_dim
+    kv = (T, cache.kv_heads, d)
+    kp, ldk = _rows(k, "k", dev, kv)
+    vp, ldv = _rows(v, "v", dev, kv)
+    qp, ldq, op, ldo, hq = None, 0, None, 0, 0
+    if q is not None:
+        hq = q.shape[1]
+        qp, ldq = _rows(q, "q", dev, (T, hq, d))
+        op, ldo = _rows(q_out, "q_out", dev, (T, hq, d))
+    elif q_out is not None:
+        raise ValueError("q_out: without q there is none")
+    rot = 0 if inv_freq is None else 2 * inv_freq.numel()
+    st = lib().moe_q4_kv_append(qp, ldq, hq, kp, ldk, vp, ldv, T, start, n_seq, cache,
+                                _flat(positions, "positions", dev, (T,), torch.int32),
+                                _flat(inv_freq, "inv_freq", dev, (rot // 2,), torch.float32), rot,
+                                1 if interleaved else 0, _flat(q_norm, "q_norm", dev, (d,), torch.float32),
+                                _flat(k_norm, "k_norm", dev, (d,), torch.float32), eps, op, ldo, _stream(stream, dev))
+    if st:
+        raise _lib.MoeQ4Error("moe_q4_kv_append", st)
+
+
+def attention_workspace_size(T: int, n_seq: int, q_heads: int, cache) -> int:
+    return int(lib().moe_q4_attention_workspace_size(int(T), int(n_seq), int(q_heads), cache))
+
+
+def moe_q4_attention(q, seq_start, cache, o, scale, ws=None, cap=0.0, window=0, slopes=None, prefix=None, tree=None,
+                     stream=None):
+    """Attention of q, o bf16 [T, Hq, d] (rows may lie in wider ones) over the
+    cache of kv_cache_struct: scores scale q.k, capped (cap > 0), less slopes
+    float32 [Hq] times the distance; causal, within ``window`` keys, and the
+    first prefix int32 [n_seq] keys of a sequence for all of it; tree int64 [T]:
+    bit j says that a row sees row j of its sequence's new ones.  ``ws``: device
+    memory of attention_workspace_size bytes."""
+    dev = _device()
+    start, n_seq = _cached(cache, seq_start, dev)
+    T, hq, d = q.shape
+    if d != cache.head_dim:
+        raise ValueError(f"q: expected heads of {cache.head_dim}, got {d}")
+    qp, ldq = _rows(q, "q", dev, (T, hq, d))
+    op, ldo = _rows(o, "o", dev, (T, hq, d))
+    wp, nb = _ws(ws, dev)
+    st = lib().moe_q4_attention(qp, ldq, hq, T, start, n_seq, cache, scale, cap, window,
+                                _flat(slopes, "slopes", dev, (hq,), torch.float32),
+                                _flat(prefix, "prefix", dev, (n_seq,), torch.int32),
+                                _flat(tree, "tree", dev, (T,), torch.int64), op, ldo, wp, nb, _stream(stream, dev))
+    if st:
+        raise _lib.MoeQ4Error("moe_q4_attention", st)
+
+
+def moe_q4_add_norm(x, u, x_out, y, pre_norm=None, post_norm=None, gate=None, gate_act=ACT_NONE, scale=1.0, eps=1e-6,
+                    stream=None):
+    """x_out = x + scale * u', u' = u normed (post_norm float32 [H]) and
+    gated (gate bf16 [T, H], or [1, H] for all rows), y = x_out normed
+    (pre_norm).  x bf16 [T, H] or None, u bf16 or float32 [T, H] or None, x_out
+    (may be x) and y bf16 [T, H] or None; rows may lie in wider ones."""
+    dev = _device()
+    T, H = (u if x is None else x).shape
+    xp, ldx = (None, 0) if x is None else _rows(x, "x", dev, (T, H))
+    f32 = u is not None and u.dtype == torch.float32
+    up, ldu = (None, 0) if u is None else _rows(u, "u", dev, (T, H), (torch.float32,) if f32 else _SIXTEEN)
+    gp, ldg = None, 0
+    if gate is not None:
+        one = gate.shape[0] == 1 and T != 1
+        gp, ldg = _rows(gate, "gate", dev, (1 if one else T, H))
+        ldg = 0 if one else ldg
+    op, ldo = (None, 0) if x_out is None else _rows(x_out, "x_out", dev, (T, H))
+    yp, ldy = (None, 0) if y is None else _rows(y, "y", dev, (T, H))
+    st = lib().moe_q4_add_norm(xp, ldx, up, ldu, F32 if f32 else BF16, T, H,
+                               _flat(post_norm, "post_norm", dev, (H,), torch.float32), gp, ldg, gate_act, scale,
+                               _flat(pre_norm, "pre_norm", dev, (H,), torch.float32), eps, op, ldo, yp, ldy,
+                               _stream(stream, dev))
+    if st:
+        raise _lib.MoeQ4Error("moe_q4_add_norm", st)
 
 
 def logprobs_workspace_size(T: int, V: int, n_top: int) -> int:

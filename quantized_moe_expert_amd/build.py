@@ -12,7 +12,8 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libmoe_q4.so")
 SOURCES = ["api.hip", "route.hip", "group.hip", "decode.hip", "prefill.hip", "shared.hip", "misc.hip",
-           "backbone_api.hip", "linear.hip", "delta.hip", "score.hip"]
+           "backbone_api.hip", "linear.hip", "delta.hip", "score.hip",
+           "cache.hip", "attention.hip", "norm.hip"]
 ARCH = os.environ.get("MOEQ4_ARCH", "gfx950")
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 

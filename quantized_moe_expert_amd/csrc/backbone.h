@@ -45,6 +45,72 @@ hipError_t launch_delta_decode(const DeltaArgs &a, hipStream_t s);
 size_t delta_workspace_bytes(int64_t T, int n_seq, int hv);
 hipError_t launch_delta_prefill(const DeltaArgs &a, void *ws, hipStream_t s);
 
+struct Cache {
+    int hkv, d, page, max_pages;
+    int64_t n_pages;
+    uint16_t *k, *v;
+    const int32_t *table, *kv_len;
+};
+struct AppendArgs {
+    const uint16_t *q, *k, *v;
+    int64_t ldq, ldk, ldv;
+    int hq;
+    int64_t T;
+    const int32_t *seq_start;
+    int n_seq;
+    Cache cache;
+    const int32_t *positions;
+    const float *inv_freq;
+    int rot;
+    bool interleaved;
+    const float *q_norm, *k_norm;
+    float eps;
+    uint16_t *q_out;
+    int64_t ldqo;
+};
+hipError_t launch_kv_append(const AppendArgs &a, hipStream_t s);
+
+struct AttentionArgs {
+    const uint16_t *q;
+    int64_t ldq;
+    int hq;
+    int64_t T;
+    const int32_t *seq_start;
+    int n_seq;
+    Cache cache;
+    float scale, cap;
+    int window;
+    const float *slopes;
+    const int32_t *prefix;
+    const uint64_t *tree;
+    uint16_t *o;
+    int64_t ldo;
+};
+size_t attention_workspace_bytes(int64_t T, int n_seq, int hq, const Cache &c);
+hipError_t launch_attention(const AttentionArgs &a, void *ws, hipStream_t s);
+
+struct AddNormArgs {
+    const uint16_t *x;
+    int64_t ldx;
+    const void *u;
+    int64_t ldu;
+    bool u_f32;
+    int64_t T;
+    int H;
+    const float *post;
+    const uint16_t *gate;
+    int64_t ldg;
+    int act;
+    float scale;
+    const float *pre;
+    float eps;
+    uint16_t *x_out;
+    int64_t ldxo;
+    uint16_t *y;
+    int64_t ldy;
+};
+hipError_t launch_add_norm(const AddNormArgs &a, hipStream_t s);
+
 struct LogprobsArgs {
     const void *logits;
     bool f32;

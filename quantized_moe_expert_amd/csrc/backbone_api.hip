@@ -3,6 +3,8 @@
 #include "../../include/moe_q4_backbone.h"
 #include "backbone.h"
 
+#include <cmath>
+
 using namespace moeq4;
 
 namespace {
@@ -55,6 +57,34 @@ int delta_args(const void *q, int64_t ldq, const void *k, int64_t ldk, const voi
                   n_states, sh->k_heads, sh->v_heads, sh->k_dim, sh->v_dim, scale, norm_qk != 0, state_in,
                   state_out, static_cast<uint16_t *>(o), ldo};
     return MOE_Q4_OK;
+}
+
+// A cache's own fields; pointers are looked at when it is used (a size may be
+// asked for before they exist).
+int check_cache(const moe_q4_kv_cache *c, int32_t q_heads) {
+    if (!c || c->kv_heads < 1 || c->head_dim < 1 || c->page_size < 1 || c->max_pages < 1 || c->n_pages < 1 ||
+        q_heads < 1 || q_heads % c->kv_heads)
+        return MOE_Q4_ERR_INVALID_ARG;
+    if ((c->head_dim != 64 && c->head_dim != 128 && c->head_dim != 256) || c->page_size % 16 || q_heads > 1024 ||
+        c->n_pages >= (int64_t)1 << 31 || (int64_t)c->max_pages * c->page_size >= (int64_t)1 << 31)
+        return MOE_Q4_ERR_UNSUPPORTED;
+    return MOE_Q4_OK;
+}
+
+int check_cache_pointers(const moe_q4_kv_cache *c) {
+    return c->k && c->v && c->page_table && c->kv_len && aligned(c->k, 16) && aligned(c->v, 16) &&
+                   aligned(c->page_table, 4) && aligned(c->kv_len, 4)
+               ? MOE_Q4_OK
+               : MOE_Q4_ERR_INVALID_ARG;
+}
+
+Cache cache_of(const moe_q4_kv_cache *c) {
+    return Cache{c->kv_heads, c->head_dim, c->page_size, c->max_pages, c->n_pages, static_cast<uint16_t *>(c->k),
+                 static_cast<uint16_t *>(c->v), c->page_table, c->kv_len};
+}
+
+bool attention_sizes(int64_t T, int32_t n_seq, int32_t q_heads) {
+    return T < (int64_t)1 << 26 && T * q_heads < (int64_t)1 << 26 && n_seq < 1 << 20;
 }
 
 }  // namespace
@@ -114,6 +144,92 @@ int moe_q4_delta_prefill(const void *q, int64_t ldq, const void *k, int64_t ldk,
     if (need && (!ws || ws_bytes < need)) return MOE_Q4_ERR_WORKSPACE;
     if (need && !aligned(ws, 256)) return MOE_Q4_ERR_INVALID_ARG;
     return hip_status(launch_delta_prefill(a, ws, reinterpret_cast<hipStream_t>(stream)));
+}
+
+int moe_q4_kv_append(const void *q, int64_t ldq, int32_t q_heads, const void *k, int64_t ldk, const void *v,
+                     int64_t ldv, int64_t T, const int32_t *seq_start, int32_t n_seq, const moe_q4_kv_cache *cache,
+                     const int32_t *positions, const float *inv_freq, int32_t rot_dim, int32_t interleaved,
+                     const float *q_norm, const float *k_norm, float eps, void *q_out, int64_t ldqo,
+                     moe_q4_stream stream) {
+    // Without q its heads do not count.
+    int st = check_cache(cache, q ? q_heads : cache ? cache->kv_heads : 0);
+    if (st) return st;
+    if (cache->kv_heads > 1024) return MOE_Q4_ERR_UNSUPPORTED;
+    if (T < 0 || n_seq < 0 || rot_dim < 0 || rot_dim > cache->head_dim || !(eps >= 0.0f)) return MOE_Q4_ERR_INVALID_ARG;
+    if (T >= 1 << 24 || n_seq >= 1 << 20 || rot_dim % 16) return MOE_Q4_ERR_UNSUPPORTED;
+    if (T == 0 || n_seq == 0) return MOE_Q4_OK;
+    if ((rot_dim > 0) != (inv_freq != nullptr) || !aligned(inv_freq, 4) || !aligned(positions, 4) ||
+        !aligned(q_norm, 4) || !aligned(k_norm, 4) || !seq_start || !aligned(seq_start, 4))
+        return MOE_Q4_ERR_INVALID_ARG;
+    if ((st = check_cache_pointers(cache))) return st;
+    const int64_t kw = (int64_t)cache->kv_heads * cache->head_dim, qw = (int64_t)q_heads * cache->head_dim;
+    if ((st = check_rows(k, ldk, kw, 16, true)) || (st = check_rows(v, ldv, kw, 16, true))) return st;
+    if (q && ((st = check_rows(q, ldq, qw, 16, true)) || (st = check_rows(q_out, ldqo, qw, 16, true)))) return st;
+    if (q ? q == q_out && ldq != ldqo : q_out != nullptr || q_norm != nullptr) return MOE_Q4_ERR_INVALID_ARG;
+    const AppendArgs a{static_cast<const uint16_t *>(q), static_cast<const uint16_t *>(k),
+                       static_cast<const uint16_t *>(v), ldq, ldk, ldv, q ? q_heads : 0, T, seq_start, n_seq,
+                       cache_of(cache), positions, inv_freq, rot_dim, interleaved != 0, q_norm, k_norm, eps,
+                       static_cast<uint16_t *>(q_out), ldqo};
+    return hip_status(launch_kv_append(a, reinterpret_cast<hipStream_t>(stream)));
+}
+
+size_t moe_q4_attention_workspace_size(int64_t T, int32_t n_seq, int32_t q_heads, const moe_q4_kv_cache *cache) {
+    if (T <= 0 || n_seq < 1 || check_cache(cache, q_heads) || !attention_sizes(T, n_seq, q_heads)) return 0;
+    return attention_workspace_bytes(T, n_seq, q_heads, cache_of(cache));
+}
+
+int moe_q4_attention(const void *q, int64_t ldq, int32_t q_heads, int64_t T, const int32_t *seq_start, int32_t n_seq,
+                     const moe_q4_kv_cache *cache, float scale, float cap, int32_t window, const float *slopes,
+                     const int32_t *prefix, const uint64_t *tree, void *o, int64_t ldo, void *ws, size_t ws_bytes,
+                     moe_q4_stream stream) {
+    int st = check_cache(cache, q_heads);
+    if (st) return st;
+    if (T < 0 || n_seq < 0 || window < 0 || !(cap >= 0.0f) || !std::isfinite(cap) || !std::isfinite(scale) ||
+        (tree && prefix))
+        return MOE_Q4_ERR_INVALID_ARG;
+    if (!attention_sizes(T, n_seq, q_heads)) return MOE_Q4_ERR_UNSUPPORTED;
+    if (T == 0 || n_seq == 0) return MOE_Q4_OK;
+    if (!seq_start || !aligned(seq_start, 4) || !aligned(slopes, 4) || !aligned(prefix, 4) || !aligned(tree, 8))
+        return MOE_Q4_ERR_INVALID_ARG;
+    if ((st = check_cache_pointers(cache))) return st;
+    const int64_t width = (int64_t)q_heads * cache->head_dim;
+    if ((st = check_rows(q, ldq, width, 16, true)) || (st = check_rows(o, ldo, width, 16, true))) return st;
+    const size_t need = moe_q4_attention_workspace_size(T, n_seq, q_heads, cache);
+    if (need && (!ws || ws_bytes < need)) return MOE_Q4_ERR_WORKSPACE;
+    if (need && !aligned(ws, 256)) return MOE_Q4_ERR_INVALID_ARG;
+    const AttentionArgs a{static_cast<const uint16_t *>(q), ldq, q_heads, T, seq_start, n_seq, cache_of(cache), scale,
+                          cap, window, slopes, prefix, tree, static_cast<uint16_t *>(o), ldo};
+    return hip_status(launch_attention(a, ws, reinterpret_cast<hipStream_t>(stream)));
+}
+
+int moe_q4_add_norm(const void *x, int64_t ldx, const void *u, int64_t ldu, int32_t u_dtype, int64_t T, int32_t H,
+                    const float *post_norm, const void *gate, int64_t ldg, int32_t gate_act, float scale,
+                    const float *pre_norm, float eps, void *x_out, int64_t ldxo, void *y, int64_t ldy,
+                    moe_q4_stream stream) {
+    if (T < 0 || H < 1 || !(eps >= 0.0f) || !std::isfinite(scale)) return MOE_Q4_ERR_INVALID_ARG;
+    if (H % 8 || H > 65536 || T >= 1 << 26 || T * H >= (int64_t)1 << 33) return MOE_Q4_ERR_UNSUPPORTED;
+    if (u_dtype != MOE_Q4_BF16 && u_dtype != MOE_Q4_F32) return MOE_Q4_ERR_UNSUPPORTED;
+    if (gate_act != MOE_Q4_ACT_NONE && gate_act != MOE_Q4_ACT_SILU && gate_act != MOE_Q4_ACT_SIGMOID)
+        return MOE_Q4_ERR_UNSUPPORTED;
+    if (T == 0) return MOE_Q4_OK;
+    if (!x && !u) return MOE_Q4_ERR_INVALID_ARG;
+    if (!u && (post_norm || gate)) return MOE_Q4_ERR_INVALID_ARG;
+    if ((pre_norm != nullptr) != (y != nullptr) || (!x_out && !y)) return MOE_Q4_ERR_INVALID_ARG;
+    if (!aligned(post_norm, 16) || !aligned(pre_norm, 16)) return MOE_Q4_ERR_INVALID_ARG;
+    int st = MOE_Q4_OK;
+    if (x) st = check_rows(x, ldx, H, 16, true);
+    if (!st && u) st = check_rows(u, ldu, H, 16, true);
+    if (!st && gate && ldg) st = check_rows(gate, ldg, H, 16, true);
+    if (!st && gate && !ldg && !aligned(gate, 16)) st = MOE_Q4_ERR_INVALID_ARG;
+    if (!st && x_out) st = check_rows(x_out, ldxo, H, 16, true);
+    if (!st && y) st = check_rows(y, ldy, H, 16, true);
+    if (st) return st;
+    if (x_out && ((x == x_out && ldx != ldxo) || x_out == y || u == x_out || gate == x_out)) return MOE_Q4_ERR_INVALID_ARG;
+    if (y && (x == y || u == y || gate == y)) return MOE_Q4_ERR_INVALID_ARG;
+    const AddNormArgs a{static_cast<const uint16_t *>(x), ldx, u, ldu, u_dtype == MOE_Q4_F32, T, H, post_norm,
+                        static_cast<const uint16_t *>(gate), ldg, gate_act, scale, pre_norm, eps,
+                        static_cast<uint16_t *>(x_out), ldxo, static_cast<uint16_t *>(y), ldy};
+    return hip_status(launch_add_norm(a, reinterpret_cast<hipStream_t>(stream)));
 }
 
 size_t moe_q4_logprobs_workspace_size(int64_t T, int64_t V, int32_t n_top) {
