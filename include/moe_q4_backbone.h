@@ -173,7 +173,7 @@ MOE_Q4_API int moe_q4_delta_prefill(const void *q, int64_t ldq, const void *k, i
  *               with an index below 0 or behind the table are not stored; keys
  *               behind the table are seen by nobody.
  * head_dim 64, 128 or 256; page_size a multiple of 16, max_pages * page_size
- * < 2^31; kv_heads at most 1024.
+ * at most 2^30; kv_heads at most 1024.
  */
 typedef struct moe_q4_kv_cache {
     int32_t kv_heads, head_dim;
@@ -245,7 +245,7 @@ MOE_Q4_API int moe_q4_kv_append(const void *q, int64_t ldq, int32_t q_heads, con
  *   ws         >= moe_q4_attention_workspace_size(T, n_seq, q_heads, cache)
  *              bytes, 256-byte aligned (may be NULL when that is 0)
  * scale, cap and the slopes must be finite, cap and window at least 0; q_heads a
- * multiple of kv_heads, at most 1024; T * q_heads < 2^26, n_seq < 2^20.
+ * multiple of kv_heads, at most 1024; T * q_heads < 2^26, n_seq < 2^20, n_seq * kv_heads < 2^22.
  * Rows behind the last sequence are neither read nor written.  Parts of a row's
  * keys are joined in a fixed order: the same input gives the same bits.  A NaN or
  * an infinity in a key or value reaches the queries that see it (some of their

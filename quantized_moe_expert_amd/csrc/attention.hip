@@ -1,85 +1,920 @@
-// Attention over the paged cache.
+// Attention over the paged cache:
+//   o = sum_j p_j v_j / sum_j p_j,  p_j = exp(s_j - max s),  s = cap tanh(scale q.k / cap) - slope |distance|.
 //
-// A simple form: one wave for each query row and head, the keys one after
-// another, running maximum and sum of the softmax in fp32.
+// The rows of a sequence that read one head of the cache (its tokens times the
+// query heads that share it, token by token) are cut into blocks, the keys that
+// a block sees into tiles.  Both kernels compute S^T = K Q^T and O^T = V^T P^T,
+// so that a lane has scores of one query and its weights are the second
+// product's operand where they are: they never leave the lane's registers.
+// Running maximum and sum of a row are fp32.
+//
+//   attention_rows_kernel  few rows in a sequence (single tokens): blocks of 16
+//       rows, every wave with key tiles of its own, K and V straight from memory
+//       into the operands.  Bound by the cache's bytes.
+//   attention_tile_kernel  more rows: blocks of 128 rows, 32 to a wave, tiles of
+//       keys shared through LDS.  Bound by the matrix products and the
+//       exponentials beside them.
+//   attention_join_kernel  joins the parts of blocks whose keys were split.
+//
+// How many workgroups share the keys of a block is decided on the device from
+// the sequences' lengths (plan_find), so that a captured call goes with them.
 #include "seq_dev.h"
 
 namespace moeq4 {
 
 namespace {
 
-constexpr int THREADS = 256;
+typedef __attribute__((__vector_size__(4 * sizeof(float)))) float f32x4_t;
+typedef __bf16 bf16v8_t __attribute__((ext_vector_type(8)));
+typedef short s16x4_t __attribute__((ext_vector_type(4)));
+typedef unsigned int u32x2_t __attribute__((ext_vector_type(2)));
+typedef __attribute__((address_space(3))) void lds_void;
 
-template <int D>
-__global__ __launch_bounds__(THREADS) void attention_kernel(AttentionArgs a) {
-    constexpr int E = D / WAVE;  // entries of a lane
-    const int64_t w = (int64_t)blockIdx.x * (THREADS / WAVE) + threadIdx.x / WAVE;
-    if (w >= a.T * a.hq) return;
-    const int64_t t = w / a.hq;
-    const int h = (int)(w % a.hq), hk = h / (a.hq / a.cache.hkv), lane = threadIdx.x & (WAVE - 1);
-    const int b = find_sequence(a.seq_start, a.n_seq, t);
-    if (b < 0) return;
-    const int64_t start = max(a.seq_start[b], 0), end = min((int64_t)a.seq_start[b + 1], a.T);
-    if (t >= end) return;
-    const int64_t kv = max(a.cache.kv_len[b], 0), n = end - start;
-    const int64_t len = min(kv, (int64_t)a.cache.max_pages * a.cache.page), before = kv - n, row = t - start;
-    const int64_t prefix = a.prefix ? a.prefix[b] : 0;
-    const uint64_t mask = a.tree ? a.tree[t] : 0;
-    const int64_t pos = a.tree ? before + __popcll(row < 64 ? mask & ~(1ull << row) : mask) : before + row;
-    const float slope = a.slopes ? a.slopes[h] : 0.0f;
-    float q[E], o[E];
-#pragma unroll
-    for (int e = 0; e < E; ++e) {
-        q[e] = bf16_to_f32(a.q[t * a.ldq + (int64_t)h * D + lane * E + e]);
-        o[e] = 0.0f;
+constexpr int THREADS = 256, WAVES = THREADS / WAVE;
+constexpr float LOG2E = 1.44269504088896340736f;
+// Rows are scaled to a new maximum when it is more than 2^RISE times the old
+// one: weights stay below 2^RISE, whose sums fp32 holds as well.
+constexpr float RISE = 8.0f;
+
+__device__ __forceinline__ f32x4_t mfma16(u32x4_t a, u32x4_t b, f32x4_t c) {
+    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16v8_t, a), __builtin_bit_cast(bf16v8_t, b),
+                                                   c, 0, 0, 0);
+}
+__device__ __forceinline__ f32x16_t mfma32(u32x4_t a, u32x4_t b, f32x16_t c) {
+    return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16v8_t, a), __builtin_bit_cast(bf16v8_t, b),
+                                                   c, 0, 0, 0);
+}
+__device__ __forceinline__ uint32_t pack_bf16x2(float a, float b) {
+    const bf16x2_t v = {(__bf16)a, (__bf16)b};
+    return __builtin_bit_cast(uint32_t, v);
+}
+// Largest value and sum over the lanes that hold one query: l, l ^ 32 and, of
+// 16 queries, l ^ 16 and l ^ 48.
+template <bool OF16>
+__device__ __forceinline__ float query_max(float v) {
+    if (OF16) {
+        const uint32_t a = __float_as_uint(v);
+        const u32x2_t p = __builtin_bit_cast(u32x2_t, __builtin_amdgcn_permlane16_swap(a, a, false, false));
+        v = fmaxf(__uint_as_float(p.x), __uint_as_float(p.y));
     }
-    float top = -INFINITY, sum = 0.0f;
-    for (int64_t i = 0; i < len; ++i) {
-        int64_t at = i;
-        bool seen;
-        if (a.tree && i >= before) {
-            const int64_t j = i - before;
-            seen = j < 64 && (mask >> j & 1);
-            if (!seen) continue;
-            at = before + __popcll(a.tree[start + j] & ~(1ull << j));
-            seen = !a.window || pos - at < a.window;
-        } else {
-            seen = (a.tree || i <= pos) && (!a.window || pos - i < a.window);
+    const uint32_t b = __float_as_uint(v);
+    const u32x2_t q = __builtin_bit_cast(u32x2_t, __builtin_amdgcn_permlane32_swap(b, b, false, false));
+    return fmaxf(__uint_as_float(q.x), __uint_as_float(q.y));
+}
+template <bool OF16>
+__device__ __forceinline__ float query_sum(float v) {
+    if (OF16) v += __shfl_xor(v, 16, WAVE);
+    return v + __shfl_xor(v, 32, WAVE);
+}
+__device__ __forceinline__ bool not_finite(u32x4_t w) {
+    bool bad = false;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) bad |= (w[i] & 0x7f80u) == 0x7f80u || (w[i] & 0x7f800000u) == 0x7f800000u;
+    return bad;
+}
+
+// ------------------------------------------------------------- sequences
+
+struct Seq {
+    int start, n;      // rows
+    int kv, len;       // tokens; those that the table has room for
+    int before, prefix;
+};
+__device__ __forceinline__ Seq load_seq(const AttentionArgs &a, int b) {
+    Seq s;
+    const int T = (int)a.T;
+    s.start = min(max(a.seq_start[b], 0), T);
+    s.n = min(max(a.seq_start[b + 1], s.start), T) - s.start;
+    s.kv = min(max(a.cache.kv_len[b], 0), 0x7fff0000);
+    s.len = min(s.kv, a.cache.max_pages * a.cache.page);
+    s.before = s.kv - s.n;
+    s.prefix = a.prefix ? min(max(a.prefix[b], 0), s.len) : 0;
+    return s;
+}
+
+// Tiles of n keys that rows i0 to i1 of a sequence see some of: those of the
+// prefix, [0, n1), and from lo on; tile j of them is j < n1 ? j : j - n1 + lo.
+struct Range {
+    int n1, lo, count;
+    __device__ __forceinline__ int tile(int j) const { return j < n1 ? j : j - n1 + lo; }
+};
+template <int N>
+__device__ __forceinline__ Range tiles_of(const AttentionArgs &a, const Seq &s, int i0, int i1) {
+    // A drafted token's position is from `before` on, and it may see all of the draft.
+    const int first = s.before + (a.tree ? 0 : i0);
+    const int hi = a.tree ? s.len : min(s.len, s.before + i1 + 1);
+    const int lo = a.window ? (int)max((int64_t)0, (int64_t)first - a.window + 1) : 0;
+    Range r;
+    const int end = hi > lo ? (hi + N - 1) / N : 0, begin = min(lo / N, end);
+    r.n1 = (s.prefix + N - 1) / N;
+    if (r.n1 >= begin) {
+        r.lo = r.n1;
+        r.count = max(end, r.n1);
+    } else {
+        r.lo = begin;
+        r.count = r.n1 + end - begin;
+    }
+    return r;
+}
+// Whether rows i0 to i1 see every key of [k0, k0 + n).
+template <int N>
+__device__ __forceinline__ bool sees_all(const AttentionArgs &a, const Seq &s, int i0, int i1, int k0) {
+    if (k0 + N > s.len) return false;
+    if (a.tree) return k0 + N <= s.before && (!a.window || s.before + WAVE - k0 < a.window);
+    return k0 + N <= s.prefix || (k0 + N - 1 <= s.before + i0 && (!a.window || s.before + i1 - k0 < a.window));
+}
+
+// What one query sees: keys lo to hi of all (tree: of the cached ones), and of
+// the draft's rows those in mask.
+struct Query {
+    int pos, lo, hi;
+    uint64_t mask;
+};
+// depth: of the draft's rows (load_depths).
+__device__ __forceinline__ Query load_query(const AttentionArgs &a, const Seq &s, const int *depth, int i) {
+    Query q;
+    q.mask = 0;
+    q.pos = s.before + i;
+    if (a.tree) {
+        q.mask = a.tree[s.start + i];
+        q.pos = s.before + __popcll(i < WAVE ? q.mask & ~(1ull << i) : q.mask);
+    }
+    q.hi = (a.tree ? min(s.before, s.len) : min(s.len, q.pos + 1)) - 1;
+    q.lo = a.window ? (int)max((int64_t)0, (int64_t)q.pos - a.window + 1) : 0;
+    if (a.tree && a.window)
+        for (int c = 0; c < WAVE; ++c)
+            if (s.before + depth[c] < q.lo) q.mask &= ~(1ull << c);
+    return q;
+}
+// Bits 0 to n - 1 of 64.
+__device__ __forceinline__ uint64_t below(int n) { return n >= 64 ? ~0ull : (1ull << max(n, 0)) - 1; }
+// Which of the 64 keys from k0 on the query sees.
+__device__ __forceinline__ uint64_t seen(const AttentionArgs &a, const Seq &s, const Query &q, int k0) {
+    uint64_t bits = (below(q.hi + 1 - k0) & ~below(q.lo - k0)) | below(s.prefix - k0);
+    if (a.tree) {
+        const int up = s.before - k0;
+        const uint64_t drafted = up >= 0 ? (up < 64 ? q.mask << up : 0) : (up > -64 ? q.mask >> -up : 0);
+        bits |= drafted & below(s.len - k0);
+    }
+    return bits;
+}
+// Position of a key.
+__device__ __forceinline__ int key_pos(const AttentionArgs &a, const Seq &s, const int *depth, int key) {
+    const int c = key - s.before;
+    return a.tree && c >= 0 ? s.before + depth[min(c, WAVE - 1)] : key;
+}
+__device__ __forceinline__ void load_depths(const AttentionArgs &a, const Seq &s, int *depth) {
+    const int c = threadIdx.x;
+    if (c < WAVE) depth[c] = c < s.n ? __popcll(a.tree[s.start + c] & ~(1ull << c)) : 0;
+    __syncthreads();
+}
+
+// ------------------------------------------------------------------ plan
+
+// A sequence of n rows has R = ceil(n r / rows) blocks (r query heads to a head
+// of the cache), each with at most m tiles of keys.  With C = max(cmin,
+// ceil(sum R m / target)) tiles to a part, a block has S = ceil(m / C) parts: at
+// most target + sum R parts in all, for each head of the cache, and at most
+// 2 target of blocks with more than one (m > C: S <= 2 m / C), whose sums go
+// through the workspace.
+struct Plan {
+    int rows, keys;    // of a block, of a tile
+    int cmin, target;
+    int items, joins, slots;  // most parts; most split blocks; most of their parts (each per head of the cache)
+};
+
+struct Found {
+    int b, block, part, parts, slot;
+    Seq seq;
+};
+
+__device__ __forceinline__ void blocks_of(const AttentionArgs &a, const Plan &p, const Seq &s, int &R, int &m) {
+    const int r = a.hq / a.cache.hkv;
+    R = (int)(((int64_t)s.n * r + p.rows - 1) / p.rows);
+    m = (s.len + p.keys - 1) / p.keys;
+    if (a.window) {
+        // Keys that some row of a block sees: the window and the block's tokens before it.
+        const int64_t span = (int64_t)a.window + (a.tree ? WAVE : p.rows / r + 1);
+        m = (int)min((int64_t)m, (s.prefix + p.keys - 1) / p.keys + span / p.keys + 2);
+    }
+    m = max(m, 1);
+}
+
+__device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
+
+__device__ __forceinline__ Seq uniform(const Seq &s) {
+    return Seq{uniform(s.start), uniform(s.n), uniform(s.kv), uniform(s.len), uniform(s.before), uniform(s.prefix)};
+}
+
+// Finds the part (JOIN: the split block) with this number; false: there are
+// fewer.  All threads of the workgroup call it.
+template <bool JOIN>
+__device__ __forceinline__ bool plan_find(const AttentionArgs &a, const Plan &p, int64_t item, Found &f) {
+    if (a.n_seq == 1) {
+        f.seq = load_seq(a, 0);
+        int R, m;
+        blocks_of(a, p, f.seq, R, m);
+        const int C = (int)max((int64_t)p.cmin, ((int64_t)R * m + p.target - 1) / p.target), S = (m + C - 1) / C;
+        if (item >= (int64_t)R * (JOIN ? 1 : S) || (JOIN && S == 1)) return false;
+        f.b = 0;
+        f.parts = S;
+        f.block = JOIN ? (int)item : R - 1 - (int)item / S;
+        f.part = JOIN ? 0 : (int)item % S;
+        f.slot = f.block * S;
+        return true;
+    }
+    __shared__ uint64_t part_sum[WAVES + 1];
+    __shared__ int found[5];
+    const int tid = threadIdx.x, lane = tid & (WAVE - 1), wave = tid / WAVE;
+    int R = 0, m = 0;
+    uint64_t work = 0;
+    for (int b = tid; b < a.n_seq; b += THREADS) {
+        blocks_of(a, p, load_seq(a, b), R, m);
+        work += (uint64_t)R * m;
+    }
+#pragma unroll
+    for (int o = WAVE / 2; o > 0; o >>= 1) work += __shfl_xor(work, o, WAVE);
+    if (lane == 0) part_sum[wave] = work;
+    if (tid == 0) found[0] = -1;
+    __syncthreads();
+    work = 0;
+#pragma unroll
+    for (int w = 0; w < WAVES; ++w) work += part_sum[w];
+    const int64_t C = max((int64_t)p.cmin, (int64_t)((work + p.target - 1) / p.target));
+    uint64_t carry = 0;  // parts (or split blocks) before, in the upper half; slots before, in the lower
+    for (int b0 = 0; b0 < a.n_seq; b0 += THREADS) {
+        const int b = b0 + tid;
+        int S = 0;
+        uint64_t mine = 0;
+        if (b < a.n_seq) {
+            blocks_of(a, p, load_seq(a, b), R, m);
+            S = (int)((m + C - 1) / C);
+            const uint32_t all = (uint32_t)R * S, split = S > 1 ? all : 0;
+            mine = (uint64_t)(JOIN ? (S > 1 ? R : 0) : all) << 32 | split;
         }
-        if (!seen && i >= prefix) continue;
-        const int page = a.cache.table[(int64_t)b * a.cache.max_pages + i / a.cache.page];
-        if (page < 0 || page >= a.cache.n_pages) continue;
-        const int64_t from = (((int64_t)page * a.cache.hkv + hk) * a.cache.page + i % a.cache.page) * D + lane * E;
-        float s = 0.0f;
+        uint64_t sum = mine;
 #pragma unroll
-        for (int e = 0; e < E; ++e) s = fmaf(q[e], bf16_to_f32(a.cache.k[from + e]), s);
-        s = seg_sum<WAVE>(s) * a.scale;
-        if (a.cap > 0.0f) s = a.cap * tanhf(s / a.cap);
-        s -= slope * (float)(pos > at ? pos - at : at - pos);
-        const float m = fmaxf(top, s), keep = expf(top - m), p = expf(s - m);
-        top = m;
-        sum = sum * keep + p;
+        for (int o = 1; o < WAVE; o <<= 1) {
+            const uint64_t v = __shfl_up(sum, o, WAVE);
+            if (lane >= o) sum += v;
+        }
+        __syncthreads();
+        if (lane == WAVE - 1) part_sum[wave] = sum;
+        __syncthreads();
+        uint64_t before = carry + sum - mine;
 #pragma unroll
-        for (int e = 0; e < E; ++e) o[e] = fmaf(p, bf16_to_f32(a.cache.v[from + e]), o[e] * keep);
+        for (int w = 0; w < WAVES; ++w) {
+            if (w < wave) before += part_sum[w];
+            carry += part_sum[w];
+        }
+        const int64_t at = item - (int64_t)(before >> 32);
+        if (at >= 0 && at < (int64_t)(mine >> 32)) {
+            const int block = JOIN ? (int)at : R - 1 - (int)at / S;
+            found[0] = b;
+            found[1] = block;
+            found[2] = JOIN ? 0 : (int)at % S;
+            found[3] = S;
+            found[4] = (int)(uint32_t)before + block * S;
+        }
+        __syncthreads();
+        if (uniform(found[0]) >= 0) break;
+    }
+    f.b = uniform(found[0]);
+    if (f.b < 0) return false;
+    f.block = uniform(found[1]);
+    f.part = uniform(found[2]);
+    f.parts = uniform(found[3]);
+    f.slot = uniform(found[4]);
+    f.seq = load_seq(a, f.b);
+    return true;
+}
+
+// A slot of the workspace: O [rows][d] over the part's own maximum, then the rows'
+// maxima (in powers of two) and sums.
+template <int D>
+__device__ __forceinline__ float *slot_of(float *ws, const Plan &p, int hkv, int64_t slot, int h) {
+    return ws + (slot * hkv + h) * ((int64_t)p.rows * (D + 2));
+}
+
+// --------------------------------------------------------------- few rows
+
+// K: A operand, row l % 16 a token, 8 entries from 8 (l / 16) on: 16 bytes from
+// memory.  Scores: lane l has query l % 16 and tokens 4 (l / 16) + 0..3 of each
+// 16.  V: the same four tokens, VE entries each; four byte permutes turn two
+// times four tokens of one entry into an operand, whose 16 rows are the entries
+// VE apart.  No LDS before the waves' sums are joined, no barrier: each wave keeps
+// K and V of a tile (D / 2 KB) in flight while it works on the other.
+//
+// The weights enter the second product as two bf16, value and remainder (16
+// bits): the matrix cores have time to spare here.
+template <int D, bool EXTRA>
+__global__ __launch_bounds__(THREADS, 2) void attention_rows_kernel(AttentionArgs a, Plan p, float *ws) {
+    constexpr int N = 32, ROWS = 16;
+    constexpr int KS = D / 32;                       // steps of the first product
+    constexpr int VE = D >= 128 ? 8 : 4, VU = D / (16 * VE);
+    constexpr int PITCH = D + 4;
+    __shared__ float o_part[WAVES][ROWS][PITCH];
+    __shared__ float m_part[WAVES][ROWS], l_part[WAVES][ROWS];
+    __shared__ int depth[WAVE];
+    const int hk = blockIdx.x % a.cache.hkv;
+    Found f;
+    if (!plan_find<false>(a, p, blockIdx.x / a.cache.hkv, f)) return;
+    const Seq s = uniform(f.seq);
+    if (a.tree) load_depths(a, s, depth);
+    const int lane = threadIdx.x & (WAVE - 1), wave = __builtin_amdgcn_readfirstlane(threadIdx.x / WAVE);
+    const int c = lane % 16, g = lane / 16;
+    const int r = a.hq / a.cache.hkv;
+    const int rows = s.n * r, row0 = f.block * ROWS;  // (T * hq < 2^26)
+    const int row = min(row0 + c, rows - 1);
+    const int i = row / r, head = hk * r + row % r;
+    const int i0 = uniform(row0 / r), i1 = uniform((min(row0 + ROWS, rows) - 1) / r);
+    const Range range = tiles_of<N>(a, s, i0, i1);
+    const int per = uniform((range.count + f.parts - 1) / f.parts);
+    const int j_end = min(range.count, (f.part + 1) * per);
+    const Query query = load_query(a, s, depth, i);
+    const float scale2 = a.cap > 0.0f ? a.scale / a.cap : a.scale * LOG2E;
+    const float cap2 = a.cap * LOG2E;
+    const float slope2 = EXTRA && a.slopes ? a.slopes[head] * LOG2E : 0.0f;
+
+    u32x4_t q[KS];
+    {
+        const uint16_t *src = a.q + (int64_t)(s.start + i) * a.ldq + (int64_t)head * D + 8 * g;
+#pragma unroll
+        for (int k = 0; k < KS; ++k) q[k] = *reinterpret_cast<const u32x4_t *>(src + 32 * k);
+    }
+    f32x4_t o[VU * VE];
+#pragma unroll
+    for (int n = 0; n < VU * VE; ++n) o[n] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
+    float m_ref = -INFINITY, l_sum = 0.0f;
+
+    // Where the two blocks of 16 tokens of this wave's next 64 tiles lie: lane l has
+    // the l-th tile's, as heads' tokens from the pool's start on (the memory's size keeps them below 2^32).
+    const int32_t *table = a.cache.table + (int64_t)f.b * a.cache.max_pages;
+    const int last16 = max(s.len - 1, 0) / 16;
+    uint32_t block_at[2];
+    uint64_t page_ok[2];
+    auto load_pages = [&](int j) {
+        const int k16 = 2 * range.tile(min(j + WAVES * lane, range.count - 1));
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+            const int k = 16 * min(k16 + t, last16), page = k / a.cache.page;
+            const int id = table[page];
+            const bool ok = id >= 0 && id < a.cache.n_pages;
+            page_ok[t] = __ballot(ok);
+            block_at[t] = (uint32_t)((ok ? id : 0) * a.cache.hkv + hk) * a.cache.page + (k - page * a.cache.page);
+        }
+    };
+    typedef __attribute__((ext_vector_type(VE / 2))) uint32_t vload_t;
+    u32x4_t kr[2][KS];
+    vload_t vr[2][4][VU];
+    auto block = [&](int u, int t) { return (int64_t)(uint32_t)__builtin_amdgcn_readlane(block_at[t], u) * D; };
+    auto load_k = [&](int64_t b0, int64_t b1) {
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+            const uint16_t *src = a.cache.k + (t ? b1 : b0) + c * D + 8 * g;
+#pragma unroll
+            for (int k = 0; k < KS; ++k) kr[t][k] = *reinterpret_cast<const u32x4_t *>(src + 32 * k);
+        }
+    };
+    auto load_v = [&](int64_t b0, int64_t b1) {
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+            const uint16_t *src = a.cache.v + (t ? b1 : b0) + 4 * g * D + VE * c;
+#pragma unroll
+            for (int x = 0; x < 4; ++x)
+#pragma unroll
+                for (int u = 0; u < VU; ++u)
+                    vr[t][x][u] = *reinterpret_cast<const vload_t *>(src + x * D + 16 * VE * u);
+        }
+    };
+    int j = f.part * per + wave, at = 0;
+    if (j < j_end) {
+        load_pages(j);
+        const int64_t b0 = block(0, 0), b1 = block(0, 1);
+        load_k(b0, b1);
+        load_v(b0, b1);
+    }
+    for (; j < j_end; j += WAVES) {
+        const int k0 = N * range.tile(j);
+        const bool ok0 = page_ok[0] >> at & 1, ok1 = page_ok[1] >> at & 1;
+        f32x4_t acc[2];
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+            acc[t] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+            for (int k = 0; k < KS; ++k) acc[t] = mfma16(kr[t][k], q[k], acc[t]);
+        }
+        // The next tile's keys (past the end the same ones again).
+        const int next = j + WAVES < j_end ? j + WAVES : j;
+        if (next != j && ++at == WAVE) {
+            load_pages(next);
+            at = 0;
+        }
+        const int64_t b0 = block(at, 0), b1 = block(at, 1);
+        load_k(b0, b1);
+
+        const bool whole = ok0 && ok1 && sees_all<N>(a, s, i0, i1, k0);
+        float sc[8];
+#pragma unroll
+        for (int t = 0; t < 2; ++t)
+#pragma unroll
+            for (int x = 0; x < 4; ++x) {
+                float v = acc[t][x] * scale2;
+                if (EXTRA) {
+                    if (a.cap > 0.0f) v = cap2 * (1.0f - 2.0f * __builtin_amdgcn_rcpf(1.0f + __expf(2.0f * v)));
+                    if (a.slopes) {
+                        const int gap = query.pos - key_pos(a, s, depth, k0 + 16 * t + 4 * g + x);
+                        v -= slope2 * fabsf((float)gap);
+                    }
+                }
+                sc[4 * t + x] = v;
+            }
+        if (!whole) {
+            const uint32_t there = (ok0 ? 0xffffu : 0u) | (ok1 ? 0xffff0000u : 0u);
+            const uint32_t bits = ((uint32_t)seen(a, s, query, k0) & there) >> (4 * g);
+#pragma unroll
+            for (int x = 0; x < 8; ++x) sc[x] = bits >> (16 * (x / 4) + x % 4) & 1 ? sc[x] : -INFINITY;
+        }
+        float top = sc[0];
+#pragma unroll
+        for (int x = 1; x < 8; ++x) top = fmaxf(top, sc[x]);
+        top = query_max<true>(top);
+        if (__any(top > m_ref + RISE)) {
+            const float m_new = fmaxf(m_ref, top);
+            const float keep = m_new == -INFINITY ? 1.0f : __builtin_amdgcn_exp2f(m_ref - m_new);
+            l_sum *= keep;
+#pragma unroll
+            for (int n = 0; n < VU * VE; ++n) o[n] *= keep;
+            m_ref = m_new;
+        }
+        const float m_use = m_ref == -INFINITY ? 0.0f : m_ref;
+        float w[8];
+#pragma unroll
+        for (int x = 0; x < 8; ++x) {
+            w[x] = __builtin_amdgcn_exp2f(sc[x] - m_use);
+            l_sum += w[x];
+        }
+        if (!whole) {
+            // 0 times NaN or infinity: values of keys that some row does not see are
+            // cleared, and the rows that see one get NaN for it.
+#pragma unroll
+            for (int t = 0; t < 2; ++t)
+#pragma unroll
+                for (int x = 0; x < 4; ++x) {
+                    bool bad = false;
+#pragma unroll
+                    for (int u = 0; u < VU; ++u) {
+                        bool b = false;
+#pragma unroll
+                        for (int e = 0; e < VE / 2; ++e)
+                            b |= (vr[t][x][u][e] & 0x7f80u) == 0x7f80u || (vr[t][x][u][e] & 0x7f800000u) == 0x7f800000u;
+                        if (b) vr[t][x][u] = vload_t(0u);
+                        bad |= b;
+                    }
+                    // (The lanes with the same four tokens are 16 neighbours.)
+                    if ((__ballot(bad) >> (16 * g) & 0xffffu) && sc[4 * t + x] != -INFINITY) w[4 * t + x] = NAN;
+                }
+        }
+        u32x4_t hi, lo;
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+            hi[x] = pack_bf16x2(w[2 * x], w[2 * x + 1]);
+            lo[x] = pack_bf16x2(w[2 * x] - __uint_as_float(hi[x] << 16),
+                                w[2 * x + 1] - __uint_as_float(hi[x] & 0xffff0000u));
+        }
+#pragma unroll
+        for (int u = 0; u < VU; ++u)
+#pragma unroll
+            for (int e = 0; e < VE; ++e) {
+                const uint32_t sel = e & 1 ? 0x07060302u : 0x05040100u;
+                u32x4_t v;
+#pragma unroll
+                for (int x = 0; x < 4; ++x)
+                    v[x] = __builtin_amdgcn_perm(vr[x / 2][2 * (x & 1) + 1][u][e / 2], vr[x / 2][2 * (x & 1)][u][e / 2], sel);
+                o[VE * u + e] = mfma16(v, hi, o[VE * u + e]);
+                o[VE * u + e] = mfma16(v, lo, o[VE * u + e]);
+            }
+        load_v(b0, b1);
+    }
+
+    // The waves' parts over their common maximum.
+    l_sum = query_sum<true>(l_sum);
+    if (g == 0) {
+        m_part[wave][c] = m_ref;
+        l_part[wave][c] = l_sum;
     }
 #pragma unroll
-    for (int e = 0; e < E; ++e)
-        a.o[t * a.ldo + (int64_t)h * D + lane * E + e] = f32_to_bf16_rne(sum == 0.0f ? 0.0f : o[e] / sum);
+    for (int u = 0; u < VU; ++u)
+#pragma unroll
+        for (int x = 0; x < 4; ++x)
+#pragma unroll
+            for (int e = 0; e < VE; e += 4) {
+                const float4 v = {o[VE * u + e][x], o[VE * u + e + 1][x], o[VE * u + e + 2][x], o[VE * u + e + 3][x]};
+                *reinterpret_cast<float4 *>(&o_part[wave][c][16 * VE * u + VE * (4 * g + x) + e]) = v;
+            }
+    __syncthreads();
+    const int live = min(ROWS, rows - row0);
+    const bool direct = f.parts == 1;
+    const int64_t slot = (int64_t)f.slot + f.part;
+    if (!direct && slot >= p.slots) return;  // (starts that do not ascend)
+    float *out = direct ? nullptr : slot_of<D>(ws, p, a.cache.hkv, slot, hk);
+    for (int x = threadIdx.x; x < live * (D / 4); x += THREADS) {
+        const int rr = x / (D / 4), d = 4 * (x % (D / 4));
+        float top = m_part[0][rr];
+#pragma unroll
+        for (int w = 1; w < WAVES; ++w) top = fmaxf(top, m_part[w][rr]);
+        float sum = 0.0f;
+        float4 v = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+        for (int w = 0; w < WAVES; ++w) {
+            const float mw = m_part[w][rr];
+            const float k = mw == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(mw - top);
+            const float4 y = *reinterpret_cast<const float4 *>(&o_part[w][rr][d]);
+            sum = fmaf(k, l_part[w][rr], sum);
+            v.x = fmaf(k, y.x, v.x), v.y = fmaf(k, y.y, v.y), v.z = fmaf(k, y.z, v.z), v.w = fmaf(k, y.w, v.w);
+        }
+        if (direct) {
+            const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+            const int rw = row0 + rr;
+            uint16_t *dst = a.o + (int64_t)(s.start + rw / r) * a.ldo + (int64_t)(hk * r + rw % r) * D + d;
+            *reinterpret_cast<uint2 *>(dst) = uint2{pack_bf16x2(v.x * inv, v.y * inv), pack_bf16x2(v.z * inv, v.w * inv)};
+        } else {
+            *reinterpret_cast<float4 *>(out + rr * D + d) = v;
+            if (d == 0) {
+                out[ROWS * D + rr] = top;
+                out[ROWS * D + ROWS + rr] = sum;
+            }
+        }
+    }
+}
+
+// ------------------------------------------------------------------- join
+
+// Rows of split blocks: 1024 / D rows to a workgroup, four entries to a thread.
+template <int D>
+__global__ __launch_bounds__(THREADS) void attention_join_kernel(AttentionArgs a, Plan p, float *ws) {
+    constexpr int JR = THREADS / (D / 4);
+    const int groups = p.rows / JR;
+    const int64_t x = blockIdx.x / a.cache.hkv;
+    const int hk = blockIdx.x % a.cache.hkv;
+    Found f;
+    if (!plan_find<true>(a, p, x / groups, f)) return;
+    const Seq s = f.seq;
+    const int r = a.hq / a.cache.hkv;
+    const int rr = (int)(x % groups) * JR + threadIdx.x / (D / 4), d = 4 * (threadIdx.x % (D / 4));
+    const int row = f.block * p.rows + rr;
+    if (row >= s.n * r || (int64_t)f.slot + f.parts > p.slots) return;
+    const int64_t stride = (int64_t)a.cache.hkv * p.rows * (D + 2);
+    const float *part = slot_of<D>(ws, p, a.cache.hkv, f.slot, hk);
+    const float *ms = part + p.rows * D + rr, *ls = ms + p.rows;
+    float top = -INFINITY;
+    for (int i = 0; i < f.parts; ++i) top = fmaxf(top, ms[i * stride]);
+    float sum = 0.0f;
+    float4 v = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll 4
+    for (int i = 0; i < f.parts; ++i) {
+        const float mi = ms[i * stride];
+        const float k = mi == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(mi - top);
+        const float4 y = *reinterpret_cast<const float4 *>(part + i * stride + rr * D + d);
+        sum = fmaf(k, ls[i * stride], sum);
+        v.x = fmaf(k, y.x, v.x), v.y = fmaf(k, y.y, v.y), v.z = fmaf(k, y.z, v.z), v.w = fmaf(k, y.w, v.w);
+    }
+    const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+    uint16_t *dst = a.o + (int64_t)(s.start + row / r) * a.ldo + (int64_t)(hk * r + row % r) * D + d;
+    *reinterpret_cast<uint2 *>(dst) = uint2{pack_bf16x2(v.x * inv, v.y * inv), pack_bf16x2(v.z * inv, v.w * inv)};
+}
+
+// -------------------------------------------------------------- more rows
+
+constexpr int TILE_ROWS = 128;
+__host__ __device__ constexpr int tile_keys(int d) { return d <= 128 ? 64 : 32; }
+
+// This wave's vector-memory (LDS) operations are done; the fences keep memory
+// operations from moving over the waits.
+#define FENCE() asm volatile("" ::: "memory")
+__device__ __forceinline__ void wait_loads() {
+    FENCE();
+    __builtin_amdgcn_s_waitcnt((0x7 << 4) | (0xf << 8));  // vmcnt(0)
+    FENCE();
+}
+__device__ __forceinline__ void wait_lds() {
+    FENCE();
+    __builtin_amdgcn_s_waitcnt(0xf | (0x3 << 14) | (0x7 << 4));  // lgkmcnt(0)
+    FENCE();
+}
+__device__ __forceinline__ void lds_barrier() {
+    FENCE();
+    __builtin_amdgcn_s_barrier();
+    FENCE();
+}
+
+// Four 16-bit entries at p and those of the 15 lanes beside it as a 16 x 4 block,
+// transposed: lane l % 16 gets column l % 16 of four rows.
+__device__ __forceinline__ u32x2_t read_transposed(const u32x4_t *lds, int byte) {
+    typedef __attribute__((address_space(3))) s16x4_t lds_s16x4;
+    const auto *p = reinterpret_cast<const char *>(lds) + byte;
+    return __builtin_bit_cast(u32x2_t, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4 *)(lds_void *)p));
+}
+
+// K: A operand of 32 x 32 x 16, row l % 32 a key.  Scores: lane l has query l % 32
+// and of each 8 keys 4 (l / 32) + 0..3.  V: transposed reads bring those four keys
+// of one entry to a lane.
+//
+// Tiles come by direct loads to LDS, two buffers, each an array of its own (so
+// that the compiler sees that loads into one and reads of another do not meet);
+// one barrier a tile: behind it the tile is there and the other buffer is free.
+// 16-byte chunks of a row are permuted by the row number (the source address
+// carries it), so that reads spread over the banks.
+//
+// The weights are rounded to bf16 for the second product (half a step, 2^-8 of a
+// weight, random over the keys); their sum is that of the unrounded ones.
+template <int D, bool EXTRA>
+__global__ __launch_bounds__(THREADS, 2) void attention_tile_kernel(AttentionArgs a, Plan p, float *ws) {
+    constexpr int N = tile_keys(D), CH = D / 8, KT = N / 32, DS = D / 16, DT = D / 32, NB = N / 16;
+    constexpr int LOADS = N * CH / THREADS;
+    __shared__ u32x4_t k_a[N * CH], k_b[N * CH], v_a[N * CH], v_b[N * CH];
+    __shared__ uint32_t bad_a[2], bad_b[2];
+    __shared__ int depth[WAVE];
+    const int hk = blockIdx.x % a.cache.hkv;
+    Found f;
+    if (!plan_find<false>(a, p, blockIdx.x / a.cache.hkv, f)) return;
+    const Seq s = uniform(f.seq);
+    if (a.tree) load_depths(a, s, depth);
+    const int tid = threadIdx.x, lane = tid & (WAVE - 1), wave = __builtin_amdgcn_readfirstlane(tid / WAVE);
+    const int c = lane % 32, hh = lane / 32;
+    const int r = a.hq / a.cache.hkv;
+    const int rows = s.n * r, row0 = f.block * TILE_ROWS;
+    const int my_row = row0 + wave * 32 + c, row = min(my_row, rows - 1);
+    const int i = row / r, head = hk * r + row % r;
+    const int i0 = uniform(row0 / r), i1 = uniform((min(row0 + TILE_ROWS, rows) - 1) / r);
+    const Range range = tiles_of<N>(a, s, i0, i1);
+    const int per = uniform((range.count + f.parts - 1) / f.parts);
+    const int j0 = f.part * per, j_end = min(range.count, j0 + per);
+    const Query query = load_query(a, s, depth, i);
+    const float scale2 = a.cap > 0.0f ? a.scale / a.cap : a.scale * LOG2E;
+    const float cap2 = a.cap * LOG2E;
+    const float slope2 = EXTRA && a.slopes ? a.slopes[head] * LOG2E : 0.0f;
+
+    u32x4_t q[DS];
+    {
+        const uint16_t *src = a.q + (int64_t)(s.start + i) * a.ldq + (int64_t)head * D + 8 * hh;
+#pragma unroll
+        for (int k = 0; k < DS; ++k) q[k] = *reinterpret_cast<const u32x4_t *>(src + 16 * k);
+    }
+    f32x16_t o[DT];
+#pragma unroll
+    for (int n = 0; n < DT; ++n)
+#pragma unroll
+        for (int x = 0; x < 16; ++x) o[n][x] = 0.0f;
+    float m_ref = -INFINITY, l_sum = 0.0f;
+
+    // Where this thread's chunks of a tile come from: entries from the first of 16 tokens on.
+    int k_from[LOADS], v_from[LOADS];
+    auto k_swizzle = [](int row) { return D == 64 ? row >> 1 & 7 : row & 15; };
+    auto v_swizzle = [](int row) { return D == 64 ? (row >> 1 & 1) << 2 : (row & 3) << 2; };
+#pragma unroll
+    for (int x = 0; x < LOADS; ++x) {
+        const int at = (wave * LOADS + x) * WAVE + lane, key = at / CH, pos = at % CH;
+        k_from[x] = key % 16 * D + 8 * (pos ^ k_swizzle(key));
+        v_from[x] = key % 16 * D + 8 * (pos ^ v_swizzle(key));
+    }
+    // A wave loads keys of one block of 16.  Where it lies in the next 64 tiles
+    // (attention_rows_kernel), and which blocks of them are there.
+    const int my_block = wave * (N / WAVES) / 16;
+    const int32_t *table = a.cache.table + (int64_t)f.b * a.cache.max_pages;
+    const int last16 = max(s.len - 1, 0) / 16;
+    int from_tile = j0;
+    uint32_t block_at = 0;
+    uint64_t page_ok[NB];
+    auto load_pages = [&](int j) {
+        const int k16 = NB * range.tile(min(j + lane, range.count - 1));
+#pragma unroll
+        for (int t = 0; t < NB; ++t) {
+            const int k = 16 * min(k16 + t, last16), page = k / a.cache.page;
+            const int id = table[page];
+            const bool ok = id >= 0 && id < a.cache.n_pages;
+            page_ok[t] = __ballot(ok);
+            if (t == my_block)
+                block_at = (uint32_t)((ok ? id : 0) * a.cache.hkv + hk) * a.cache.page + (k - page * a.cache.page);
+        }
+        from_tile = j;
+    };
+    auto load = [&](int j, u32x4_t *kd, u32x4_t *vd) {
+        const int64_t block = (int64_t)(uint32_t)__builtin_amdgcn_readlane(block_at, j - from_tile) * D;
+        const uint16_t *ks = a.cache.k + block, *vs = a.cache.v + block;
+#pragma unroll
+        for (int x = 0; x < LOADS; ++x)
+            __builtin_amdgcn_global_load_lds((const void *)(ks + k_from[x]),
+                                             (lds_void *)(kd + (wave * LOADS + x) * WAVE), 16, 0, 0);
+#pragma unroll
+        for (int x = 0; x < LOADS; ++x)
+            __builtin_amdgcn_global_load_lds((const void *)(vs + v_from[x]),
+                                             (lds_void *)(vd + (wave * LOADS + x) * WAVE), 16, 0, 0);
+    };
+    auto step = [&](int j, u32x4_t *kb, u32x4_t *vb, u32x4_t *kn, u32x4_t *vn, uint32_t *bad) {
+        const int k0 = N * range.tile(j);
+        uint32_t there = 0;
+#pragma unroll
+        for (int t = 0; t < NB; ++t) there |= (uint32_t)(page_ok[t] >> (j - from_tile) & 1) << t;
+        const bool whole = there == (1u << NB) - 1 && sees_all<N>(a, s, i0, i1, k0);
+        if (!whole && tid < 2) bad[tid] = 0;
+        if (!whole) wait_lds();
+        wait_loads();
+        lds_barrier();
+        const int next = j + 1;
+        if (next < j_end) {
+            if (next - from_tile == WAVE) load_pages(next);
+            load(next, kn, vn);
+        }
+        if (!whole) {
+            // 0 times NaN or infinity: values of keys that some row does not see are
+            // cleared, and the rows that see one get NaN for it.
+#pragma unroll
+            for (int x = 0; x < LOADS; ++x) {
+                const int at = (wave * LOADS + x) * WAVE + lane, key = at / CH;
+                if (not_finite(vb[at])) {
+                    vb[at] = u32x4_t{0, 0, 0, 0};
+                    atomicOr(&bad[key / 32], 1u << key % 32);
+                }
+            }
+            wait_lds();
+            lds_barrier();
+        }
+        f32x16_t sc[KT];
+#pragma unroll
+        for (int t = 0; t < KT; ++t) {
+#pragma unroll
+            for (int x = 0; x < 16; ++x) sc[t][x] = 0.0f;
+            const int key = 32 * t + c;
+#pragma unroll
+            for (int k = 0; k < DS; ++k) sc[t] = mfma32(kb[key * CH + ((2 * k + hh) ^ k_swizzle(key))], q[k], sc[t]);
+        }
+#pragma unroll
+        for (int t = 0; t < KT; ++t)
+#pragma unroll
+            for (int x = 0; x < 16; ++x) {
+                float v = sc[t][x] * scale2;
+                if (EXTRA) {
+                    if (a.cap > 0.0f) v = cap2 * (1.0f - 2.0f * __builtin_amdgcn_rcpf(1.0f + __expf(2.0f * v)));
+                    if (a.slopes) {
+                        const int gap = query.pos - key_pos(a, s, depth, k0 + 32 * t + 8 * (x / 4) + 4 * hh + x % 4);
+                        v -= slope2 * fabsf((float)gap);
+                    }
+                }
+                sc[t][x] = v;
+            }
+        if (!whole) {
+            uint64_t all = seen(a, s, query, k0);
+#pragma unroll
+            for (int t = 0; t < NB; ++t)
+                if (!(there >> t & 1)) all &= ~(0xffffull << (16 * t));
+#pragma unroll
+            for (int t = 0; t < KT; ++t) {
+                const uint32_t bits = (uint32_t)(all >> (32 * t)) >> (4 * hh);
+#pragma unroll
+                for (int x = 0; x < 16; ++x) sc[t][x] = bits >> (8 * (x / 4) + x % 4) & 1 ? sc[t][x] : -INFINITY;
+            }
+        }
+        float top = -INFINITY;
+#pragma unroll
+        for (int t = 0; t < KT; ++t)
+#pragma unroll
+            for (int x = 0; x < 16; ++x) top = fmaxf(top, sc[t][x]);
+        top = query_max<false>(top);
+        if (__any(top > m_ref + RISE)) {
+            const float m_new = fmaxf(m_ref, top);
+            const float keep = m_new == -INFINITY ? 1.0f : __builtin_amdgcn_exp2f(m_ref - m_new);
+            l_sum *= keep;
+#pragma unroll
+            for (int n = 0; n < DT; ++n)
+#pragma unroll
+                for (int x = 0; x < 16; ++x) o[n][x] *= keep;
+            m_ref = m_new;
+        }
+        const float m_use = m_ref == -INFINITY ? 0.0f : m_ref;
+        u32x4_t w[KT][2];
+        uint32_t spoiled[KT];
+#pragma unroll
+        for (int t = 0; t < KT; ++t) spoiled[t] = whole ? 0u : bad[t];
+#pragma unroll
+        for (int t = 0; t < KT; ++t) {
+            float e[16];
+#pragma unroll
+            for (int x = 0; x < 16; ++x) {
+                e[x] = __builtin_amdgcn_exp2f(sc[t][x] - m_use);
+                l_sum += e[x];
+            }
+            if (spoiled[t]) {
+#pragma unroll
+                for (int x = 0; x < 16; ++x)
+                    if (spoiled[t] >> (8 * (x / 4) + 4 * hh + x % 4) & 1 && sc[t][x] != -INFINITY) e[x] = NAN;
+            }
+#pragma unroll
+            for (int x = 0; x < 8; ++x) w[t][x / 4][x % 4] = pack_bf16x2(e[2 * x], e[2 * x + 1]);
+        }
+#pragma unroll
+        for (int t = 0; t < KT; ++t)
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+                const int key = 32 * t + 16 * u + 4 * hh + lane % 16 / 4;
+#pragma unroll
+                for (int n = 0; n < DT; ++n) {
+                    const int chunk = 4 * n + (lane / 16 % 2) * 2 + lane % 4 / 2;
+                    const int byte = (key * CH + (chunk ^ v_swizzle(key))) * 16 + lane % 2 * 8;
+                    const u32x2_t x = read_transposed(vb, byte), y = read_transposed(vb, byte + 8 * CH * 16);
+                    o[n] = mfma32(u32x4_t{x[0], x[1], y[0], y[1]}, w[t][u], o[n]);
+                }
+            }
+    };
+    if (j0 < j_end) {
+        load_pages(j0);
+        load(j0, k_a, v_a);
+        for (int j = j0; j < j_end; j += 2) {
+            step(j, k_a, v_a, k_b, v_b, bad_a);
+            if (j + 1 == j_end) break;
+            step(j + 1, k_b, v_b, k_a, v_a, bad_b);
+        }
+    }
+    l_sum = query_sum<false>(l_sum);
+    if (my_row >= rows) return;
+    if (f.parts == 1) {
+        const float inv = l_sum == 0.0f ? 0.0f : 1.0f / l_sum;
+        uint16_t *dst = a.o + (int64_t)(s.start + i) * a.ldo + (int64_t)head * D + 4 * hh;
+#pragma unroll
+        for (int n = 0; n < DT; ++n)
+#pragma unroll
+            for (int x = 0; x < 4; ++x)
+                *reinterpret_cast<uint2 *>(dst + 32 * n + 8 * x) =
+                    uint2{pack_bf16x2(o[n][4 * x] * inv, o[n][4 * x + 1] * inv),
+                          pack_bf16x2(o[n][4 * x + 2] * inv, o[n][4 * x + 3] * inv)};
+        return;
+    }
+    const int64_t slot = (int64_t)f.slot + f.part;
+    if (slot >= p.slots) return;  // (starts that do not ascend)
+    const int rr = wave * 32 + c;
+    float *out = slot_of<D>(ws, p, a.cache.hkv, slot, hk);
+#pragma unroll
+    for (int n = 0; n < DT; ++n)
+#pragma unroll
+        for (int x = 0; x < 4; ++x)
+            *reinterpret_cast<float4 *>(out + rr * D + 32 * n + 8 * x + 4 * hh) =
+                float4{o[n][4 * x], o[n][4 * x + 1], o[n][4 * x + 2], o[n][4 * x + 3]};
+    if (hh == 0) {
+        out[TILE_ROWS * D + rr] = m_ref;
+        out[TILE_ROWS * D + TILE_ROWS + rr] = l_sum;
+    }
+}
+
+// ------------------------------------------------------------------ launch
+
+// Which kernel, and how its parts are cut.
+bool few_rows(int64_t T, int n_seq, int r) { return T * r <= (int64_t)16 * n_seq; }
+
+Plan make_plan(int64_t T, int n_seq, int hq, const Cache &c) {
+    const int r = hq / c.hkv;
+    Plan p;
+    const bool few = few_rows(T, n_seq, r);
+    p.rows = few ? 16 : TILE_ROWS;
+    p.keys = few ? 32 : tile_keys(c.d);
+    p.cmin = few ? WAVES : 8;
+    p.target = max(1, 512 / c.hkv);
+    const int64_t blocks = T * r / p.rows + min(T, (int64_t)n_seq);
+    const int64_t tiles = ((int64_t)c.max_pages * c.page + p.keys - 1) / p.keys;
+    const int64_t parts = (tiles + p.cmin - 1) / p.cmin;  // of one block, at most
+    p.items = (int)min(blocks * parts, blocks + p.target);
+    p.joins = parts > 1 ? (int)min(blocks, (int64_t)p.target) : 0;
+    p.slots = parts > 1 ? (int)min(blocks * parts, (int64_t)2 * p.target) : 0;
+    return p;
+}
+
+template <int D, bool EXTRA>
+hipError_t launch(const AttentionArgs &a, const Plan &p, float *ws, hipStream_t s) {
+    const dim3 grid((unsigned)((int64_t)p.items * a.cache.hkv));
+    if (p.rows == 16)
+        attention_rows_kernel<D, EXTRA><<<grid, THREADS, 0, s>>>(a, p, ws);
+    else
+        attention_tile_kernel<D, EXTRA><<<grid, THREADS, 0, s>>>(a, p, ws);
+    hipError_t e = hipGetLastError();
+    if (e != hipSuccess || !p.joins) return e;
+    const unsigned groups = p.rows * (D / 4) / THREADS;
+    attention_join_kernel<D><<<dim3((unsigned)((int64_t)p.joins * groups * a.cache.hkv)), THREADS, 0, s>>>(a, p, ws);
+    return hipGetLastError();
 }
 
 }  // namespace
 
-size_t attention_workspace_bytes(int64_t, int, int, const Cache &) { return 0; }
+size_t attention_workspace_bytes(int64_t T, int n_seq, int hq, const Cache &c) {
+    const Plan p = make_plan(T, n_seq, hq, c);
+    return (size_t)p.slots * c.hkv * p.rows * (c.d + 2) * sizeof(float);
+}
 
-hipError_t launch_attention(const AttentionArgs &a, void *, hipStream_t s) {
-    const dim3 grid((unsigned)((a.T * a.hq + THREADS / WAVE - 1) / (THREADS / WAVE)));
-    if (a.cache.d == 64)
-        attention_kernel<64><<<grid, THREADS, 0, s>>>(a);
-    else if (a.cache.d == 128)
-        attention_kernel<128><<<grid, THREADS, 0, s>>>(a);
-    else
-        attention_kernel<256><<<grid, THREADS, 0, s>>>(a);
-    return hipGetLastError();
+hipError_t launch_attention(const AttentionArgs &a, void *ws, hipStream_t s) {
+    const Plan p = make_plan(a.T, a.n_seq, a.hq, a.cache);
+    const bool extra = a.cap > 0.0f || a.slopes;
+    float *w = static_cast<float *>(ws);
+    if (a.cache.d == 64) return extra ? launch<64, true>(a, p, w, s) : launch<64, false>(a, p, w, s);
+    if (a.cache.d == 128) return extra ? launch<128, true>(a, p, w, s) : launch<128, false>(a, p, w, s);
+    return extra ? launch<256, true>(a, p, w, s) : launch<256, false>(a, p, w, s);
 }
 
 }  // namespace moeq4

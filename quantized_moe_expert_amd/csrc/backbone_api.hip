@@ -66,7 +66,7 @@ int check_cache(const moe_q4_kv_cache *c, int32_t q_heads) {
         q_heads < 1 || q_heads % c->kv_heads)
         return MOE_Q4_ERR_INVALID_ARG;
     if ((c->head_dim != 64 && c->head_dim != 128 && c->head_dim != 256) || c->page_size % 16 || q_heads > 1024 ||
-        c->n_pages >= (int64_t)1 << 31 || (int64_t)c->max_pages * c->page_size >= (int64_t)1 << 31)
+        c->n_pages >= (int64_t)1 << 31 || (int64_t)c->max_pages * c->page_size > (int64_t)1 << 30)
         return MOE_Q4_ERR_UNSUPPORTED;
     return MOE_Q4_OK;
 }
@@ -83,8 +83,9 @@ Cache cache_of(const moe_q4_kv_cache *c) {
                  static_cast<uint16_t *>(c->v), c->page_table, c->kv_len};
 }
 
-bool attention_sizes(int64_t T, int32_t n_seq, int32_t q_heads) {
-    return T < (int64_t)1 << 26 && T * q_heads < (int64_t)1 << 26 && n_seq < 1 << 20;
+bool attention_sizes(int64_t T, int32_t n_seq, int32_t q_heads, int32_t kv_heads) {
+    return T < (int64_t)1 << 26 && T * q_heads < (int64_t)1 << 26 && n_seq < 1 << 20 &&
+           (int64_t)n_seq * kv_heads < 1 << 22;
 }
 
 }  // namespace
@@ -174,7 +175,7 @@ int moe_q4_kv_append(const void *q, int64_t ldq, int32_t q_heads, const void *k,
 }
 
 size_t moe_q4_attention_workspace_size(int64_t T, int32_t n_seq, int32_t q_heads, const moe_q4_kv_cache *cache) {
-    if (T <= 0 || n_seq < 1 || check_cache(cache, q_heads) || !attention_sizes(T, n_seq, q_heads)) return 0;
+    if (T <= 0 || n_seq < 1 || check_cache(cache, q_heads) || !attention_sizes(T, n_seq, q_heads, cache->kv_heads)) return 0;
     return attention_workspace_bytes(T, n_seq, q_heads, cache_of(cache));
 }
 
@@ -187,7 +188,7 @@ int moe_q4_attention(const void *q, int64_t ldq, int32_t q_heads, int64_t T, con
     if (T < 0 || n_seq < 0 || window < 0 || !(cap >= 0.0f) || !std::isfinite(cap) || !std::isfinite(scale) ||
         (tree && prefix))
         return MOE_Q4_ERR_INVALID_ARG;
-    if (!attention_sizes(T, n_seq, q_heads)) return MOE_Q4_ERR_UNSUPPORTED;
+    if (!attention_sizes(T, n_seq, q_heads, cache->kv_heads)) return MOE_Q4_ERR_UNSUPPORTED;
     if (T == 0 || n_seq == 0) return MOE_Q4_OK;
     if (!seq_start || !aligned(seq_start, 4) || !aligned(slopes, 4) || !aligned(prefix, 4) || !aligned(tree, 8))
         return MOE_Q4_ERR_INVALID_ARG;
