@@ -20,6 +20,8 @@
 // the sequences' lengths (plan_find), so that a captured call goes with them.
 #include "seq_dev.h"
 
+#include <type_traits>
+
 namespace moeq4 {
 
 namespace {
@@ -651,7 +653,9 @@ __global__ __launch_bounds__(THREADS, 2) void attention_tile_kernel(AttentionArg
     const int per = uniform((range.count + f.parts - 1) / f.parts);
     const int j0 = f.part * per, j_end = min(range.count, j0 + per);
     const Query query = load_query(a, s, depth, i);
-    const float scale2 = a.cap > 0.0f ? a.scale / a.cap : a.scale * LOG2E;
+    // (A negative scale goes to the queries' signs, so that the largest product has the largest
+    // score; above 0, so that -inf stays.)
+    const float scale2 = fmaxf(fabsf(a.cap > 0.0f ? a.scale / a.cap : a.scale * LOG2E), 1e-37f);
     const float cap2 = a.cap * LOG2E;
     const float slope2 = EXTRA && a.slopes ? a.slopes[head] * LOG2E : 0.0f;
 
@@ -659,7 +663,10 @@ __global__ __launch_bounds__(THREADS, 2) void attention_tile_kernel(AttentionArg
     {
         const uint16_t *src = a.q + (int64_t)(s.start + i) * a.ldq + (int64_t)head * D + 8 * hh;
 #pragma unroll
-        for (int k = 0; k < DS; ++k) q[k] = *reinterpret_cast<const u32x4_t *>(src + 16 * k);
+        for (int k = 0; k < DS; ++k) {
+            q[k] = *reinterpret_cast<const u32x4_t *>(src + 16 * k);
+            if (a.scale < 0.0f) q[k] ^= u32x4_t{0x80008000u, 0x80008000u, 0x80008000u, 0x80008000u};
+        }
     }
     f32x16_t o[DT];
 #pragma unroll
@@ -668,16 +675,20 @@ __global__ __launch_bounds__(THREADS, 2) void attention_tile_kernel(AttentionArg
         for (int x = 0; x < 16; ++x) o[n][x] = 0.0f;
     float m_ref = -INFINITY, l_sum = 0.0f;
 
-    // Where this thread's chunks of a tile come from: entries from the first of 16 tokens on.
-    int k_from[LOADS], v_from[LOADS];
+    // Where this thread's chunks of a tile come from: bytes from the first of 16 tokens on.
+    uint32_t k_from[LOADS], v_from[LOADS];
     auto k_swizzle = [](int row) { return D == 64 ? row >> 1 & 7 : row & 15; };
     auto v_swizzle = [](int row) { return D == 64 ? (row >> 1 & 1) << 2 : (row & 3) << 2; };
 #pragma unroll
     for (int x = 0; x < LOADS; ++x) {
         const int at = (wave * LOADS + x) * WAVE + lane, key = at / CH, pos = at % CH;
-        k_from[x] = key % 16 * D + 8 * (pos ^ k_swizzle(key));
-        v_from[x] = key % 16 * D + 8 * (pos ^ v_swizzle(key));
+        k_from[x] = key % 16 * (2 * D) + 16 * (pos ^ k_swizzle(key));
+        v_from[x] = key % 16 * (2 * D) + 16 * (pos ^ v_swizzle(key));
     }
+    // Where a lane's operands lie in a tile: K (chunks), V (bytes).
+    const int k_read = c * CH;
+    const int v_key = 4 * hh + lane % 16 / 4;
+    const int v_read = (v_key * CH + (lane / 16 % 2) * 2 + lane % 4 / 2) * 16 + lane % 2 * 8;
     // A wave loads keys of one block of 16.  Where it lies in the next 64 tiles
     // (attention_rows_kernel), and which blocks of them are there.
     const int my_block = wave * (N / WAVES) / 16;
@@ -700,8 +711,9 @@ __global__ __launch_bounds__(THREADS, 2) void attention_tile_kernel(AttentionArg
         from_tile = j;
     };
     auto load = [&](int j, u32x4_t *kd, u32x4_t *vd) {
-        const int64_t block = (int64_t)(uint32_t)__builtin_amdgcn_readlane(block_at, j - from_tile) * D;
-        const uint16_t *ks = a.cache.k + block, *vs = a.cache.v + block;
+        const int64_t block = (int64_t)(uint32_t)__builtin_amdgcn_readlane(block_at, j - from_tile) * (2 * D);
+        const char *ks = reinterpret_cast<const char *>(a.cache.k) + block;
+        const char *vs = reinterpret_cast<const char *>(a.cache.v) + block;
 #pragma unroll
         for (int x = 0; x < LOADS; ++x)
             __builtin_amdgcn_global_load_lds((const void *)(ks + k_from[x]),
@@ -711,22 +723,10 @@ __global__ __launch_bounds__(THREADS, 2) void attention_tile_kernel(AttentionArg
             __builtin_amdgcn_global_load_lds((const void *)(vs + v_from[x]),
                                              (lds_void *)(vd + (wave * LOADS + x) * WAVE), 16, 0, 0);
     };
-    auto step = [&](int j, u32x4_t *kb, u32x4_t *vb, u32x4_t *kn, u32x4_t *vn, uint32_t *bad) {
-        const int k0 = N * range.tile(j);
-        uint32_t there = 0;
-#pragma unroll
-        for (int t = 0; t < NB; ++t) there |= (uint32_t)(page_ok[t] >> (j - from_tile) & 1) << t;
-        const bool whole = there == (1u << NB) - 1 && sees_all<N>(a, s, i0, i1, k0);
-        if (!whole && tid < 2) bad[tid] = 0;
-        if (!whole) wait_lds();
-        wait_loads();
-        lds_barrier();
-        const int next = j + 1;
-        if (next < j_end) {
-            if (next - from_tile == WAVE) load_pages(next);
-            load(next, kn, vn);
-        }
-        if (!whole) {
+    // A tile that every row sees whole, and any other.
+    auto work = [&](auto masked, int k0, uint32_t there, const u32x4_t *kb, u32x4_t *vb, uint32_t *bad) {
+        constexpr bool MASKED = decltype(masked)::value;
+        if (MASKED) {
             // 0 times NaN or infinity: values of keys that some row does not see are
             // cleared, and the rows that see one get NaN for it.
 #pragma unroll
@@ -745,25 +745,26 @@ __global__ __launch_bounds__(THREADS, 2) void attention_tile_kernel(AttentionArg
         for (int t = 0; t < KT; ++t) {
 #pragma unroll
             for (int x = 0; x < 16; ++x) sc[t][x] = 0.0f;
-            const int key = 32 * t + c;
+            // (The upper bits of a chunk's number are not permuted: one address for all k % 8.)
 #pragma unroll
-            for (int k = 0; k < DS; ++k) sc[t] = mfma32(kb[key * CH + ((2 * k + hh) ^ k_swizzle(key))], q[k], sc[t]);
+            for (int k = 0; k < DS; ++k)
+                sc[t] = mfma32(kb[k_read + ((2 * (k % 8) + hh) ^ k_swizzle(c)) + 16 * (k / 8) + 32 * t * CH], q[k], sc[t]);
         }
+        if (EXTRA) {
 #pragma unroll
-        for (int t = 0; t < KT; ++t)
+            for (int t = 0; t < KT; ++t)
 #pragma unroll
-            for (int x = 0; x < 16; ++x) {
-                float v = sc[t][x] * scale2;
-                if (EXTRA) {
+                for (int x = 0; x < 16; ++x) {
+                    float v = sc[t][x] * scale2;
                     if (a.cap > 0.0f) v = cap2 * (1.0f - 2.0f * __builtin_amdgcn_rcpf(1.0f + __expf(2.0f * v)));
                     if (a.slopes) {
                         const int gap = query.pos - key_pos(a, s, depth, k0 + 32 * t + 8 * (x / 4) + 4 * hh + x % 4);
                         v -= slope2 * fabsf((float)gap);
                     }
+                    sc[t][x] = v;
                 }
-                sc[t][x] = v;
-            }
-        if (!whole) {
+        }
+        if (MASKED) {
             uint64_t all = seen(a, s, query, k0);
 #pragma unroll
             for (int t = 0; t < NB; ++t)
@@ -781,6 +782,7 @@ __global__ __launch_bounds__(THREADS, 2) void attention_tile_kernel(AttentionArg
 #pragma unroll
             for (int x = 0; x < 16; ++x) top = fmaxf(top, sc[t][x]);
         top = query_max<false>(top);
+        if (!EXTRA) top *= scale2;
         if (__any(top > m_ref + RISE)) {
             const float m_new = fmaxf(m_ref, top);
             const float keep = m_new == -INFINITY ? 1.0f : __builtin_amdgcn_exp2f(m_ref - m_new);
@@ -792,39 +794,50 @@ __global__ __launch_bounds__(THREADS, 2) void attention_tile_kernel(AttentionArg
             m_ref = m_new;
         }
         const float m_use = m_ref == -INFINITY ? 0.0f : m_ref;
-        u32x4_t w[KT][2];
-        uint32_t spoiled[KT];
-#pragma unroll
-        for (int t = 0; t < KT; ++t) spoiled[t] = whole ? 0u : bad[t];
 #pragma unroll
         for (int t = 0; t < KT; ++t) {
-            float e[16];
-#pragma unroll
-            for (int x = 0; x < 16; ++x) {
-                e[x] = __builtin_amdgcn_exp2f(sc[t][x] - m_use);
-                l_sum += e[x];
-            }
-            if (spoiled[t]) {
-#pragma unroll
-                for (int x = 0; x < 16; ++x)
-                    if (spoiled[t] >> (8 * (x / 4) + 4 * hh + x % 4) & 1 && sc[t][x] != -INFINITY) e[x] = NAN;
-            }
-#pragma unroll
-            for (int x = 0; x < 8; ++x) w[t][x / 4][x % 4] = pack_bf16x2(e[2 * x], e[2 * x + 1]);
-        }
-#pragma unroll
-        for (int t = 0; t < KT; ++t)
+            const uint32_t spoiled = MASKED ? bad[t] : 0u;
 #pragma unroll
             for (int u = 0; u < 2; ++u) {
-                const int key = 32 * t + 16 * u + 4 * hh + lane % 16 / 4;
+                float e[8];
+#pragma unroll
+                for (int x = 0; x < 8; ++x) {
+                    const float v = sc[t][8 * u + x];
+                    e[x] = __builtin_amdgcn_exp2f(EXTRA ? v - m_use : fmaf(v, scale2, -m_use));
+                    l_sum += e[x];
+                    if (MASKED && spoiled >> (16 * u + 8 * (x / 4) + 4 * hh + x % 4) & 1 && v != -INFINITY) e[x] = NAN;
+                }
+                const u32x4_t w = {pack_bf16x2(e[0], e[1]), pack_bf16x2(e[2], e[3]), pack_bf16x2(e[4], e[5]),
+                                   pack_bf16x2(e[6], e[7])};
 #pragma unroll
                 for (int n = 0; n < DT; ++n) {
-                    const int chunk = 4 * n + (lane / 16 % 2) * 2 + lane % 4 / 2;
-                    const int byte = (key * CH + (chunk ^ v_swizzle(key))) * 16 + lane % 2 * 8;
+                    const int byte = v_read + ((4 * (n % 4)) ^ v_swizzle(v_key)) * 16 + (16 * (n / 4) + (32 * t + 16 * u) * CH) * 16;
                     const u32x2_t x = read_transposed(vb, byte), y = read_transposed(vb, byte + 8 * CH * 16);
-                    o[n] = mfma32(u32x4_t{x[0], x[1], y[0], y[1]}, w[t][u], o[n]);
+                    o[n] = mfma32(u32x4_t{x[0], x[1], y[0], y[1]}, w, o[n]);
                 }
             }
+        }
+    };
+    auto step = [&](int j, u32x4_t *kb, u32x4_t *vb, u32x4_t *kn, u32x4_t *vn, uint32_t *bad) {
+        const int k0 = N * range.tile(j);
+        uint32_t there = 0;
+#pragma unroll
+        for (int t = 0; t < NB; ++t) there |= (uint32_t)(page_ok[t] >> (j - from_tile) & 1) << t;
+        const bool whole = there == (1u << NB) - 1 && sees_all<N>(a, s, i0, i1, k0);
+        if (!whole) {
+            if (tid < 2) bad[tid] = 0;
+            wait_lds();
+        }
+        wait_loads();
+        lds_barrier();
+        if (j + 1 < j_end) {
+            if (j + 1 - from_tile == WAVE) load_pages(j + 1);
+            load(j + 1, kn, vn);
+        }
+        if (whole)
+            work(std::false_type{}, k0, there, kb, vb, bad);
+        else
+            work(std::true_type{}, k0, there, kb, vb, bad);
     };
     if (j0 < j_end) {
         load_pages(j0);
