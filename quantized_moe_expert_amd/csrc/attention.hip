@@ -20,8 +20,6 @@
 // the sequences' lengths (plan_find), so that a captured call goes with them.
 #include "seq_dev.h"
 
-#include <type_traits>
-
 namespace moeq4 {
 
 namespace {
@@ -631,7 +629,7 @@ __device__ __forceinline__ u32x2_t read_transposed(const u32x4_t *lds, int byte)
 // The weights are rounded to bf16 for the second product (half a step, 2^-8 of a
 // weight, random over the keys); their sum is that of the unrounded ones.
 template <int D, bool EXTRA>
-__global__ __launch_bounds__(THREADS, 2) void attention_tile_kernel(AttentionArgs a, Plan p, float *ws) {
+__global__ __launch_bounds__(THREADS, D == 256 ? 1 : 2) void attention_tile_kernel(AttentionArgs a, Plan p, float *ws) {
     constexpr int N = tile_keys(D), CH = D / 8, KT = N / 32, DS = D / 16, DT = D / 32, NB = N / 16;
     constexpr int LOADS = N * CH / THREADS;
     __shared__ u32x4_t k_a[N * CH], k_b[N * CH], v_a[N * CH], v_b[N * CH];
@@ -723,10 +721,23 @@ __global__ __launch_bounds__(THREADS, 2) void attention_tile_kernel(AttentionArg
             __builtin_amdgcn_global_load_lds((const void *)(vs + v_from[x]),
                                              (lds_void *)(vd + (wave * LOADS + x) * WAVE), 16, 0, 0);
     };
-    // A tile that every row sees whole, and any other.
-    auto work = [&](auto masked, int k0, uint32_t there, const u32x4_t *kb, u32x4_t *vb, uint32_t *bad) {
-        constexpr bool MASKED = decltype(masked)::value;
-        if (MASKED) {
+    auto step = [&](int j, u32x4_t *kb, u32x4_t *vb, u32x4_t *kn, u32x4_t *vn, uint32_t *bad) {
+        const int k0 = N * range.tile(j);
+        uint32_t there = 0;
+#pragma unroll
+        for (int t = 0; t < NB; ++t) there |= (uint32_t)(page_ok[t] >> (j - from_tile) & 1) << t;
+        const bool whole = there == (1u << NB) - 1 && sees_all<N>(a, s, i0, i1, k0);
+        if (!whole) {
+            if (tid < 2) bad[tid] = 0;
+            wait_lds();
+        }
+        wait_loads();
+        lds_barrier();
+        // (Past the end the last tile again, never used.)
+        const int next = min(j + 1, j_end - 1);
+        if (next - from_tile == WAVE) load_pages(next);
+        load(next, kn, vn);
+        if (!whole) {
             // 0 times NaN or infinity: values of keys that some row does not see are
             // cleared, and the rows that see one get NaN for it.
 #pragma unroll
@@ -764,16 +775,19 @@ __global__ __launch_bounds__(THREADS, 2) void attention_tile_kernel(AttentionArg
                     sc[t][x] = v;
                 }
         }
-        if (MASKED) {
+        if (!whole) {
             uint64_t all = seen(a, s, query, k0);
 #pragma unroll
             for (int t = 0; t < NB; ++t)
                 if (!(there >> t & 1)) all &= ~(0xffffull << (16 * t));
 #pragma unroll
             for (int t = 0; t < KT; ++t) {
-                const uint32_t bits = (uint32_t)(all >> (32 * t)) >> (4 * hh);
+                const uint32_t bits = (uint32_t)(all >> (32 * t)) >> (4 * hh), spoiled = bad[t] >> (4 * hh);
 #pragma unroll
-                for (int x = 0; x < 16; ++x) sc[t][x] = bits >> (8 * (x / 4) + x % 4) & 1 ? sc[t][x] : -INFINITY;
+                for (int x = 0; x < 16; ++x) {
+                    const int at = 8 * (x / 4) + x % 4;
+                    sc[t][x] = bits >> at & 1 ? (spoiled >> at & 1 ? NAN : sc[t][x]) : -INFINITY;
+                }
             }
         }
         float top = -INFINITY;
@@ -796,7 +810,6 @@ __global__ __launch_bounds__(THREADS, 2) void attention_tile_kernel(AttentionArg
         const float m_use = m_ref == -INFINITY ? 0.0f : m_ref;
 #pragma unroll
         for (int t = 0; t < KT; ++t) {
-            const uint32_t spoiled = MASKED ? bad[t] : 0u;
 #pragma unroll
             for (int u = 0; u < 2; ++u) {
                 float e[8];
@@ -805,7 +818,6 @@ __global__ __launch_bounds__(THREADS, 2) void attention_tile_kernel(AttentionArg
                     const float v = sc[t][8 * u + x];
                     e[x] = __builtin_amdgcn_exp2f(EXTRA ? v - m_use : fmaf(v, scale2, -m_use));
                     l_sum += e[x];
-                    if (MASKED && spoiled >> (16 * u + 8 * (x / 4) + 4 * hh + x % 4) & 1 && v != -INFINITY) e[x] = NAN;
                 }
                 const u32x4_t w = {pack_bf16x2(e[0], e[1]), pack_bf16x2(e[2], e[3]), pack_bf16x2(e[4], e[5]),
                                    pack_bf16x2(e[6], e[7])};
@@ -818,35 +830,15 @@ __global__ __launch_bounds__(THREADS, 2) void attention_tile_kernel(AttentionArg
             }
         }
     };
-    auto step = [&](int j, u32x4_t *kb, u32x4_t *vb, u32x4_t *kn, u32x4_t *vn, uint32_t *bad) {
-        const int k0 = N * range.tile(j);
-        uint32_t there = 0;
-#pragma unroll
-        for (int t = 0; t < NB; ++t) there |= (uint32_t)(page_ok[t] >> (j - from_tile) & 1) << t;
-        const bool whole = there == (1u << NB) - 1 && sees_all<N>(a, s, i0, i1, k0);
-        if (!whole) {
-            if (tid < 2) bad[tid] = 0;
-            wait_lds();
-        }
-        wait_loads();
-        lds_barrier();
-        if (j + 1 < j_end) {
-            if (j + 1 - from_tile == WAVE) load_pages(j + 1);
-            load(j + 1, kn, vn);
-        }
-        if (whole)
-            work(std::false_type{}, k0, there, kb, vb, bad);
-        else
-            work(std::true_type{}, k0, there, kb, vb, bad);
-    };
     if (j0 < j_end) {
         load_pages(j0);
         load(j0, k_a, v_a);
-        for (int j = j0; j < j_end; j += 2) {
+        int j = j0;
+        for (; j + 1 < j_end; j += 2) {
             step(j, k_a, v_a, k_b, v_b, bad_a);
-            if (j + 1 == j_end) break;
             step(j + 1, k_b, v_b, k_a, v_a, bad_b);
         }
+        if (j < j_end) step(j, k_a, v_a, k_b, v_b, bad_a);
     }
     l_sum = query_sum<false>(l_sum);
     if (my_row >= rows) return;
