@@ -178,8 +178,9 @@ __device__ __forceinline__ void load_depths(const AttentionArgs &a, const Seq &s
 // 2 target of blocks with more than one (m > C: S <= 2 m / C), whose sums go
 // through the workspace.
 struct Plan {
-    int rows, keys;    // of a block, of a tile
-    int cmin, target;
+    int rows, row_shift;    // of a block, a power of two
+    int key_shift;          // keys of a tile, a power of two
+    int cmin, target_shift;
     int items, joins, slots;  // most parts; most split blocks; most of their parts (each per head of the cache)
 };
 
@@ -189,15 +190,20 @@ struct Found {
 };
 
 __device__ __forceinline__ void blocks_of(const AttentionArgs &a, const Plan &p, const Seq &s, int &R, int &m) {
-    const int r = a.hq / a.cache.hkv;
-    R = (int)(((int64_t)s.n * r + p.rows - 1) / p.rows);
-    m = (s.len + p.keys - 1) / p.keys;
+    const int r = a.hq / a.cache.hkv, up = (1 << p.key_shift) - 1;
+    R = (s.n * r + p.rows - 1) >> p.row_shift;
+    m = (s.len + up) >> p.key_shift;
     if (a.window) {
         // Keys that some row of a block sees: the window and the block's tokens before it.
         const int64_t span = (int64_t)a.window + (a.tree ? WAVE : p.rows / r + 1);
-        m = (int)min((int64_t)m, (s.prefix + p.keys - 1) / p.keys + span / p.keys + 2);
+        m = (int)min((int64_t)m, ((s.prefix + up) >> p.key_shift) + (span >> p.key_shift) + 2);
     }
     m = max(m, 1);
+}
+// Tiles to a part. (No sequence has 2^30.)
+__device__ __forceinline__ int tiles_to_a_part(const Plan &p, uint64_t work) {
+    const uint64_t c = (work + (1u << p.target_shift) - 1) >> p.target_shift;
+    return max(p.cmin, (int)min(c, (uint64_t)1 << 30));
 }
 
 __device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
@@ -210,17 +216,38 @@ __device__ __forceinline__ Seq uniform(const Seq &s) {
 // fewer.  All threads of the workgroup call it.
 template <bool JOIN>
 __device__ __forceinline__ bool plan_find(const AttentionArgs &a, const Plan &p, int64_t item, Found &f) {
-    if (a.n_seq == 1) {
-        f.seq = load_seq(a, 0);
-        int R, m;
-        blocks_of(a, p, f.seq, R, m);
-        const int C = (int)max((int64_t)p.cmin, ((int64_t)R * m + p.target - 1) / p.target), S = (m + C - 1) / C;
-        if (item >= (int64_t)R * (JOIN ? 1 : S) || (JOIN && S == 1)) return false;
-        f.b = 0;
-        f.parts = S;
-        f.block = JOIN ? (int)item : R - 1 - (int)item / S;
-        f.part = JOIN ? 0 : (int)item % S;
-        f.slot = f.block * S;
+    if (a.n_seq <= WAVE) {
+        // Each wave for itself, a sequence to a lane: no barrier.
+        const int lane = threadIdx.x & (WAVE - 1);
+        Seq s = {0, 0, 0, 0, 0, 0};
+        int R = 0, m = 1;
+        if (lane < a.n_seq) {
+            s = load_seq(a, lane);
+            blocks_of(a, p, s, R, m);
+        }
+        uint64_t work = (uint64_t)R * m;
+        if (a.n_seq > 1)
+#pragma unroll
+            for (int o = 1; o < WAVE; o <<= 1) work += __shfl_xor(work, o, WAVE);
+        else
+            work = (uint64_t)uniform((int)(work >> 32)) << 32 | (uint32_t)uniform((int)work);
+        const int C = tiles_to_a_part(p, work), S = (m + C - 1) / C;
+        const int all = R * S, split = S > 1 ? all : 0, mine = JOIN ? (S > 1 ? R : 0) : all;
+        // (At most items and slots of the plan: they fit in 32 bits.)
+        const int end = wave_inclusive_scan_i32(mine);
+        const int at = (int)item - (end - mine);
+        const uint64_t hit = __ballot(at >= 0 && at < mine);
+        if (!hit) return false;
+        const int b = __builtin_ctzll(hit);
+        f.b = b;
+        f.parts = __builtin_amdgcn_readlane(S, b);
+        const int j = __builtin_amdgcn_readlane(at, b);
+        f.block = JOIN ? j : __builtin_amdgcn_readlane(R, b) - 1 - j / f.parts;
+        f.part = JOIN ? 0 : j % f.parts;
+        f.slot = __builtin_amdgcn_readlane(wave_inclusive_scan_i32(split) - split, b) + f.block * f.parts;
+        f.seq = Seq{__builtin_amdgcn_readlane(s.start, b), __builtin_amdgcn_readlane(s.n, b),
+                    __builtin_amdgcn_readlane(s.kv, b), __builtin_amdgcn_readlane(s.len, b),
+                    __builtin_amdgcn_readlane(s.before, b), __builtin_amdgcn_readlane(s.prefix, b)};
         return true;
     }
     __shared__ uint64_t part_sum[WAVES + 1];
@@ -240,7 +267,7 @@ __device__ __forceinline__ bool plan_find(const AttentionArgs &a, const Plan &p,
     work = 0;
 #pragma unroll
     for (int w = 0; w < WAVES; ++w) work += part_sum[w];
-    const int64_t C = max((int64_t)p.cmin, (int64_t)((work + p.target - 1) / p.target));
+    const int C = tiles_to_a_part(p, work);
     uint64_t carry = 0;  // parts (or split blocks) before, in the upper half; slots before, in the lower
     for (int b0 = 0; b0 < a.n_seq; b0 += THREADS) {
         const int b = b0 + tid;
@@ -248,7 +275,7 @@ __device__ __forceinline__ bool plan_find(const AttentionArgs &a, const Plan &p,
         uint64_t mine = 0;
         if (b < a.n_seq) {
             blocks_of(a, p, load_seq(a, b), R, m);
-            S = (int)((m + C - 1) / C);
+            S = (m + C - 1) / C;
             const uint32_t all = (uint32_t)R * S, split = S > 1 ? all : 0;
             mine = (uint64_t)(JOIN ? (S > 1 ? R : 0) : all) << 32 | split;
         }
@@ -550,38 +577,90 @@ __global__ __launch_bounds__(THREADS, 2) void attention_rows_kernel(AttentionArg
 
 // ------------------------------------------------------------------- join
 
-// Rows of split blocks: 1024 / D rows to a workgroup, four entries to a thread.
-template <int D>
+// Rows of split blocks: four entries to a thread, G groups of threads share the
+// parts of a row.  Bound by the latency of the parts' loads (single tokens: 64
+// parts and more, G as large as a workgroup allows) or by their bytes.
+constexpr int JOIN_GROUPS = 4;  // workgroups to a block of 16 rows: most have fewer
+
+template <int D, int G>
 __global__ __launch_bounds__(THREADS) void attention_join_kernel(AttentionArgs a, Plan p, float *ws) {
-    constexpr int JR = THREADS / (D / 4);
-    const int groups = p.rows / JR;
+    constexpr int TD = D / 4, ROWS = THREADS / (TD * G);
+    __shared__ float4 v_part[G > 1 ? G * ROWS : 1][TD];
+    __shared__ float m_part[G * ROWS], l_part[G * ROWS];
+    const int groups = G > 1 ? JOIN_GROUPS : p.rows / ROWS;
     const int64_t x = blockIdx.x / a.cache.hkv;
     const int hk = blockIdx.x % a.cache.hkv;
     Found f;
     if (!plan_find<true>(a, p, x / groups, f)) return;
-    const Seq s = f.seq;
+    const Seq s = uniform(f.seq);
     const int r = a.hq / a.cache.hkv;
-    const int rr = (int)(x % groups) * JR + threadIdx.x / (D / 4), d = 4 * (threadIdx.x % (D / 4));
-    const int row = f.block * p.rows + rr;
-    if (row >= s.n * r || (int64_t)f.slot + f.parts > p.slots) return;
+    if ((int64_t)f.slot + f.parts > p.slots) return;
+    const int sub = threadIdx.x / TD, g = sub / ROWS, d = 4 * (threadIdx.x % TD);
     const int64_t stride = (int64_t)a.cache.hkv * p.rows * (D + 2);
     const float *part = slot_of<D>(ws, p, a.cache.hkv, f.slot, hk);
+    const int live = min(p.rows, s.n * r - f.block * p.rows);
+    for (int row0 = (int)(x % groups) * ROWS; row0 < live; row0 += groups * ROWS) {
+    // (Rows behind the sequence's last are in the slots too, as whatever is there; they are not stored.)
+    const int rr = row0 + sub % ROWS, row = f.block * p.rows + rr;
     const float *ms = part + p.rows * D + rr, *ls = ms + p.rows;
-    float top = -INFINITY;
-    for (int i = 0; i < f.parts; ++i) top = fmaxf(top, ms[i * stride]);
-    float sum = 0.0f;
+    float top = -INFINITY, sum = 0.0f;
     float4 v = {0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll 4
-    for (int i = 0; i < f.parts; ++i) {
-        const float mi = ms[i * stride];
-        const float k = mi == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(mi - top);
-        const float4 y = *reinterpret_cast<const float4 *>(part + i * stride + rr * D + d);
-        sum = fmaf(k, ls[i * stride], sum);
-        v.x = fmaf(k, y.x, v.x), v.y = fmaf(k, y.y, v.y), v.z = fmaf(k, y.z, v.z), v.w = fmaf(k, y.w, v.w);
+    for (int i0 = g; i0 < f.parts; i0 += 8 * G) {
+        // Eight parts at once (past the end the last one again, with weight 0).
+        float mi[8], li[8];
+        float4 y[8];
+#pragma unroll
+        for (int u = 0; u < 8; ++u) {
+            const int i = min(i0 + u * G, f.parts - 1);
+            mi[u] = ms[i * stride];
+            li[u] = ls[i * stride];
+            y[u] = *reinterpret_cast<const float4 *>(part + i * stride + rr * D + d);
+        }
+        float now = top;
+#pragma unroll
+        for (int u = 0; u < 8; ++u) {
+            if (i0 + u * G >= f.parts) mi[u] = -INFINITY;
+            now = fmaxf(now, mi[u]);
+        }
+        const float keep = top == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(top - now);
+        top = now;
+        sum *= keep;
+        v.x *= keep, v.y *= keep, v.z *= keep, v.w *= keep;
+#pragma unroll
+        for (int u = 0; u < 8; ++u) {
+            if (mi[u] == -INFINITY) continue;
+            const float k = __builtin_amdgcn_exp2f(mi[u] - top);
+            sum = fmaf(k, li[u], sum);
+            v.x = fmaf(k, y[u].x, v.x), v.y = fmaf(k, y[u].y, v.y);
+            v.z = fmaf(k, y[u].z, v.z), v.w = fmaf(k, y[u].w, v.w);
+        }
     }
+    if (G > 1) {
+        __syncthreads();
+        if (d == 0) {
+            m_part[sub] = top;
+            l_part[sub] = sum;
+        }
+        v_part[sub][d / 4] = v;
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < G; ++i) top = fmaxf(top, m_part[sub % ROWS + i * ROWS]);
+        sum = 0.0f;
+        v = float4{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+        for (int i = 0; i < G; ++i) {
+            const float mi = m_part[sub % ROWS + i * ROWS];
+            const float k = mi == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(mi - top);
+            const float4 y = v_part[sub % ROWS + i * ROWS][d / 4];
+            sum = fmaf(k, l_part[sub % ROWS + i * ROWS], sum);
+            v.x = fmaf(k, y.x, v.x), v.y = fmaf(k, y.y, v.y), v.z = fmaf(k, y.z, v.z), v.w = fmaf(k, y.w, v.w);
+        }
+    }
+    if (g > 0 || rr >= live) continue;
     const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
     uint16_t *dst = a.o + (int64_t)(s.start + row / r) * a.ldo + (int64_t)(hk * r + row % r) * D + d;
     *reinterpret_cast<uint2 *>(dst) = uint2{pack_bf16x2(v.x * inv, v.y * inv), pack_bf16x2(v.z * inv, v.w * inv)};
+    }
 }
 
 // -------------------------------------------------------------- more rows
@@ -879,16 +958,19 @@ Plan make_plan(int64_t T, int n_seq, int hq, const Cache &c) {
     const int r = hq / c.hkv;
     Plan p;
     const bool few = few_rows(T, n_seq, r);
-    p.rows = few ? 16 : TILE_ROWS;
-    p.keys = few ? 32 : tile_keys(c.d);
-    p.cmin = few ? WAVES : 8;
-    p.target = max(1, 512 / c.hkv);
+    p.row_shift = few ? 4 : 7;
+    p.rows = 1 << p.row_shift;
+    p.key_shift = few || tile_keys(c.d) == 32 ? 5 : 6;
+    p.cmin = few ? WAVES : 2;
+    p.target_shift = 0;
+    while ((2 << p.target_shift) * c.hkv <= 512) ++p.target_shift;
+    const int target = 1 << p.target_shift;
     const int64_t blocks = T * r / p.rows + min(T, (int64_t)n_seq);
-    const int64_t tiles = ((int64_t)c.max_pages * c.page + p.keys - 1) / p.keys;
+    const int64_t tiles = ((int64_t)c.max_pages * c.page + (1 << p.key_shift) - 1) >> p.key_shift;
     const int64_t parts = (tiles + p.cmin - 1) / p.cmin;  // of one block, at most
-    p.items = (int)min(blocks * parts, blocks + p.target);
-    p.joins = parts > 1 ? (int)min(blocks, (int64_t)p.target) : 0;
-    p.slots = parts > 1 ? (int)min(blocks * parts, (int64_t)2 * p.target) : 0;
+    p.items = (int)min(blocks * parts, blocks + target);
+    p.joins = parts > 1 ? (int)min(blocks, (int64_t)target) : 0;
+    p.slots = parts > 1 ? (int)min(blocks * parts, (int64_t)2 * target) : 0;
     return p;
 }
 
@@ -901,8 +983,11 @@ hipError_t launch(const AttentionArgs &a, const Plan &p, float *ws, hipStream_t 
         attention_tile_kernel<D, EXTRA><<<grid, THREADS, 0, s>>>(a, p, ws);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess || !p.joins) return e;
-    const unsigned groups = p.rows * (D / 4) / THREADS;
-    attention_join_kernel<D><<<dim3((unsigned)((int64_t)p.joins * groups * a.cache.hkv)), THREADS, 0, s>>>(a, p, ws);
+    const unsigned heads = (unsigned)(p.joins * a.cache.hkv);
+    if (p.rows == 16)
+        attention_join_kernel<D, 1024 / D><<<dim3(heads * JOIN_GROUPS), THREADS, 0, s>>>(a, p, ws);
+    else
+        attention_join_kernel<D, 1><<<dim3(heads * (p.rows * D / 1024)), THREADS, 0, s>>>(a, p, ws);
     return hipGetLastError();
 }
 
