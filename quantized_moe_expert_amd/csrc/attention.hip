@@ -242,8 +242,10 @@ __device__ __forceinline__ bool plan_find(const AttentionArgs &a, const Plan &p,
         f.b = b;
         f.parts = __builtin_amdgcn_readlane(S, b);
         const int j = __builtin_amdgcn_readlane(at, b);
-        f.block = JOIN ? j : __builtin_amdgcn_readlane(R, b) - 1 - j / f.parts;
-        f.part = JOIN ? 0 : j % f.parts;
+        const int blocks = __builtin_amdgcn_readlane(R, b);
+        // (The blocks of one part read the same keys; the last blocks have the most.)
+        f.block = JOIN ? j : blocks - 1 - j % blocks;
+        f.part = JOIN ? 0 : j / blocks;
         f.slot = __builtin_amdgcn_readlane(wave_inclusive_scan_i32(split) - split, b) + f.block * f.parts;
         f.seq = Seq{__builtin_amdgcn_readlane(s.start, b), __builtin_amdgcn_readlane(s.n, b),
                     __builtin_amdgcn_readlane(s.kv, b), __builtin_amdgcn_readlane(s.len, b),
@@ -296,10 +298,10 @@ __device__ __forceinline__ bool plan_find(const AttentionArgs &a, const Plan &p,
         }
         const int64_t at = item - (int64_t)(before >> 32);
         if (at >= 0 && at < (int64_t)(mine >> 32)) {
-            const int block = JOIN ? (int)at : R - 1 - (int)at / S;
+            const int block = JOIN ? (int)at : R - 1 - (int)at % R;
             found[0] = b;
             found[1] = block;
-            found[2] = JOIN ? 0 : (int)at % S;
+            found[2] = JOIN ? 0 : (int)at / R;
             found[3] = S;
             found[4] = (int)(uint32_t)before + block * S;
         }
@@ -705,18 +707,24 @@ __device__ __forceinline__ u32x2_t read_transposed(const u32x4_t *lds, int byte)
 // 16-byte chunks of a row are permuted by the row number (the source address
 // carries it), so that reads spread over the banks.
 //
+// Of heads of 256 a workgroup has half of the entries of o (and reads that half of
+// V): with all of them a wave has 512 registers, is alone on its SIMD and waits
+// for LDS (448 TFLOP/s); the first product is done twice.
+//
 // The weights are rounded to bf16 for the second product (half a step, 2^-8 of a
 // weight, random over the keys); their sum is that of the unrounded ones.
 template <int D, bool EXTRA>
-__global__ __launch_bounds__(THREADS, D == 256 ? 1 : 2) void attention_tile_kernel(AttentionArgs a, Plan p, float *ws) {
-    constexpr int N = tile_keys(D), CH = D / 8, KT = N / 32, DS = D / 16, DT = D / 32, NB = N / 16;
-    constexpr int LOADS = N * CH / THREADS;
-    __shared__ u32x4_t k_a[N * CH], k_b[N * CH], v_a[N * CH], v_b[N * CH];
+__global__ __launch_bounds__(THREADS, 2) void attention_tile_kernel(AttentionArgs a, Plan p, float *ws) {
+    constexpr int DO = D < 128 ? D : 128, HALVES = D / DO;
+    constexpr int N = tile_keys(D), CH = D / 8, CV = DO / 8, KT = N / 32, DS = D / 16, DT = DO / 32, NB = N / 16;
+    constexpr int LOADS = N * CH / THREADS, V_LOADS = N * CV / THREADS;
+    __shared__ u32x4_t k_a[N * CH], k_b[N * CH], v_a[N * CV], v_b[N * CV];
     __shared__ uint32_t bad_a[2], bad_b[2];
     __shared__ int depth[WAVE];
     const int hk = blockIdx.x % a.cache.hkv;
+    const int d0 = HALVES == 1 ? 0 : (int)(blockIdx.x / a.cache.hkv) % HALVES * DO;  // the first of its entries of o
     Found f;
-    if (!plan_find<false>(a, p, blockIdx.x / a.cache.hkv, f)) return;
+    if (!plan_find<false>(a, p, blockIdx.x / a.cache.hkv / HALVES, f)) return;
     const Seq s = uniform(f.seq);
     if (a.tree) load_depths(a, s, depth);
     const int tid = threadIdx.x, lane = tid & (WAVE - 1), wave = __builtin_amdgcn_readfirstlane(tid / WAVE);
@@ -753,19 +761,23 @@ __global__ __launch_bounds__(THREADS, D == 256 ? 1 : 2) void attention_tile_kern
     float m_ref = -INFINITY, l_sum = 0.0f;
 
     // Where this thread's chunks of a tile come from: bytes from the first of 16 tokens on.
-    uint32_t k_from[LOADS], v_from[LOADS];
+    uint32_t k_from[LOADS], v_from[V_LOADS];
     auto k_swizzle = [](int row) { return D == 64 ? row >> 1 & 7 : row & 15; };
     auto v_swizzle = [](int row) { return D == 64 ? (row >> 1 & 1) << 2 : (row & 3) << 2; };
 #pragma unroll
     for (int x = 0; x < LOADS; ++x) {
         const int at = (wave * LOADS + x) * WAVE + lane, key = at / CH, pos = at % CH;
         k_from[x] = key % 16 * (2 * D) + 16 * (pos ^ k_swizzle(key));
-        v_from[x] = key % 16 * (2 * D) + 16 * (pos ^ v_swizzle(key));
+    }
+#pragma unroll
+    for (int x = 0; x < V_LOADS; ++x) {
+        const int at = (wave * V_LOADS + x) * WAVE + lane, key = at / CV, pos = at % CV;
+        v_from[x] = key % 16 * (2 * D) + 16 * (pos ^ v_swizzle(key)) + 2 * d0;
     }
     // Where a lane's operands lie in a tile: K (chunks), V (bytes).
     const int k_read = c * CH;
     const int v_key = 4 * hh + lane % 16 / 4;
-    const int v_read = (v_key * CH + (lane / 16 % 2) * 2 + lane % 4 / 2) * 16 + lane % 2 * 8;
+    const int v_read = (v_key * CV + (lane / 16 % 2) * 2 + lane % 4 / 2) * 16 + lane % 2 * 8;
     // A wave loads keys of one block of 16.  Where it lies in the next 64 tiles
     // (attention_rows_kernel), and which blocks of them are there.
     const int my_block = wave * (N / WAVES) / 16;
@@ -796,9 +808,9 @@ __global__ __launch_bounds__(THREADS, D == 256 ? 1 : 2) void attention_tile_kern
             __builtin_amdgcn_global_load_lds((const void *)(ks + k_from[x]),
                                              (lds_void *)(kd + (wave * LOADS + x) * WAVE), 16, 0, 0);
 #pragma unroll
-        for (int x = 0; x < LOADS; ++x)
+        for (int x = 0; x < V_LOADS; ++x)
             __builtin_amdgcn_global_load_lds((const void *)(vs + v_from[x]),
-                                             (lds_void *)(vd + (wave * LOADS + x) * WAVE), 16, 0, 0);
+                                             (lds_void *)(vd + (wave * V_LOADS + x) * WAVE), 16, 0, 0);
     };
     auto step = [&](int j, u32x4_t *kb, u32x4_t *vb, u32x4_t *kn, u32x4_t *vn, uint32_t *bad) {
         const int k0 = N * range.tile(j);
@@ -820,8 +832,8 @@ __global__ __launch_bounds__(THREADS, D == 256 ? 1 : 2) void attention_tile_kern
             // 0 times NaN or infinity: values of keys that some row does not see are
             // cleared, and the rows that see one get NaN for it.
 #pragma unroll
-            for (int x = 0; x < LOADS; ++x) {
-                const int at = (wave * LOADS + x) * WAVE + lane, key = at / CH;
+            for (int x = 0; x < V_LOADS; ++x) {
+                const int at = (wave * V_LOADS + x) * WAVE + lane, key = at / CV;
                 if (not_finite(vb[at])) {
                     vb[at] = u32x4_t{0, 0, 0, 0};
                     atomicOr(&bad[key / 32], 1u << key % 32);
@@ -902,8 +914,8 @@ __global__ __launch_bounds__(THREADS, D == 256 ? 1 : 2) void attention_tile_kern
                                    pack_bf16x2(e[6], e[7])};
 #pragma unroll
                 for (int n = 0; n < DT; ++n) {
-                    const int byte = v_read + ((4 * (n % 4)) ^ v_swizzle(v_key)) * 16 + (16 * (n / 4) + (32 * t + 16 * u) * CH) * 16;
-                    const u32x2_t x = read_transposed(vb, byte), y = read_transposed(vb, byte + 8 * CH * 16);
+                    const int byte = v_read + ((4 * n) ^ v_swizzle(v_key)) * 16 + (32 * t + 16 * u) * CV * 16;
+                    const u32x2_t x = read_transposed(vb, byte), y = read_transposed(vb, byte + 8 * CV * 16);
                     o[n] = mfma32(u32x4_t{x[0], x[1], y[0], y[1]}, w, o[n]);
                 }
             }
@@ -923,7 +935,7 @@ __global__ __launch_bounds__(THREADS, D == 256 ? 1 : 2) void attention_tile_kern
     if (my_row >= rows) return;
     if (f.parts == 1) {
         const float inv = l_sum == 0.0f ? 0.0f : 1.0f / l_sum;
-        uint16_t *dst = a.o + (int64_t)(s.start + i) * a.ldo + (int64_t)head * D + 4 * hh;
+        uint16_t *dst = a.o + (int64_t)(s.start + i) * a.ldo + (int64_t)head * D + d0 + 4 * hh;
 #pragma unroll
         for (int n = 0; n < DT; ++n)
 #pragma unroll
@@ -941,9 +953,9 @@ __global__ __launch_bounds__(THREADS, D == 256 ? 1 : 2) void attention_tile_kern
     for (int n = 0; n < DT; ++n)
 #pragma unroll
         for (int x = 0; x < 4; ++x)
-            *reinterpret_cast<float4 *>(out + rr * D + 32 * n + 8 * x + 4 * hh) =
+            *reinterpret_cast<float4 *>(out + rr * D + d0 + 32 * n + 8 * x + 4 * hh) =
                 float4{o[n][4 * x], o[n][4 * x + 1], o[n][4 * x + 2], o[n][4 * x + 3]};
-    if (hh == 0) {
+    if (hh == 0 && d0 == 0) {
         out[TILE_ROWS * D + rr] = m_ref;
         out[TILE_ROWS * D + TILE_ROWS + rr] = l_sum;
     }
@@ -980,7 +992,7 @@ hipError_t launch(const AttentionArgs &a, const Plan &p, float *ws, hipStream_t 
     if (p.rows == 16)
         attention_rows_kernel<D, EXTRA><<<grid, THREADS, 0, s>>>(a, p, ws);
     else
-        attention_tile_kernel<D, EXTRA><<<grid, THREADS, 0, s>>>(a, p, ws);
+        attention_tile_kernel<D, EXTRA><<<dim3(grid.x * (D > 128 ? D / 128 : 1)), THREADS, 0, s>>>(a, p, ws);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess || !p.joins) return e;
     const unsigned heads = (unsigned)(p.joins * a.cache.hkv);
