@@ -31,6 +31,7 @@ typedef unsigned int u32x2_t __attribute__((ext_vector_type(2)));
 typedef __attribute__((address_space(3))) void lds_void;
 
 constexpr int THREADS = 256, WAVES = THREADS / WAVE;
+enum { PLAIN, CAPPED, BIASED };  // scores as they are; capped; less a bias (and capped, or not)
 constexpr float LOG2E = 1.44269504088896340736f;
 // Rows are scaled to a new maximum when it is more than 2^RISE times the old
 // one: weights stay below 2^RISE, whose sums fp32 holds as well.
@@ -48,6 +49,9 @@ __device__ __forceinline__ uint32_t pack_bf16x2(float a, float b) {
     const bf16x2_t v = {(__bf16)a, (__bf16)b};
     return __builtin_bit_cast(uint32_t, v);
 }
+// cap2 tanh(x), v = 2 log2(e) x: 1 - 2 / (1 + e^2x), off by 2^-22 of cap2.
+__device__ __forceinline__ float cap_rest(float v) { return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(v)); }
+__device__ __forceinline__ float capped(float v, float cap2) { return fmaf(-2.0f * cap2, cap_rest(v), cap2); }
 // Largest value and sum over the lanes that hold one query: l, l ^ 32 and, of
 // 16 queries, l ^ 16 and l ^ 48.
 template <bool OF16>
@@ -234,8 +238,17 @@ __device__ __forceinline__ bool plan_find(const AttentionArgs &a, const Plan &p,
         const int C = tiles_to_a_part(p, work), S = (m + C - 1) / C;
         const int all = R * S, split = S > 1 ? all : 0, mine = JOIN ? (S > 1 ? R : 0) : all;
         // (At most items and slots of the plan: they fit in 32 bits.)
-        const int end = wave_inclusive_scan_i32(mine);
-        const int at = (int)item - (end - mine);
+        int before = wave_inclusive_scan_i32(mine) - mine;
+        if (!JOIN && p.row_shift > 4 && a.n_seq > 1) {
+            // The longest parts first.
+            const int size = mine ? (m + S - 1) / S : 0;
+            before = 0;
+            for (int i = 0; i < a.n_seq; ++i) {
+                const int other = __builtin_amdgcn_readlane(size, i);
+                if (other > size || (other == size && i < lane)) before += __builtin_amdgcn_readlane(mine, i);
+            }
+        }
+        const int at = (int)item - before;
         const uint64_t hit = __ballot(at >= 0 && at < mine);
         if (!hit) return false;
         const int b = __builtin_ctzll(hit);
@@ -336,7 +349,7 @@ __device__ __forceinline__ float *slot_of(float *ws, const Plan &p, int hkv, int
 //
 // The weights enter the second product as two bf16, value and remainder (16
 // bits): the matrix cores have time to spare here.
-template <int D, bool EXTRA>
+template <int D, int MODE>
 __global__ __launch_bounds__(THREADS, 2) void attention_rows_kernel(AttentionArgs a, Plan p, float *ws) {
     constexpr int N = 32, ROWS = 16;
     constexpr int KS = D / 32;                       // steps of the first product
@@ -361,9 +374,9 @@ __global__ __launch_bounds__(THREADS, 2) void attention_rows_kernel(AttentionArg
     const int per = uniform((range.count + f.parts - 1) / f.parts);
     const int j_end = min(range.count, (f.part + 1) * per);
     const Query query = load_query(a, s, depth, i);
-    const float scale2 = a.cap > 0.0f ? a.scale / a.cap : a.scale * LOG2E;
+    const float scale2 = a.cap > 0.0f ? a.scale / a.cap * (2.0f * LOG2E) : a.scale * LOG2E;
     const float cap2 = a.cap * LOG2E;
-    const float slope2 = EXTRA && a.slopes ? a.slopes[head] * LOG2E : 0.0f;
+    const float slope2 = MODE == BIASED ? a.slopes[head] * LOG2E : 0.0f;
 
     u32x4_t q[KS];
     {
@@ -449,13 +462,8 @@ __global__ __launch_bounds__(THREADS, 2) void attention_rows_kernel(AttentionArg
 #pragma unroll
             for (int x = 0; x < 4; ++x) {
                 float v = acc[t][x] * scale2;
-                if (EXTRA) {
-                    if (a.cap > 0.0f) v = cap2 * (1.0f - 2.0f * __builtin_amdgcn_rcpf(1.0f + __expf(2.0f * v)));
-                    if (a.slopes) {
-                        const int gap = query.pos - key_pos(a, s, depth, k0 + 16 * t + 4 * g + x);
-                        v -= slope2 * fabsf((float)gap);
-                    }
-                }
+                if (MODE == CAPPED || (MODE == BIASED && a.cap > 0.0f)) v = capped(v, cap2);
+                if (MODE == BIASED) v -= slope2 * fabsf((float)(query.pos - key_pos(a, s, depth, k0 + 16 * t + 4 * g + x)));
                 sc[4 * t + x] = v;
             }
         if (!whole) {
@@ -713,7 +721,7 @@ __device__ __forceinline__ u32x2_t read_transposed(const u32x4_t *lds, int byte)
 //
 // The weights are rounded to bf16 for the second product (half a step, 2^-8 of a
 // weight, random over the keys); their sum is that of the unrounded ones.
-template <int D, bool EXTRA>
+template <int D, int MODE>
 __global__ __launch_bounds__(THREADS, 2) void attention_tile_kernel(AttentionArgs a, Plan p, float *ws) {
     constexpr int DO = D < 128 ? D : 128, HALVES = D / DO;
     constexpr int N = tile_keys(D), CH = D / 8, CV = DO / 8, KT = N / 32, DS = D / 16, DT = DO / 32, NB = N / 16;
@@ -740,9 +748,9 @@ __global__ __launch_bounds__(THREADS, 2) void attention_tile_kernel(AttentionArg
     const Query query = load_query(a, s, depth, i);
     // (A negative scale goes to the queries' signs, so that the largest product has the largest
     // score; above 0, so that -inf stays.)
-    const float scale2 = fmaxf(fabsf(a.cap > 0.0f ? a.scale / a.cap : a.scale * LOG2E), 1e-37f);
+    const float scale2 = fmaxf(fabsf(a.cap > 0.0f ? a.scale / a.cap * (2.0f * LOG2E) : a.scale * LOG2E), 1e-37f);
     const float cap2 = a.cap * LOG2E;
-    const float slope2 = EXTRA && a.slopes ? a.slopes[head] * LOG2E : 0.0f;
+    const float slope2 = MODE == BIASED ? a.slopes[head] * LOG2E : 0.0f;
 
     u32x4_t q[DS];
     {
@@ -842,6 +850,7 @@ __global__ __launch_bounds__(THREADS, 2) void attention_tile_kernel(AttentionArg
             wait_lds();
             lds_barrier();
         }
+        __builtin_amdgcn_s_setprio(2);
         f32x16_t sc[KT];
 #pragma unroll
         for (int t = 0; t < KT; ++t) {
@@ -852,22 +861,24 @@ __global__ __launch_bounds__(THREADS, 2) void attention_tile_kernel(AttentionArg
             for (int k = 0; k < DS; ++k)
                 sc[t] = mfma32(kb[k_read + ((2 * (k % 8) + hh) ^ k_swizzle(c)) + 16 * (k / 8) + 32 * t * CH], q[k], sc[t]);
         }
-        if (EXTRA) {
+        __builtin_amdgcn_s_setprio(1);
+        if (MODE == BIASED) {
+            const bool drafted = a.tree && k0 + N > s.before;
+            const float gap0 = (float)(query.pos - k0 - 4 * hh);
 #pragma unroll
             for (int t = 0; t < KT; ++t)
 #pragma unroll
                 for (int x = 0; x < 16; ++x) {
                     float v = sc[t][x] * scale2;
-                    if (a.cap > 0.0f) v = cap2 * (1.0f - 2.0f * __builtin_amdgcn_rcpf(1.0f + __expf(2.0f * v)));
-                    if (a.slopes) {
-                        const int gap = query.pos - key_pos(a, s, depth, k0 + 32 * t + 8 * (x / 4) + 4 * hh + x % 4);
-                        v -= slope2 * fabsf((float)gap);
-                    }
-                    sc[t][x] = v;
+                    if (a.cap > 0.0f) v = capped(v, cap2);
+                    const int key = 32 * t + 8 * (x / 4) + x % 4;
+                    const float gap = drafted ? (float)(query.pos - key_pos(a, s, depth, k0 + 4 * hh + key)) : gap0 - (float)key;
+                    sc[t][x] = v - slope2 * fabsf(gap);
                 }
         }
+        uint64_t all = ~0ull;
         if (!whole) {
-            uint64_t all = seen(a, s, query, k0);
+            all = seen(a, s, query, k0);
 #pragma unroll
             for (int t = 0; t < NB; ++t)
                 if (!(there >> t & 1)) all &= ~(0xffffull << (16 * t));
@@ -887,7 +898,8 @@ __global__ __launch_bounds__(THREADS, 2) void attention_tile_kernel(AttentionArg
 #pragma unroll
             for (int x = 0; x < 16; ++x) top = fmaxf(top, sc[t][x]);
         top = query_max<false>(top);
-        if (!EXTRA) top *= scale2;
+        if (MODE == PLAIN) top *= scale2;
+        if (MODE == CAPPED && top != -INFINITY) top = capped(top * scale2, cap2);
         if (__any(top > m_ref + RISE)) {
             const float m_new = fmaxf(m_ref, top);
             const float keep = m_new == -INFINITY ? 1.0f : __builtin_amdgcn_exp2f(m_ref - m_new);
@@ -899,6 +911,21 @@ __global__ __launch_bounds__(THREADS, 2) void attention_tile_kernel(AttentionArg
             m_ref = m_new;
         }
         const float m_use = m_ref == -INFINITY ? 0.0f : m_ref;
+        if (MODE == CAPPED) {
+#pragma unroll
+            for (int t = 0; t < KT; ++t)
+#pragma unroll
+                for (int x = 0; x < 16; ++x) sc[t][x] = cap_rest(sc[t][x] * scale2);
+            if (!whole) {
+#pragma unroll
+                for (int t = 0; t < KT; ++t) {
+                    const uint32_t bits = (uint32_t)(all >> (32 * t)) >> (4 * hh);
+#pragma unroll
+                    for (int x = 0; x < 16; ++x) sc[t][x] = bits >> (8 * (x / 4) + x % 4) & 1 ? sc[t][x] : INFINITY;
+                }
+            }
+        }
+        __builtin_amdgcn_s_setprio(0);
 #pragma unroll
         for (int t = 0; t < KT; ++t) {
 #pragma unroll
@@ -907,7 +934,9 @@ __global__ __launch_bounds__(THREADS, 2) void attention_tile_kernel(AttentionArg
 #pragma unroll
                 for (int x = 0; x < 8; ++x) {
                     const float v = sc[t][8 * u + x];
-                    e[x] = __builtin_amdgcn_exp2f(EXTRA ? v - m_use : fmaf(v, scale2, -m_use));
+                    e[x] = __builtin_amdgcn_exp2f(MODE == PLAIN    ? fmaf(v, scale2, -m_use)
+                                                  : MODE == CAPPED ? fmaf(v, -2.0f * cap2, cap2 - m_use)
+                                                                   : v - m_use);
                     l_sum += e[x];
                 }
                 const u32x4_t w = {pack_bf16x2(e[0], e[1]), pack_bf16x2(e[2], e[3]), pack_bf16x2(e[4], e[5]),
@@ -986,13 +1015,13 @@ Plan make_plan(int64_t T, int n_seq, int hq, const Cache &c) {
     return p;
 }
 
-template <int D, bool EXTRA>
-hipError_t launch(const AttentionArgs &a, const Plan &p, float *ws, hipStream_t s) {
+template <int D, int MODE>
+hipError_t launch_mode(const AttentionArgs &a, const Plan &p, float *ws, hipStream_t s) {
     const dim3 grid((unsigned)((int64_t)p.items * a.cache.hkv));
     if (p.rows == 16)
-        attention_rows_kernel<D, EXTRA><<<grid, THREADS, 0, s>>>(a, p, ws);
+        attention_rows_kernel<D, MODE><<<grid, THREADS, 0, s>>>(a, p, ws);
     else
-        attention_tile_kernel<D, EXTRA><<<dim3(grid.x * (D > 128 ? D / 128 : 1)), THREADS, 0, s>>>(a, p, ws);
+        attention_tile_kernel<D, MODE><<<dim3(grid.x * (D > 128 ? D / 128 : 1)), THREADS, 0, s>>>(a, p, ws);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess || !p.joins) return e;
     const unsigned heads = (unsigned)(p.joins * a.cache.hkv);
@@ -1001,6 +1030,12 @@ hipError_t launch(const AttentionArgs &a, const Plan &p, float *ws, hipStream_t 
     else
         attention_join_kernel<D, 1><<<dim3(heads * (p.rows * D / 1024)), THREADS, 0, s>>>(a, p, ws);
     return hipGetLastError();
+}
+
+template <int D>
+hipError_t launch(const AttentionArgs &a, const Plan &p, float *ws, hipStream_t s) {
+    if (a.slopes) return launch_mode<D, BIASED>(a, p, ws, s);
+    return a.cap > 0.0f ? launch_mode<D, CAPPED>(a, p, ws, s) : launch_mode<D, PLAIN>(a, p, ws, s);
 }
 
 }  // namespace
@@ -1012,11 +1047,8 @@ size_t attention_workspace_bytes(int64_t T, int n_seq, int hq, const Cache &c) {
 
 hipError_t launch_attention(const AttentionArgs &a, void *ws, hipStream_t s) {
     const Plan p = make_plan(a.T, a.n_seq, a.hq, a.cache);
-    const bool extra = a.cap > 0.0f || a.slopes;
     float *w = static_cast<float *>(ws);
-    if (a.cache.d == 64) return extra ? launch<64, true>(a, p, w, s) : launch<64, false>(a, p, w, s);
-    if (a.cache.d == 128) return extra ? launch<128, true>(a, p, w, s) : launch<128, false>(a, p, w, s);
-    return extra ? launch<256, true>(a, p, w, s) : launch<256, false>(a, p, w, s);
+    return a.cache.d == 64 ? launch<64>(a, p, w, s) : a.cache.d == 128 ? launch<128>(a, p, w, s) : launch<256>(a, p, w, s);
 }
 
 }  // namespace moeq4
