@@ -111,7 +111,10 @@ def _rows(t, what, dev, shape, types=_SIXTEEN):
     stride open)."""
     if t.dtype not in types or t.shape != shape:
         raise ValueError(f"{what}: expected {tuple(shape)} of {types}, got {tuple(t.shape)} of {t.dtype}")
-    _here(t, dev)
+    if t.get_device() != dev:
+        raise ValueError("moe_q4 takes device tensors of the current device")
+    if t.is_contiguous():
+        return t.data_ptr(), shape[1] if len(shape) == 2 else shape[1] * shape[2]
     st, width = t.stride(), 1
     for d in range(len(shape) - 1, 0, -1):
         if shape[d] != 1 and st[d] != width:

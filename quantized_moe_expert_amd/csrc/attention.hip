@@ -18,7 +18,7 @@
 //
 // How many workgroups share the keys of a block is decided on the device from
 // the sequences' lengths (plan_find), so that a captured call goes with them.
-#include "seq_dev.h"
+#include "rows_dev.h"
 
 namespace moeq4 {
 
@@ -44,10 +44,6 @@ __device__ __forceinline__ f32x4_t mfma16(u32x4_t a, u32x4_t b, f32x4_t c) {
 __device__ __forceinline__ f32x16_t mfma32(u32x4_t a, u32x4_t b, f32x16_t c) {
     return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16v8_t, a), __builtin_bit_cast(bf16v8_t, b),
                                                    c, 0, 0, 0);
-}
-__device__ __forceinline__ uint32_t pack_bf16x2(float a, float b) {
-    const bf16x2_t v = {(__bf16)a, (__bf16)b};
-    return __builtin_bit_cast(uint32_t, v);
 }
 // cap2 tanh(x), v = 2 log2(e) x: 1 - 2 / (1 + e^2x), off by 2^-22 of cap2.
 __device__ __forceinline__ float cap_rest(float v) { return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(v)); }
@@ -185,6 +181,7 @@ struct Plan {
     int rows, row_shift;    // of a block, a power of two
     int key_shift;          // keys of a tile, a power of two
     int cmin, target_shift;
+    int join_groups;        // workgroups that share the rows of a split block (of 16)
     int items, joins, slots;  // most parts; most split blocks; most of their parts (each per head of the cache)
 };
 
@@ -590,14 +587,12 @@ __global__ __launch_bounds__(THREADS, 2) void attention_rows_kernel(AttentionArg
 // Rows of split blocks: four entries to a thread, G groups of threads share the
 // parts of a row.  Bound by the latency of the parts' loads (single tokens: 64
 // parts and more, G as large as a workgroup allows) or by their bytes.
-constexpr int JOIN_GROUPS = 4;  // workgroups to a block of 16 rows: most have fewer
-
 template <int D, int G>
 __global__ __launch_bounds__(THREADS) void attention_join_kernel(AttentionArgs a, Plan p, float *ws) {
     constexpr int TD = D / 4, ROWS = THREADS / (TD * G);
     __shared__ float4 v_part[G > 1 ? G * ROWS : 1][TD];
     __shared__ float m_part[G * ROWS], l_part[G * ROWS];
-    const int groups = G > 1 ? JOIN_GROUPS : p.rows / ROWS;
+    const int groups = G > 1 ? p.join_groups : p.rows / ROWS;
     const int64_t x = blockIdx.x / a.cache.hkv;
     const int hk = blockIdx.x % a.cache.hkv;
     Found f;
@@ -1006,6 +1001,7 @@ Plan make_plan(int64_t T, int n_seq, int hq, const Cache &c) {
     p.target_shift = 0;
     while ((2 << p.target_shift) * c.hkv <= 512) ++p.target_shift;
     const int target = 1 << p.target_shift;
+    p.join_groups = (int)min((int64_t)16, (T * r + n_seq - 1) / n_seq);  // as many as a sequence has rows, on average
     const int64_t blocks = T * r / p.rows + min(T, (int64_t)n_seq);
     const int64_t tiles = ((int64_t)c.max_pages * c.page + (1 << p.key_shift) - 1) >> p.key_shift;
     const int64_t parts = (tiles + p.cmin - 1) / p.cmin;  // of one block, at most
@@ -1026,7 +1022,7 @@ hipError_t launch_mode(const AttentionArgs &a, const Plan &p, float *ws, hipStre
     if (e != hipSuccess || !p.joins) return e;
     const unsigned heads = (unsigned)(p.joins * a.cache.hkv);
     if (p.rows == 16)
-        attention_join_kernel<D, 1024 / D><<<dim3(heads * JOIN_GROUPS), THREADS, 0, s>>>(a, p, ws);
+        attention_join_kernel<D, 1024 / D><<<dim3(heads * p.join_groups), THREADS, 0, s>>>(a, p, ws);
     else
         attention_join_kernel<D, 1><<<dim3(heads * (p.rows * D / 1024)), THREADS, 0, s>>>(a, p, ws);
     return hipGetLastError();

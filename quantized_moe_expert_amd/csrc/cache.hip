@@ -5,7 +5,7 @@
 // Bound by the bytes of the rows, read and written once, and for few tokens by
 // one chain of loads.  One workgroup per token: its rot / 2 angles are computed
 // once, in 64 bits, and kept in LDS for all heads.
-#include "seq_dev.h"
+#include "rows_dev.h"
 
 namespace moeq4 {
 
@@ -14,28 +14,46 @@ namespace {
 constexpr int THREADS = 256;
 constexpr int MAX_HALF = 128;  // pairs of a head of 256
 
-__device__ __forceinline__ void unpack8(u32x4_t w, float *f) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        f[2 * i] = __uint_as_float(w[i] << 16);
-        f[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
-    }
-}
-__device__ __forceinline__ u32x4_t pack8(const float *f) {
-    u32x4_t w;
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-        w[i] = (uint32_t)f32_to_bf16_rne(f[2 * i]) | ((uint32_t)f32_to_bf16_rne(f[2 * i + 1]) << 16);
-    return w;
+__device__ __forceinline__ void turn(float a, float b, float co, float si, float &y0, float &y1) {
+    y0 = fmaf(-b, si, a * co);
+    y1 = fmaf(a, si, b * co);
 }
 
-// Each lane has 8 entries of a head, D / 8 lanes a head.  The partner's entries
-// (half pairs) are loaded beside its own: the second reading is the cache's.
+struct __attribute__((packed, aligned(4))) Eight {
+    float v[8];
+};
+
+// Each lane has 8 entries of a head, D / 8 lanes a head; the partner's entries
+// (half pairs) come from its lane.  The first GROUP heads of a lane are loaded before the token's sequence is
+// looked up: neither waits for the other.
 template <int D>
-__global__ __launch_bounds__(THREADS) void kv_append_kernel(AppendArgs a) {
+__global__ __launch_bounds__(THREADS, 8) void kv_append_kernel(AppendArgs a) {
     constexpr int LPH = D / 8, HPW = WAVE / LPH;  // lanes a head, heads a wave
-    __shared__ float cs[MAX_HALF], sn[MAX_HALF];
+    constexpr int STEP = THREADS / WAVE * HPW, GROUP = 2;
+    __shared__ __attribute__((aligned(16))) float cs[MAX_HALF], sn[MAX_HALF];
     const int64_t t = blockIdx.x;
+    const int tid = threadIdx.x, lane = tid & (WAVE - 1), wave = tid / WAVE;
+    const int c = lane % LPH;  // 8 entries from 8 c on
+    const int heads = a.hq + 2 * a.cache.hkv, half = a.rot / 2;
+    const bool turned = 8 * c < a.rot;
+    int mate = c;  // the chunk of the other halves of the lane's pairs
+    if (turned && !a.interleaved) mate = 16 * c < a.rot ? c + a.rot / 16 : c - a.rot / 16;
+    u32x4_t own[GROUP];
+    auto load = [&](int h0) {
+#pragma unroll
+        for (int u = 0; u < GROUP; ++u) {
+            const int h = h0 + u * STEP;
+            if (h >= heads) continue;
+            const bool is_q = h < a.hq, is_v = h >= a.hq + a.cache.hkv;
+            const int hh = is_q ? h : is_v ? h - a.hq - a.cache.hkv : h - a.hq;
+            const uint16_t *src = (is_q ? a.q + t * a.ldq : is_v ? a.v + t * a.ldv : a.k + t * a.ldk) + hh * D;
+            own[u] = *reinterpret_cast<const u32x4_t *>(src + 8 * c);
+        }
+    };
+    int h0 = wave * HPW + lane / LPH;
+    load(h0);
+    const float freq = tid < half ? a.inv_freq[tid] : 0.0f;
+
     const int b = find_sequence(a.seq_start, a.n_seq, t);
     if (b < 0) return;
     const int64_t end = min((int64_t)a.seq_start[b + 1], a.T);
@@ -51,97 +69,98 @@ __global__ __launch_bounds__(THREADS) void kv_append_kernel(AppendArgs a) {
         const int id = a.cache.table[(int64_t)b * a.cache.max_pages + p];
         if (id >= 0 && id < a.cache.n_pages) page = id;
     }
-    const int half = a.rot / 2;
     if (half) {
-        const int tid = threadIdx.x;
         if (tid < half) {
             const double pos = a.positions ? (double)a.positions[t] : (double)index;
             // In turns: what lies beyond whole ones is exact to 2^-52 of the product.
-            const double turns = pos * (double)a.inv_freq[tid] * 0.15915494309189533577;
-            const double rest = turns - rint(turns);
-            float s, c;
-            sincospif((float)(2.0 * rest), &s, &c);
-            cs[tid] = c;
-            sn[tid] = s;
+            const double turns = pos * (double)freq * 0.15915494309189533577;
+            float si, co;
+            sincospif((float)(2.0 * (turns - rint(turns))), &si, &co);
+            cs[tid] = co;
+            sn[tid] = si;
         }
         __syncthreads();
     }
-    const int lane = threadIdx.x & (WAVE - 1), wave = threadIdx.x / WAVE;
-    const int c = lane % LPH;  // 8 entries from 8 c on
-    const int heads = a.hq + 2 * a.cache.hkv;
-    for (int h0 = wave * HPW; h0 < heads; h0 += THREADS / WAVE * HPW) {
-        const int h = h0 + lane / LPH;
-        if (h >= heads) break;
-        const bool is_q = h < a.hq, is_v = h >= a.hq + a.cache.hkv;
-        const int hh = is_q ? h : (h - a.hq) % a.cache.hkv;
-        const uint16_t *src = is_q ? a.q + t * a.ldq : is_v ? a.v + t * a.ldv : a.k + t * a.ldk;
-        src += (int64_t)hh * D;
-        uint16_t *dst = nullptr;
-        if (is_q)
-            dst = a.q_out + t * a.ldqo + (int64_t)hh * D;
-        else if (page >= 0)
-            dst = (is_v ? a.cache.v : a.cache.k) + ((page * a.cache.hkv + hh) * a.cache.page + off) * D;
-        const u32x4_t raw = *reinterpret_cast<const u32x4_t *>(src + 8 * c);
-        u32x4_t res = raw;
-        if (!is_v) {
-            const float *w = is_q ? a.q_norm : a.k_norm;
-            const bool turned = 8 * c < a.rot;
-            int mate = c;  // the chunk of the other halves of the lane's pairs
-            if (turned && !a.interleaved) mate = 16 * c < a.rot ? c + a.rot / 16 : c - a.rot / 16;
-            float x[8], m[8];
-            unpack8(raw, x);
-            unpack8(mate == c ? raw : *reinterpret_cast<const u32x4_t *>(src + 8 * mate), m);
-            if (w) {
-                float sum = 0.0f;
+    for (; h0 < heads; h0 += GROUP * STEP) {
 #pragma unroll
-                for (int i = 0; i < 8; ++i) sum = fmaf(x[i], x[i], sum);
-                // (The lanes of a head are in one wave and leave the loop together.)
-                sum = seg_sum<LPH>(sum);
-                const float inv = 1.0f / sqrtf(sum * (1.0f / D) + a.eps);
+        for (int u = 0; u < GROUP; ++u) {
+            const int h = h0 + u * STEP;
+            if (h >= heads) continue;  // (for all lanes of a head)
+            const bool is_q = h < a.hq, is_v = h >= a.hq + a.cache.hkv;
+            const int hh = is_q ? h : is_v ? h - a.hq - a.cache.hkv : h - a.hq;
+            uint16_t *dst = nullptr;
+            if (is_q)
+                dst = a.q_out + t * a.ldqo + hh * D;
+            else if (page >= 0)
+                dst = (is_v ? a.cache.v : a.cache.k) + ((page * a.cache.hkv + hh) * a.cache.page + off) * D;
+            const float *w = is_v ? nullptr : is_q ? a.q_norm : a.k_norm;
+            u32x4_t res = own[u];
+            if (!is_v && (w || a.rot)) {
+                float x[8], m[8];
+                unpack8(own[u], x);
+                u32x4_t other = own[u];
+                if (a.rot && !a.interleaved)
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    x[i] *= inv * w[8 * c + i];
-                    m[i] *= inv * w[8 * mate + i];
-                }
-            }
-            if (turned) {
-                float y[8];
-                if (a.interleaved) {
+                    for (int i = 0; i < 4; ++i) other[i] = __shfl(own[u][i], lane - c + mate, WAVE);
+                unpack8(other, m);
+                if (w) {
+                    float sum = 0.0f;
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const float co = cs[4 * c + i], si = sn[4 * c + i];
-                        y[2 * i] = x[2 * i] * co - x[2 * i + 1] * si;
-                        y[2 * i + 1] = x[2 * i + 1] * co + x[2 * i] * si;
-                    }
-                } else {
-                    const bool second = 16 * c >= a.rot;
-                    const int j = 8 * (second ? mate : c);
+                    for (int i = 0; i < 8; ++i) sum = fmaf(x[i], x[i], sum);
+                    sum = seg_sum<LPH>(sum);
+                    const float inv = 1.0f / sqrtf(sum * (1.0f / D) + a.eps);
+                    const Eight wx = *reinterpret_cast<const Eight *>(w + 8 * c);
+                    const Eight wm = *reinterpret_cast<const Eight *>(w + 8 * mate);
 #pragma unroll
                     for (int i = 0; i < 8; ++i) {
-                        const float si = second ? sn[j + i] : -sn[j + i];
-                        y[i] = fmaf(m[i], si, x[i] * cs[j + i]);
+                        x[i] *= inv * wx.v[i];
+                        m[i] *= inv * wm.v[i];
                     }
                 }
+                if (turned) {
+                    float y[8];
+                    if (a.interleaved) {
+                        const float4 co = *reinterpret_cast<const float4 *>(cs + 4 * c);
+                        const float4 si = *reinterpret_cast<const float4 *>(sn + 4 * c);
+                        turn(x[0], x[1], co.x, si.x, y[0], y[1]);
+                        turn(x[2], x[3], co.y, si.y, y[2], y[3]);
+                        turn(x[4], x[5], co.z, si.z, y[4], y[5]);
+                        turn(x[6], x[7], co.w, si.w, y[6], y[7]);
+                    } else {
+                        const bool second = 16 * c >= a.rot;
+                        const int j = 8 * (second ? mate : c);
 #pragma unroll
-                for (int i = 0; i < 8; ++i) x[i] = y[i];
+                        for (int i = 0; i < 8; i += 4) {
+                            const float4 co = *reinterpret_cast<const float4 *>(cs + j + i);
+                            const float4 si = *reinterpret_cast<const float4 *>(sn + j + i);
+                            const float sign = second ? 1.0f : -1.0f;
+                            y[i] = fmaf(m[i], sign * si.x, x[i] * co.x);
+                            y[i + 1] = fmaf(m[i + 1], sign * si.y, x[i + 1] * co.y);
+                            y[i + 2] = fmaf(m[i + 2], sign * si.z, x[i + 2] * co.z);
+                            y[i + 3] = fmaf(m[i + 3], sign * si.w, x[i + 3] * co.w);
+                        }
+                    }
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) x[i] = y[i];
+                }
+                res = pack8(x);
             }
-            if (w || turned) res = pack8(x);
+            if (dst) *reinterpret_cast<u32x4_t *>(dst + 8 * c) = res;
         }
-        if (dst) *reinterpret_cast<u32x4_t *>(dst + 8 * c) = res;
+        if (h0 + GROUP * STEP < heads) load(h0 + GROUP * STEP);
     }
+}
+
+template <int D>
+hipError_t launch(const AppendArgs &a, hipStream_t s) {
+    kv_append_kernel<D><<<dim3((unsigned)a.T), THREADS, 0, s>>>(a);
+    return hipGetLastError();
 }
 
 }  // namespace
 
 hipError_t launch_kv_append(const AppendArgs &a, hipStream_t s) {
-    const dim3 grid((unsigned)a.T);
-    if (a.cache.d == 64)
-        kv_append_kernel<64><<<grid, THREADS, 0, s>>>(a);
-    else if (a.cache.d == 128)
-        kv_append_kernel<128><<<grid, THREADS, 0, s>>>(a);
-    else
-        kv_append_kernel<256><<<grid, THREADS, 0, s>>>(a);
-    return hipGetLastError();
+    return a.cache.d == 64 ? launch<64>(a, s) : a.cache.d == 128 ? launch<128>(a, s) : launch<256>(a, s);
 }
 
 }  // namespace moeq4

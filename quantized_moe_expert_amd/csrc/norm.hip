@@ -5,29 +5,15 @@
 // Bound by the bytes of the rows, each read and written once: a row stays in
 // registers between the two sums of squares.  For few rows: one chain of loads
 // and two sums.
-#include "backbone.h"
+#include "rows_dev.h"
 #include "../../include/moe_q4_backbone.h"
 
 namespace moeq4 {
 
 namespace {
 
-__device__ __forceinline__ void unpack8(u32x4_t w, float *f) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        f[2 * i] = __uint_as_float(w[i] << 16);
-        f[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
-    }
-}
-__device__ __forceinline__ u32x4_t pack8(const float *f) {
-    u32x4_t w;
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-        w[i] = (uint32_t)f32_to_bf16_rne(f[2 * i]) | ((uint32_t)f32_to_bf16_rne(f[2 * i + 1]) << 16);
-    return w;
-}
-
-// Sum over the LANES lanes of a row (a part of a wave, or several waves).
+// Sum over the LANES lanes of a row (a part of a wave, or several waves; part:
+// an array for this sum alone).
 template <int LANES>
 __device__ __forceinline__ float row_sum(float v, float *part) {
     v = seg_sum<(LANES < WAVE ? LANES : WAVE)>(v);
@@ -38,30 +24,32 @@ __device__ __forceinline__ float row_sum(float v, float *part) {
         v = part[0];
 #pragma unroll
         for (int i = 1; i < LANES / WAVE; ++i) v += part[i];
-        __syncthreads();
     }
     return v;
 }
 
-// LANES lanes a row, each with N times 8 values at a distance of LANES * 8.
+// LANES lanes a row, each with N times 8 values at a distance of LANES * 8.  All
+// of a row's loads are issued before the first sum.
 template <int LANES, int N>
-__global__ __launch_bounds__(LANES < 256 ? 256 : LANES) void add_norm_kernel(AddNormArgs a) {
+__global__ __launch_bounds__(LANES < 256 ? 256 : LANES, N == 1 ? 8 : 4) void add_norm_kernel(AddNormArgs a) {
     constexpr int THREADS = LANES < 256 ? 256 : LANES, ROWS = THREADS / LANES;
-    __shared__ float part[THREADS / WAVE];
-    static_assert(LANES <= WAVE || ROWS == 1 || LANES % WAVE == 0, "");
+    static_assert(ROWS == 1 || LANES <= WAVE, "a barrier needs all threads");
+    __shared__ float part[2][THREADS / WAVE];
     const int lane = threadIdx.x % LANES;
     const int64_t t = (int64_t)blockIdx.x * ROWS + threadIdx.x / LANES;
-    const bool live = t < a.T;  // (ROWS > 1 only where a row is within a wave: no barrier is left out)
     const float inv_h = 1.0f / (float)a.H;
     float r[N][8];
+    u32x4_t xr[N], gr[N];
     bool in[N];
 #pragma unroll
     for (int n = 0; n < N; ++n) {
-        const int64_t at = 8 * ((int64_t)n * LANES + lane);
-        in[n] = live && at < a.H;
+        const int at = 8 * (n * LANES + lane);
+        in[n] = t < a.T && at < a.H;
+        xr[n] = gr[n] = u32x4_t{0, 0, 0, 0};
 #pragma unroll
         for (int i = 0; i < 8; ++i) r[n][i] = 0.0f;
-        if (in[n] && a.u) {
+        if (!in[n]) continue;
+        if (a.u) {
             if (a.u_f32) {
                 const float4 *p = reinterpret_cast<const float4 *>(static_cast<const float *>(a.u) + t * a.ldu + at);
                 const float4 p0 = p[0], p1 = p[1];
@@ -71,6 +59,8 @@ __global__ __launch_bounds__(LANES < 256 ? 256 : LANES) void add_norm_kernel(Add
                 unpack8(*reinterpret_cast<const u32x4_t *>(static_cast<const uint16_t *>(a.u) + t * a.ldu + at), r[n]);
             }
         }
+        if (a.gate) gr[n] = *reinterpret_cast<const u32x4_t *>(a.gate + t * a.ldg + at);
+        if (a.x) xr[n] = *reinterpret_cast<const u32x4_t *>(a.x + t * a.ldx + at);
     }
     float inv = 1.0f;
     if (a.post) {
@@ -79,45 +69,45 @@ __global__ __launch_bounds__(LANES < 256 ? 256 : LANES) void add_norm_kernel(Add
         for (int n = 0; n < N; ++n)
 #pragma unroll
             for (int i = 0; i < 8; ++i) sum = fmaf(r[n][i], r[n][i], sum);
-        inv = 1.0f / sqrtf(row_sum<LANES>(sum, part) * inv_h + a.eps);
+        inv = 1.0f / sqrtf(row_sum<LANES>(sum, part[0]) * inv_h + a.eps);
     }
     float sum = 0.0f;
 #pragma unroll
     for (int n = 0; n < N; ++n) {
-        if (!in[n]) continue;
-        const int64_t at = 8 * ((int64_t)n * LANES + lane);
-        if (a.post)
+        const int at = 8 * (n * LANES + lane);
+        float x[8];
+        unpack8(xr[n], x);
+        if (in[n] && a.u) {
+            if (a.post)
 #pragma unroll
-            for (int i = 0; i < 8; ++i) r[n][i] *= inv * a.post[at + i];
-        if (a.gate) {
-            float g[8];
-            unpack8(*reinterpret_cast<const u32x4_t *>(a.gate + t * a.ldg + at), g);
+                for (int i = 0; i < 8; ++i) r[n][i] *= inv * a.post[at + i];
+            if (a.gate) {
+                float g[8];
+                unpack8(gr[n], g);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                if (a.act == MOE_Q4_ACT_SILU)
-                    g[i] = g[i] / (1.0f + expf(-g[i]));
-                else if (a.act == MOE_Q4_ACT_SIGMOID)
-                    g[i] = 1.0f / (1.0f + expf(-g[i]));
-                r[n][i] *= g[i];
+                for (int i = 0; i < 8; ++i) {
+                    if (a.act == MOE_Q4_ACT_SILU)
+                        g[i] = g[i] / (1.0f + expf(-g[i]));
+                    else if (a.act == MOE_Q4_ACT_SIGMOID)
+                        g[i] = 1.0f / (1.0f + expf(-g[i]));
+                    r[n][i] *= g[i];
+                }
             }
-        }
-        float x[8] = {};
-        if (a.x) unpack8(*reinterpret_cast<const u32x4_t *>(a.x + t * a.ldx + at), x);
-        if (a.u)
 #pragma unroll
             for (int i = 0; i < 8; ++i) x[i] = fmaf(a.scale, r[n][i], x[i]);
+        }
         const u32x4_t w = pack8(x);
-        if (a.x_out) *reinterpret_cast<u32x4_t *>(a.x_out + t * a.ldxo + at) = w;
+        if (in[n] && a.x_out) *reinterpret_cast<u32x4_t *>(a.x_out + t * a.ldxo + at) = w;
         unpack8(w, r[n]);
 #pragma unroll
         for (int i = 0; i < 8; ++i) sum = fmaf(r[n][i], r[n][i], sum);
     }
     if (!a.pre) return;
-    inv = 1.0f / sqrtf(row_sum<LANES>(sum, part) * inv_h + a.eps);
+    inv = 1.0f / sqrtf(row_sum<LANES>(sum, part[1]) * inv_h + a.eps);
 #pragma unroll
     for (int n = 0; n < N; ++n) {
         if (!in[n]) continue;
-        const int64_t at = 8 * ((int64_t)n * LANES + lane);
+        const int at = 8 * (n * LANES + lane);
 #pragma unroll
         for (int i = 0; i < 8; ++i) r[n][i] *= inv * a.pre[at + i];
         *reinterpret_cast<u32x4_t *>(a.y + t * a.ldy + at) = pack8(r[n]);
@@ -140,7 +130,7 @@ hipError_t launch_add_norm(const AddNormArgs &a, hipStream_t s) {
     if (chunks <= 32) return launch<32, 1>(a, s);
     if (chunks <= 64) return launch<64, 1>(a, s);
     if (chunks <= 256) return launch<256, 1>(a, s);
-    if (chunks <= 512) return launch<256, 2>(a, s);
+    if (chunks <= 512) return launch<512, 1>(a, s);
     if (chunks <= 1024) return launch<256, 4>(a, s);
     if (chunks <= 2048) return launch<512, 4>(a, s);
     if (chunks <= 4096) return launch<1024, 4>(a, s);

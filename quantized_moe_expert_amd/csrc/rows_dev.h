@@ -1,10 +1,26 @@
-// Packed sequences on the device: which sequence a row belongs to, and where
-// a token of a sequence lies in the paged cache.
+// Rows on the device: eight bf16 values at a time, and which of the packed
+// sequences a row belongs to.
 #pragma once
 
 #include "backbone.h"
 
 namespace moeq4 {
+
+// Two floats rounded to bf16 (nearest even), a in the low half.
+__device__ __forceinline__ uint32_t pack_bf16x2(float a, float b) {
+    const bf16x2_t v = {(__bf16)a, (__bf16)b};
+    return __builtin_bit_cast(uint32_t, v);
+}
+__device__ __forceinline__ u32x4_t pack8(const float *f) {
+    return u32x4_t{pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]), pack_bf16x2(f[6], f[7])};
+}
+__device__ __forceinline__ void unpack8(u32x4_t w, float *f) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        f[2 * i] = __uint_as_float(w[i] << 16);
+        f[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+    }
+}
 
 // The last sequence that starts at or before row t (t >= 0), by the whole wave:
 // 64 starts are looked at in each step.  -1: none.  With ascending starts the
