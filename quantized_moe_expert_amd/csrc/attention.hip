@@ -346,9 +346,11 @@ __device__ __forceinline__ float *slot_of(float *ws, const Plan &p, int hkv, int
 //
 // The weights enter the second product as two bf16, value and remainder (16
 // bits): the matrix cores have time to spare here.
+__host__ __device__ constexpr int rows_keys(int) { return 32; }
+
 template <int D, int MODE>
 __global__ __launch_bounds__(THREADS, 2) void attention_rows_kernel(AttentionArgs a, Plan p, float *ws) {
-    constexpr int N = 32, ROWS = 16;
+    constexpr int N = rows_keys(D), NB = N / 16, ROWS = 16;
     constexpr int KS = D / 32;                       // steps of the first product
     constexpr int VE = D >= 128 ? 8 : 4, VU = D / (16 * VE);
     constexpr int PITCH = D + 4;
@@ -386,16 +388,16 @@ __global__ __launch_bounds__(THREADS, 2) void attention_rows_kernel(AttentionArg
     for (int n = 0; n < VU * VE; ++n) o[n] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
     float m_ref = -INFINITY, l_sum = 0.0f;
 
-    // Where the two blocks of 16 tokens of this wave's next 64 tiles lie: lane l has
+    // Where the blocks of 16 tokens of this wave's next 64 tiles lie: lane l has
     // the l-th tile's, as heads' tokens from the pool's start on (the memory's size keeps them below 2^32).
     const int32_t *table = a.cache.table + (int64_t)f.b * a.cache.max_pages;
     const int last16 = max(s.len - 1, 0) / 16;
-    uint32_t block_at[2];
-    uint64_t page_ok[2];
+    uint32_t block_at[NB];
+    uint64_t page_ok[NB];
     auto load_pages = [&](int j) {
-        const int k16 = 2 * range.tile(min(j + WAVES * lane, range.count - 1));
+        const int k16 = NB * range.tile(min(j + WAVES * lane, range.count - 1));
 #pragma unroll
-        for (int t = 0; t < 2; ++t) {
+        for (int t = 0; t < NB; ++t) {
             const int k = 16 * min(k16 + t, last16), page = k / a.cache.page;
             const int id = table[page];
             const bool ok = id >= 0 && id < a.cache.n_pages;
@@ -404,21 +406,21 @@ __global__ __launch_bounds__(THREADS, 2) void attention_rows_kernel(AttentionArg
         }
     };
     typedef __attribute__((ext_vector_type(VE / 2))) uint32_t vload_t;
-    u32x4_t kr[2][KS];
-    vload_t vr[2][4][VU];
+    u32x4_t kr[NB][KS];
+    vload_t vr[NB][4][VU];
     auto block = [&](int u, int t) { return (int64_t)(uint32_t)__builtin_amdgcn_readlane(block_at[t], u) * D; };
-    auto load_k = [&](int64_t b0, int64_t b1) {
+    auto load_k = [&](int at) {
 #pragma unroll
-        for (int t = 0; t < 2; ++t) {
-            const uint16_t *src = a.cache.k + (t ? b1 : b0) + c * D + 8 * g;
+        for (int t = 0; t < NB; ++t) {
+            const uint16_t *src = a.cache.k + block(at, t) + c * D + 8 * g;
 #pragma unroll
             for (int k = 0; k < KS; ++k) kr[t][k] = *reinterpret_cast<const u32x4_t *>(src + 32 * k);
         }
     };
-    auto load_v = [&](int64_t b0, int64_t b1) {
+    auto load_v = [&](int at) {
 #pragma unroll
-        for (int t = 0; t < 2; ++t) {
-            const uint16_t *src = a.cache.v + (t ? b1 : b0) + 4 * g * D + VE * c;
+        for (int t = 0; t < NB; ++t) {
+            const uint16_t *src = a.cache.v + block(at, t) + 4 * g * D + VE * c;
 #pragma unroll
             for (int x = 0; x < 4; ++x)
 #pragma unroll
@@ -429,16 +431,17 @@ __global__ __launch_bounds__(THREADS, 2) void attention_rows_kernel(AttentionArg
     int j = f.part * per + wave, at = 0;
     if (j < j_end) {
         load_pages(j);
-        const int64_t b0 = block(0, 0), b1 = block(0, 1);
-        load_k(b0, b1);
-        load_v(b0, b1);
+        load_k(0);
+        load_v(0);
     }
     for (; j < j_end; j += WAVES) {
         const int k0 = N * range.tile(j);
-        const bool ok0 = page_ok[0] >> at & 1, ok1 = page_ok[1] >> at & 1;
-        f32x4_t acc[2];
+        uint32_t there = 0;
 #pragma unroll
-        for (int t = 0; t < 2; ++t) {
+        for (int t = 0; t < NB; ++t) there |= (uint32_t)(page_ok[t] >> at & 1) << t;
+        f32x4_t acc[NB];
+#pragma unroll
+        for (int t = 0; t < NB; ++t) {
             acc[t] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
             for (int k = 0; k < KS; ++k) acc[t] = mfma16(kr[t][k], q[k], acc[t]);
@@ -449,13 +452,12 @@ __global__ __launch_bounds__(THREADS, 2) void attention_rows_kernel(AttentionArg
             load_pages(next);
             at = 0;
         }
-        const int64_t b0 = block(at, 0), b1 = block(at, 1);
-        load_k(b0, b1);
+        load_k(at);
 
-        const bool whole = ok0 && ok1 && sees_all<N>(a, s, i0, i1, k0);
-        float sc[8];
+        const bool whole = there == (1u << NB) - 1 && sees_all<N>(a, s, i0, i1, k0);
+        float sc[4 * NB];
 #pragma unroll
-        for (int t = 0; t < 2; ++t)
+        for (int t = 0; t < NB; ++t)
 #pragma unroll
             for (int x = 0; x < 4; ++x) {
                 float v = acc[t][x] * scale2;
@@ -464,14 +466,16 @@ __global__ __launch_bounds__(THREADS, 2) void attention_rows_kernel(AttentionArg
                 sc[4 * t + x] = v;
             }
         if (!whole) {
-            const uint32_t there = (ok0 ? 0xffffu : 0u) | (ok1 ? 0xffff0000u : 0u);
-            const uint32_t bits = ((uint32_t)seen(a, s, query, k0) & there) >> (4 * g);
+            const uint64_t bits = seen(a, s, query, k0) >> (4 * g);
 #pragma unroll
-            for (int x = 0; x < 8; ++x) sc[x] = bits >> (16 * (x / 4) + x % 4) & 1 ? sc[x] : -INFINITY;
+            for (int t = 0; t < NB; ++t)
+#pragma unroll
+                for (int x = 0; x < 4; ++x)
+                    sc[4 * t + x] = (there >> t & 1) && (bits >> (16 * t + x) & 1) ? sc[4 * t + x] : -INFINITY;
         }
         float top = sc[0];
 #pragma unroll
-        for (int x = 1; x < 8; ++x) top = fmaxf(top, sc[x]);
+        for (int x = 1; x < 4 * NB; ++x) top = fmaxf(top, sc[x]);
         top = query_max<true>(top);
         if (__any(top > m_ref + RISE)) {
             const float m_new = fmaxf(m_ref, top);
@@ -482,9 +486,9 @@ __global__ __launch_bounds__(THREADS, 2) void attention_rows_kernel(AttentionArg
             m_ref = m_new;
         }
         const float m_use = m_ref == -INFINITY ? 0.0f : m_ref;
-        float w[8];
+        float w[4 * NB];
 #pragma unroll
-        for (int x = 0; x < 8; ++x) {
+        for (int x = 0; x < 4 * NB; ++x) {
             w[x] = __builtin_amdgcn_exp2f(sc[x] - m_use);
             l_sum += w[x];
         }
@@ -492,7 +496,7 @@ __global__ __launch_bounds__(THREADS, 2) void attention_rows_kernel(AttentionArg
             // 0 times NaN or infinity: values of keys that some row does not see are
             // cleared, and the rows that see one get NaN for it.
 #pragma unroll
-            for (int t = 0; t < 2; ++t)
+            for (int t = 0; t < NB; ++t)
 #pragma unroll
                 for (int x = 0; x < 4; ++x) {
                     bool bad = false;
@@ -509,26 +513,30 @@ __global__ __launch_bounds__(THREADS, 2) void attention_rows_kernel(AttentionArg
                     if ((__ballot(bad) >> (16 * g) & 0xffffu) && sc[4 * t + x] != -INFINITY) w[4 * t + x] = NAN;
                 }
         }
-        u32x4_t hi, lo;
 #pragma unroll
-        for (int x = 0; x < 4; ++x) {
-            hi[x] = pack_bf16x2(w[2 * x], w[2 * x + 1]);
-            lo[x] = pack_bf16x2(w[2 * x] - __uint_as_float(hi[x] << 16),
-                                w[2 * x + 1] - __uint_as_float(hi[x] & 0xffff0000u));
-        }
+        for (int y = 0; y < NB / 2; ++y) {  // 32 keys
+            u32x4_t hi, lo;
 #pragma unroll
-        for (int u = 0; u < VU; ++u)
-#pragma unroll
-            for (int e = 0; e < VE; ++e) {
-                const uint32_t sel = e & 1 ? 0x07060302u : 0x05040100u;
-                u32x4_t v;
-#pragma unroll
-                for (int x = 0; x < 4; ++x)
-                    v[x] = __builtin_amdgcn_perm(vr[x / 2][2 * (x & 1) + 1][u][e / 2], vr[x / 2][2 * (x & 1)][u][e / 2], sel);
-                o[VE * u + e] = mfma16(v, hi, o[VE * u + e]);
-                o[VE * u + e] = mfma16(v, lo, o[VE * u + e]);
+            for (int x = 0; x < 4; ++x) {
+                const float w0 = w[8 * y + 2 * x], w1 = w[8 * y + 2 * x + 1];
+                hi[x] = pack_bf16x2(w0, w1);
+                lo[x] = pack_bf16x2(w0 - __uint_as_float(hi[x] << 16), w1 - __uint_as_float(hi[x] & 0xffff0000u));
             }
-        load_v(b0, b1);
+#pragma unroll
+            for (int u = 0; u < VU; ++u)
+#pragma unroll
+                for (int e = 0; e < VE; ++e) {
+                    const uint32_t sel = e & 1 ? 0x07060302u : 0x05040100u;
+                    u32x4_t v;
+#pragma unroll
+                    for (int x = 0; x < 4; ++x)
+                        v[x] = __builtin_amdgcn_perm(vr[2 * y + x / 2][2 * (x & 1) + 1][u][e / 2],
+                                                     vr[2 * y + x / 2][2 * (x & 1)][u][e / 2], sel);
+                    o[VE * u + e] = mfma16(v, hi, o[VE * u + e]);
+                    o[VE * u + e] = mfma16(v, lo, o[VE * u + e]);
+                }
+        }
+        load_v(at);
     }
 
     // The waves' parts over their common maximum.
@@ -741,6 +749,7 @@ __global__ __launch_bounds__(THREADS, 2) void attention_tile_kernel(AttentionArg
     const int per = uniform((range.count + f.parts - 1) / f.parts);
     const int j0 = f.part * per, j_end = min(range.count, j0 + per);
     const Query query = load_query(a, s, depth, i);
+    const bool idle = row0 + wave * 32 >= rows;  // a wave without rows brings keys for the others
     // (A negative scale goes to the queries' signs, so that the largest product has the largest
     // score; above 0, so that -inf stays.)
     const float scale2 = fmaxf(fabsf(a.cap > 0.0f ? a.scale / a.cap * (2.0f * LOG2E) : a.scale * LOG2E), 1e-37f);
@@ -845,6 +854,14 @@ __global__ __launch_bounds__(THREADS, 2) void attention_tile_kernel(AttentionArg
             wait_lds();
             lds_barrier();
         }
+        uint64_t all = ~0ull;  // keys that the lane's query sees
+        if (!whole) {
+            all = seen(a, s, query, k0);
+#pragma unroll
+            for (int t = 0; t < NB; ++t)
+                if (!(there >> t & 1)) all &= ~(0xffffull << (16 * t));
+        }
+        if (idle || !__any(all != 0)) return;
         __builtin_amdgcn_s_setprio(2);
         f32x16_t sc[KT];
 #pragma unroll
@@ -871,12 +888,7 @@ __global__ __launch_bounds__(THREADS, 2) void attention_tile_kernel(AttentionArg
                     sc[t][x] = v - slope2 * fabsf(gap);
                 }
         }
-        uint64_t all = ~0ull;
         if (!whole) {
-            all = seen(a, s, query, k0);
-#pragma unroll
-            for (int t = 0; t < NB; ++t)
-                if (!(there >> t & 1)) all &= ~(0xffffull << (16 * t));
 #pragma unroll
             for (int t = 0; t < KT; ++t) {
                 const uint32_t bits = (uint32_t)(all >> (32 * t)) >> (4 * hh), spoiled = bad[t] >> (4 * hh);
@@ -996,10 +1008,10 @@ Plan make_plan(int64_t T, int n_seq, int hq, const Cache &c) {
     const bool few = few_rows(T, n_seq, r);
     p.row_shift = few ? 4 : 7;
     p.rows = 1 << p.row_shift;
-    p.key_shift = few || tile_keys(c.d) == 32 ? 5 : 6;
+    p.key_shift = (few ? rows_keys(c.d) : tile_keys(c.d)) == 32 ? 5 : 6;
     p.cmin = few ? WAVES : 2;
     p.target_shift = 0;
-    while ((2 << p.target_shift) * c.hkv <= 512) ++p.target_shift;
+    while ((2 << p.target_shift) * c.hkv <= (few ? 1024 : 512)) ++p.target_shift;
     const int target = 1 << p.target_shift;
     p.join_groups = (int)min((int64_t)16, (T * r + n_seq - 1) / n_seq);  // as many as a sequence has rows, on average
     const int64_t blocks = T * r / p.rows + min(T, (int64_t)n_seq);
