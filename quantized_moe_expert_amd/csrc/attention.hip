@@ -45,6 +45,12 @@ __device__ __forceinline__ f32x16_t mfma32(u32x4_t a, u32x4_t b, f32x16_t c) {
     return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16v8_t, a), __builtin_bit_cast(bf16v8_t, b),
                                                    c, 0, 0, 0);
 }
+// What a product is multiplied by: to a power of two's exponent, or (capped) to v
+// below.  Finite, so that a product of 0 stays one.
+__device__ __forceinline__ float score_scale(const AttentionArgs &a) {
+    const float v = a.cap > 0.0f ? a.scale / a.cap * (2.0f * LOG2E) : a.scale * LOG2E;
+    return fminf(fmaxf(v, -3e38f), 3e38f);
+}
 // cap2 tanh(x), v = 2 log2(e) x: 1 - 2 / (1 + e^2x), off by 2^-22 of cap2.
 __device__ __forceinline__ float cap_rest(float v) { return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(v)); }
 __device__ __forceinline__ float capped(float v, float cap2) { return fmaf(-2.0f * cap2, cap_rest(v), cap2); }
@@ -373,7 +379,7 @@ __global__ __launch_bounds__(THREADS, 2) void attention_rows_kernel(AttentionArg
     const int per = uniform((range.count + f.parts - 1) / f.parts);
     const int j_end = min(range.count, (f.part + 1) * per);
     const Query query = load_query(a, s, depth, i);
-    const float scale2 = a.cap > 0.0f ? a.scale / a.cap * (2.0f * LOG2E) : a.scale * LOG2E;
+    const float scale2 = score_scale(a);
     const float cap2 = a.cap * LOG2E;
     const float slope2 = MODE == BIASED ? a.slopes[head] * LOG2E : 0.0f;
 
@@ -477,9 +483,11 @@ __global__ __launch_bounds__(THREADS, 2) void attention_rows_kernel(AttentionArg
 #pragma unroll
         for (int x = 1; x < 4 * NB; ++x) top = fmaxf(top, sc[x]);
         top = query_max<true>(top);
-        if (__any(top > m_ref + RISE)) {
-            const float m_new = fmaxf(m_ref, top);
-            const float keep = m_new == -INFINITY ? 1.0f : __builtin_amdgcn_exp2f(m_ref - m_new);
+        const bool rise = top > m_ref + RISE;
+        if (__any(rise)) {
+            // (Each row by its own scores: its bits do not depend on the rows beside it.)
+            const float m_new = rise ? top : m_ref;
+            const float keep = rise ? __builtin_amdgcn_exp2f(m_ref - m_new) : 1.0f;
             l_sum *= keep;
 #pragma unroll
             for (int n = 0; n < VU * VE; ++n) o[n] *= keep;
@@ -558,7 +566,7 @@ __global__ __launch_bounds__(THREADS, 2) void attention_rows_kernel(AttentionArg
     const int live = min(ROWS, rows - row0);
     const bool direct = f.parts == 1;
     const int64_t slot = (int64_t)f.slot + f.part;
-    if (!direct && slot >= p.slots) return;  // (starts that do not ascend)
+    if (!direct && (uint64_t)slot >= (uint64_t)p.slots) return;  // (starts that do not ascend)
     float *out = direct ? nullptr : slot_of<D>(ws, p, a.cache.hkv, slot, hk);
     for (int x = threadIdx.x; x < live * (D / 4); x += THREADS) {
         const int rr = x / (D / 4), d = 4 * (x % (D / 4));
@@ -607,72 +615,72 @@ __global__ __launch_bounds__(THREADS) void attention_join_kernel(AttentionArgs a
     if (!plan_find<true>(a, p, x / groups, f)) return;
     const Seq s = uniform(f.seq);
     const int r = a.hq / a.cache.hkv;
-    if ((int64_t)f.slot + f.parts > p.slots) return;
+    if (f.slot < 0 || (int64_t)f.slot + f.parts > p.slots) return;  // (starts that do not ascend)
     const int sub = threadIdx.x / TD, g = sub / ROWS, d = 4 * (threadIdx.x % TD);
     const int64_t stride = (int64_t)a.cache.hkv * p.rows * (D + 2);
     const float *part = slot_of<D>(ws, p, a.cache.hkv, f.slot, hk);
     const int live = min(p.rows, s.n * r - f.block * p.rows);
     for (int row0 = (int)(x % groups) * ROWS; row0 < live; row0 += groups * ROWS) {
-    // (Rows behind the sequence's last are in the slots too, as whatever is there; they are not stored.)
-    const int rr = row0 + sub % ROWS, row = f.block * p.rows + rr;
-    const float *ms = part + p.rows * D + rr, *ls = ms + p.rows;
-    float top = -INFINITY, sum = 0.0f;
-    float4 v = {0.0f, 0.0f, 0.0f, 0.0f};
-    for (int i0 = g; i0 < f.parts; i0 += 8 * G) {
-        // Eight parts at once (past the end the last one again, with weight 0).
-        float mi[8], li[8];
-        float4 y[8];
+        // (Rows behind the sequence's last are in the slots too, as whatever is there; they are not stored.)
+        const int rr = row0 + sub % ROWS, row = f.block * p.rows + rr;
+        const float *ms = part + p.rows * D + rr, *ls = ms + p.rows;
+        float top = -INFINITY, sum = 0.0f;
+        float4 v = {0.0f, 0.0f, 0.0f, 0.0f};
+        for (int i0 = g; i0 < f.parts; i0 += 8 * G) {
+            // Eight parts at once (past the end the last one again, with weight 0).
+            float mi[8], li[8];
+            float4 y[8];
 #pragma unroll
-        for (int u = 0; u < 8; ++u) {
-            const int i = min(i0 + u * G, f.parts - 1);
-            mi[u] = ms[i * stride];
-            li[u] = ls[i * stride];
-            y[u] = *reinterpret_cast<const float4 *>(part + i * stride + rr * D + d);
-        }
-        float now = top;
+            for (int u = 0; u < 8; ++u) {
+                const int i = min(i0 + u * G, f.parts - 1);
+                mi[u] = ms[i * stride];
+                li[u] = ls[i * stride];
+                y[u] = *reinterpret_cast<const float4 *>(part + i * stride + rr * D + d);
+            }
+            float now = top;
 #pragma unroll
-        for (int u = 0; u < 8; ++u) {
-            if (i0 + u * G >= f.parts) mi[u] = -INFINITY;
-            now = fmaxf(now, mi[u]);
-        }
-        const float keep = top == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(top - now);
-        top = now;
-        sum *= keep;
-        v.x *= keep, v.y *= keep, v.z *= keep, v.w *= keep;
+            for (int u = 0; u < 8; ++u) {
+                if (i0 + u * G >= f.parts) mi[u] = -INFINITY;
+                now = fmaxf(now, mi[u]);
+            }
+            const float keep = top == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(top - now);
+            top = now;
+            sum *= keep;
+            v.x *= keep, v.y *= keep, v.z *= keep, v.w *= keep;
 #pragma unroll
-        for (int u = 0; u < 8; ++u) {
-            if (mi[u] == -INFINITY) continue;
-            const float k = __builtin_amdgcn_exp2f(mi[u] - top);
-            sum = fmaf(k, li[u], sum);
-            v.x = fmaf(k, y[u].x, v.x), v.y = fmaf(k, y[u].y, v.y);
-            v.z = fmaf(k, y[u].z, v.z), v.w = fmaf(k, y[u].w, v.w);
+            for (int u = 0; u < 8; ++u) {
+                if (mi[u] == -INFINITY) continue;
+                const float k = __builtin_amdgcn_exp2f(mi[u] - top);
+                sum = fmaf(k, li[u], sum);
+                v.x = fmaf(k, y[u].x, v.x), v.y = fmaf(k, y[u].y, v.y);
+                v.z = fmaf(k, y[u].z, v.z), v.w = fmaf(k, y[u].w, v.w);
+            }
         }
-    }
-    if (G > 1) {
-        __syncthreads();
-        if (d == 0) {
-            m_part[sub] = top;
-            l_part[sub] = sum;
-        }
-        v_part[sub][d / 4] = v;
-        __syncthreads();
+        if (G > 1) {
+            __syncthreads();
+            if (d == 0) {
+                m_part[sub] = top;
+                l_part[sub] = sum;
+            }
+            v_part[sub][d / 4] = v;
+            __syncthreads();
 #pragma unroll
-        for (int i = 0; i < G; ++i) top = fmaxf(top, m_part[sub % ROWS + i * ROWS]);
-        sum = 0.0f;
-        v = float4{0.0f, 0.0f, 0.0f, 0.0f};
+            for (int i = 0; i < G; ++i) top = fmaxf(top, m_part[sub % ROWS + i * ROWS]);
+            sum = 0.0f;
+            v = float4{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-        for (int i = 0; i < G; ++i) {
-            const float mi = m_part[sub % ROWS + i * ROWS];
-            const float k = mi == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(mi - top);
-            const float4 y = v_part[sub % ROWS + i * ROWS][d / 4];
-            sum = fmaf(k, l_part[sub % ROWS + i * ROWS], sum);
-            v.x = fmaf(k, y.x, v.x), v.y = fmaf(k, y.y, v.y), v.z = fmaf(k, y.z, v.z), v.w = fmaf(k, y.w, v.w);
+            for (int i = 0; i < G; ++i) {
+                const float mi = m_part[sub % ROWS + i * ROWS];
+                const float k = mi == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(mi - top);
+                const float4 y = v_part[sub % ROWS + i * ROWS][d / 4];
+                sum = fmaf(k, l_part[sub % ROWS + i * ROWS], sum);
+                v.x = fmaf(k, y.x, v.x), v.y = fmaf(k, y.y, v.y), v.z = fmaf(k, y.z, v.z), v.w = fmaf(k, y.w, v.w);
+            }
         }
-    }
-    if (g > 0 || rr >= live) continue;
-    const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
-    uint16_t *dst = a.o + (int64_t)(s.start + row / r) * a.ldo + (int64_t)(hk * r + row % r) * D + d;
-    *reinterpret_cast<uint2 *>(dst) = uint2{pack_bf16x2(v.x * inv, v.y * inv), pack_bf16x2(v.z * inv, v.w * inv)};
+        if (g > 0 || rr >= live) continue;
+        const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+        uint16_t *dst = a.o + (int64_t)(s.start + row / r) * a.ldo + (int64_t)(hk * r + row % r) * D + d;
+        *reinterpret_cast<uint2 *>(dst) = uint2{pack_bf16x2(v.x * inv, v.y * inv), pack_bf16x2(v.z * inv, v.w * inv)};
     }
 }
 
@@ -752,7 +760,7 @@ __global__ __launch_bounds__(THREADS, 2) void attention_tile_kernel(AttentionArg
     const bool idle = row0 + wave * 32 >= rows;  // a wave without rows brings keys for the others
     // (A negative scale goes to the queries' signs, so that the largest product has the largest
     // score; above 0, so that -inf stays.)
-    const float scale2 = fmaxf(fabsf(a.cap > 0.0f ? a.scale / a.cap * (2.0f * LOG2E) : a.scale * LOG2E), 1e-37f);
+    const float scale2 = fmaxf(fabsf(score_scale(a)), 1e-37f);
     const float cap2 = a.cap * LOG2E;
     const float slope2 = MODE == BIASED ? a.slopes[head] * LOG2E : 0.0f;
 
@@ -907,9 +915,11 @@ __global__ __launch_bounds__(THREADS, 2) void attention_tile_kernel(AttentionArg
         top = query_max<false>(top);
         if (MODE == PLAIN) top *= scale2;
         if (MODE == CAPPED && top != -INFINITY) top = capped(top * scale2, cap2);
-        if (__any(top > m_ref + RISE)) {
-            const float m_new = fmaxf(m_ref, top);
-            const float keep = m_new == -INFINITY ? 1.0f : __builtin_amdgcn_exp2f(m_ref - m_new);
+        const bool rise = top > m_ref + RISE;
+        if (__any(rise)) {
+            // (Each row by its own scores: its bits do not depend on the rows beside it.)
+            const float m_new = rise ? top : m_ref;
+            const float keep = rise ? __builtin_amdgcn_exp2f(m_ref - m_new) : 1.0f;
             l_sum *= keep;
 #pragma unroll
             for (int n = 0; n < DT; ++n)
@@ -966,6 +976,7 @@ __global__ __launch_bounds__(THREADS, 2) void attention_tile_kernel(AttentionArg
             step(j + 1, k_b, v_b, k_a, v_a, bad_b);
         }
         if (j < j_end) step(j, k_a, v_a, k_b, v_b, bad_a);
+        wait_loads();  // (nothing comes to LDS after the end)
     }
     l_sum = query_sum<false>(l_sum);
     if (my_row >= rows) return;
@@ -982,7 +993,7 @@ __global__ __launch_bounds__(THREADS, 2) void attention_tile_kernel(AttentionArg
         return;
     }
     const int64_t slot = (int64_t)f.slot + f.part;
-    if (slot >= p.slots) return;  // (starts that do not ascend)
+    if ((uint64_t)slot >= (uint64_t)p.slots) return;  // (starts that do not ascend)
     const int rr = wave * 32 + c;
     float *out = slot_of<D>(ws, p, a.cache.hkv, slot, hk);
 #pragma unroll

@@ -315,3 +315,64 @@ def test_binding_refusals():
             bad()
     with pytest.raises(m.MoeQ4Error):
         c.run(prefix=torch.zeros(1, dtype=torch.int32, device="cuda"), tree=torch.zeros(2, dtype=torch.int64, device="cuda"))
+
+
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("scale", [-0.1, 0.0, 1e-30, 2.0])
+@pytest.mark.parametrize("lens,hist", [([1, 2], [100, 600]), ([70], [40])])
+def test_scales(d, scale, lens, hist):
+    for kw in ({}, {"cap": 5.0}, {"slopes": torch.tensor([0.5, 0.01, 0.0, 1.0], device="cuda")}):
+        c = Case(lens, hist, 4, 2, d, 16, seed=3, q_scale=0.5)
+        c.scale = scale
+        both(c, f"scale {scale} {kw}", **kw)
+
+
+@pytest.mark.parametrize("cap", [1e-30, 1e-3, 1e6])
+def test_caps_of_any_size(cap):
+    for lens, hist in (([1], [300]), ([60], [20])):
+        both(Case(lens, hist, 4, 2, 128, 16, seed=3), f"cap {cap}", cap=cap)
+
+
+@pytest.mark.parametrize("window", [2, 1000, (1 << 31) - 1])
+@pytest.mark.parametrize("lens,hist", [([1, 1], [2500, 10]), ([100], [1500])])
+def test_windows(window, lens, hist):
+    both(Case(lens, hist, 4, 2, 64, 16, seed=3), f"window {window}", window=window)
+    both(Case(lens, hist, 4, 2, 64, 16, seed=3), f"window {window} and prefix", window=window,
+         prefix=torch.full((len(lens),), 70, dtype=torch.int32, device="cuda"))
+
+
+@pytest.mark.parametrize("hq", [100, 300, 1024])
+def test_many_query_heads_on_one(hq):
+    for lens, hist in (([1, 2], [50, 700]), ([5], [0])):
+        both(Case(lens, hist, hq, 1, 64, 16, seed=1), f"{hq} heads on one")
+
+
+@pytest.mark.parametrize("lens,hist", [([200] + [1] * 300, [50] + [7] * 300), ([300, 1, 1, 1], [10, 2000, 5, 0]),
+                                       ([0] * 70 + [40], [3] * 71), ([0] * 200 + [1], [5] * 200 + [3000])])
+def test_sequences_of_another_kind(lens, hist):
+    """A prompt among single tokens, single tokens beside a prompt, sequences without rows."""
+    both(Case(lens, hist, 4, 2, 64, 16, seed=1), f"{len(lens)} sequences")
+
+
+@pytest.mark.parametrize("d,n", [(64, 1), (128, 1), (64, 33), (256, 20)])
+def test_more_than_a_wave_of_sequences(d, n):
+    """The plan over several waves, with blocks that are split."""
+    B = 90
+    hist = [(i * 17) % 60 for i in range(B)]
+    hist[5], hist[70], hist[89] = 3000, 1500, 2200
+    both(Case([n + i % 2 for i in range(B)], hist, 4, 1, d, 32, seed=1), f"{B} sequences of {n} rows")
+
+
+def test_starts_that_do_not_ascend_stay_in_bounds():
+    """Numbers are undefined; nothing outside o and the workspace is written (guard bytes on both sides)."""
+    for B, n in ((40, 1), (300, 1), (40, 30), (300, 9)):
+        c = Case([n] * B, [200] * B, 4, 2, 64, 16, seed=1)
+        gen = torch.Generator().manual_seed(2)
+        c.start.copy_(torch.randint(-5, c.T + 9, (B + 1,), generator=gen))
+        size = m.attention_workspace_size(c.T, B, 4, c.cache)
+        ws = torch.full((size + 512,), 77, dtype=torch.uint8, device="cuda")
+        out = torch.full((c.T + 16, 4, 64), 7.0, dtype=torch.bfloat16, device="cuda")
+        c.run(o=out[8:8 + c.T], ws=ws[256:256 + size])
+        torch.cuda.synchronize()
+        assert (ws[:256] == 77).all() and (ws[256 + size:] == 77).all()
+        assert (out[:8] == 7).all() and (out[8 + c.T:] == 7).all()
