@@ -23,7 +23,7 @@ from ._backbone import (ACT_GELU, ACT_NONE, ACT_SIGMOID, ACT_SILU, BACKBONE_EXPO
                         kv_cache_struct, linear_struct, logprobs_workspace_size, moe_q4_add_norm, moe_q4_attention,
                         moe_q4_delta_decode, moe_q4_delta_prefill, moe_q4_kv_append, moe_q4_linear, moe_q4_logprobs)
 from .layer import MoeQ4Layer
-from .mixer import DeltaMixer
+from .mixer import AttentionMixer, DeltaMixer
 
 __all__ = ["ASYM_G64", "SYM_G128", "FP8_B128", "NVFP4", "WS_DECODE", "WS_GROUP", "WS_PREFILL", "WS_ROUTE", "EXPORTS", "MoeQ4Error",
            "error_string", "layer_struct", "lib", "moe_q4_decode", "moe_q4_dequant", "moe_q4_group",
@@ -38,4 +38,4 @@ __all__ = ["ASYM_G64", "SYM_G128", "FP8_B128", "NVFP4", "WS_DECODE", "WS_GROUP",
            "LinearWeights", "delta_workspace_size", "linear_struct", "logprobs_workspace_size",
            "moe_q4_delta_decode", "moe_q4_delta_prefill", "moe_q4_linear", "moe_q4_logprobs", "DeltaMixer",
            "ACT_SIGMOID", "KVCache", "attention_workspace_size", "kv_cache_struct", "moe_q4_add_norm", "moe_q4_attention",
-           "moe_q4_kv_append"]
+           "moe_q4_kv_append", "AttentionMixer"]
