@@ -187,7 +187,7 @@ struct Plan {
     int rows, row_shift;    // of a block, a power of two
     int key_shift;          // keys of a tile, a power of two
     int cmin, target_shift;
-    int join_groups;        // workgroups that share the rows of a split block (of 16)
+    int join_groups;        // workgroups that share the rows of a split block (share_parts)
     int items, joins, slots;  // most parts; most split blocks; most of their parts (each per head of the cache)
 };
 
@@ -1024,7 +1024,8 @@ Plan make_plan(int64_t T, int n_seq, int hq, const Cache &c) {
     p.target_shift = 0;
     while ((2 << p.target_shift) * c.hkv <= (few ? 1024 : 512)) ++p.target_shift;
     const int target = 1 << p.target_shift;
-    p.join_groups = (int)min((int64_t)16, (T * r + n_seq - 1) / n_seq);  // as many as a sequence has rows, on average
+    // Of 16 rows as many as a sequence has, on average.
+    p.join_groups = few ? (int)min((int64_t)16, (T * r + n_seq - 1) / n_seq) : p.rows;
     const int64_t blocks = T * r / p.rows + min(T, (int64_t)n_seq);
     const int64_t tiles = ((int64_t)c.max_pages * c.page + (1 << p.key_shift) - 1) >> p.key_shift;
     const int64_t parts = (tiles + p.cmin - 1) / p.cmin;  // of one block, at most
@@ -1033,6 +1034,11 @@ Plan make_plan(int64_t T, int n_seq, int hq, const Cache &c) {
     p.slots = parts > 1 ? (int)min(blocks * parts, (int64_t)2 * target) : 0;
     return p;
 }
+
+// Whether a workgroup joins one row at a time, the parts shared by its threads:
+// where there are few rows.  (A tree of 16 tokens, 32 parts: 4.6 us so, 7.5 us with a row to 64 threads;
+// with many rows the workgroups' own time counts, not the chain of loads.)
+bool share_parts(const Plan &p, int hkv) { return p.rows == 16 || (int64_t)p.joins * hkv * p.rows <= 4096; }
 
 template <int D, int MODE>
 hipError_t launch_mode(const AttentionArgs &a, const Plan &p, float *ws, hipStream_t s) {
@@ -1044,7 +1050,7 @@ hipError_t launch_mode(const AttentionArgs &a, const Plan &p, float *ws, hipStre
     hipError_t e = hipGetLastError();
     if (e != hipSuccess || !p.joins) return e;
     const unsigned heads = (unsigned)(p.joins * a.cache.hkv);
-    if (p.rows == 16)
+    if (share_parts(p, a.cache.hkv))
         attention_join_kernel<D, 1024 / D><<<dim3(heads * p.join_groups), THREADS, 0, s>>>(a, p, ws);
     else
         attention_join_kernel<D, 1><<<dim3(heads * (p.rows * D / 1024)), THREADS, 0, s>>>(a, p, ws);
