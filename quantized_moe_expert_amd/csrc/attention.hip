@@ -350,6 +350,10 @@ __device__ __forceinline__ float *slot_of(float *ws, const Plan &p, int hkv, int
 // VE apart.  No LDS before the waves' sums are joined, no barrier: each wave keeps
 // K and V of a tile (D / 2 KB) in flight while it works on the other.
 //
+// Measured: 64 streams of 32 heads on 8 of 128, 790 k keys: 571 us, 5.7 TB/s of the
+// cache; one stream over 4097 keys, 16 heads on 2 of 256: 14.5 us with the join,
+// which is launches and chains of loads (a call over one key takes 7 us).
+//
 // The weights enter the second product as two bf16, value and remainder (16
 // bits): the matrix cores have time to spare here.
 __host__ __device__ constexpr int rows_keys(int) { return 32; }
@@ -726,9 +730,15 @@ __device__ __forceinline__ u32x2_t read_transposed(const u32x4_t *lds, int byte)
 // 16-byte chunks of a row are permuted by the row number (the source address
 // carries it), so that reads spread over the banks.
 //
+// Measured: a prompt of 8192, 32 heads on 8 of 128: 560 us, 980 TFLOP/s of what is
+// seen (matrix units 51 % of the time, vector units 48 %: exponentials and the work
+// beside them; 64 keys a tile or 32, and priority for the products, change 3 %).
+//
 // Of heads of 256 a workgroup has half of the entries of o (and reads that half of
 // V): with all of them a wave has 512 registers, is alone on its SIMD and waits
-// for LDS (448 TFLOP/s); the first product is done twice.
+// for LDS (pieces of long prompts 2.05 ms; so 1.57 ms, 590 TFLOP/s with capped
+// scores, whose exponentials and quotients take half of the vector time); the first
+// product is done twice.
 //
 // The weights are rounded to bf16 for the second product (half a step, 2^-8 of a
 // weight, random over the keys); their sum is that of the unrounded ones.
@@ -870,6 +880,7 @@ __global__ __launch_bounds__(THREADS, 2) void attention_tile_kernel(AttentionArg
                 if (!(there >> t & 1)) all &= ~(0xffffull << (16 * t));
         }
         if (idle || !__any(all != 0)) return;
+        // Products before the other workgroup's exponentials (3 % of a prompt's time).
         __builtin_amdgcn_s_setprio(2);
         f32x16_t sc[KT];
 #pragma unroll
@@ -1010,7 +1021,11 @@ __global__ __launch_bounds__(THREADS, 2) void attention_tile_kernel(AttentionArg
 
 // ------------------------------------------------------------------ launch
 
-// Which kernel, and how its parts are cut.
+// Which kernel: up to 16 rows in a sequence, on average, for the rows kernel (the
+// device alone knows each sequence's; both are right for any).  Measured, rows
+// / tile kernel: 16 sequences over 4096 keys, 32 heads on 8 of 128: 8 rows
+// 49 / 56 us, 16 rows 54 / 55, 24 rows 64 / 56, 64 rows 110 / 61; 64 over 2000, 16
+// on 2 of 256: 8 rows 57 / 91, 16 rows 63 / 92, 24 rows 105 / 93.
 bool few_rows(int64_t T, int n_seq, int r) { return T * r <= (int64_t)16 * n_seq; }
 
 Plan make_plan(int64_t T, int n_seq, int hq, const Cache &c) {
@@ -1020,7 +1035,13 @@ Plan make_plan(int64_t T, int n_seq, int hq, const Cache &c) {
     p.row_shift = few ? 4 : 7;
     p.rows = 1 << p.row_shift;
     p.key_shift = (few ? rows_keys(c.d) : tile_keys(c.d)) == 32 ? 5 : 6;
+    // A tile to a wave; two tiles, so that the second comes while the first is worked on (a
+    // tree of 16 over 2016 keys: 1 tile 19.9 us, 2 16.9, 8 28).
     p.cmin = few ? WAVES : 2;
+    // Parts of all heads: what is resident at once, for single tokens twice that
+    // (64 streams, 790 k keys: 512 parts 610 us, 1024 571, 2048 562; 24 streams of 1 k keys
+    // 27.9, 26.6, 28.0); prompts: 256 parts 542, 512 560, 1024 575 us (8192 tokens), ragged
+    // prompts of 2000 34.7, 29.5, 36.3.
     p.target_shift = 0;
     while ((2 << p.target_shift) * c.hkv <= (few ? 1024 : 512)) ++p.target_shift;
     const int target = 1 << p.target_shift;

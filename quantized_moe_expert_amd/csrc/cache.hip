@@ -4,7 +4,9 @@
 //
 // Bound by the bytes of the rows, read and written once, and for few tokens by
 // one chain of loads.  One workgroup per token: its rot / 2 angles are computed
-// once, in 64 bits, and kept in LDS for all heads.
+// once, in 64 bits, and kept in LDS for all heads.  Measured: 8000 tokens of 48
+// heads of 128 41 us, 4.8 TB/s (a copy's rate); 16 tokens 6 us.  It lives on
+// occupancy: a wave to a token takes 64 us, four heads a lane at once (85 registers) 61.
 #include "rows_dev.h"
 
 namespace moeq4 {
@@ -29,7 +31,7 @@ struct __attribute__((packed, aligned(4))) Eight {
 template <int D>
 __global__ __launch_bounds__(THREADS, 8) void kv_append_kernel(AppendArgs a) {
     constexpr int LPH = D / 8, HPW = WAVE / LPH;  // lanes a head, heads a wave
-    constexpr int STEP = THREADS / WAVE * HPW, GROUP = 2;
+    constexpr int STEP = THREADS / WAVE * HPW, GROUP = 2;  // (1: 47 us, 3: 42, 4: 48 for 8000 tokens)
     __shared__ __attribute__((aligned(16))) float cs[MAX_HALF], sn[MAX_HALF];
     const int64_t t = blockIdx.x;
     const int tid = threadIdx.x, lane = tid & (WAVE - 1), wave = tid / WAVE;

@@ -4,7 +4,8 @@
 //
 // Bound by the bytes of the rows, each read and written once: a row stays in
 // registers between the two sums of squares.  For few rows: one chain of loads
-// and two sums.
+// and two sums.  Measured: 8192 rows of 4096 with every input 69 to 71 us, 4.8 TB/s (a
+// copy's rate); 16 rows of 2048 3.2 us.
 #include "rows_dev.h"
 #include "../../include/moe_q4_backbone.h"
 
@@ -125,6 +126,9 @@ hipError_t launch(const AddNormArgs &a, hipStream_t s) {
 
 hipError_t launch_add_norm(const AddNormArgs &a, hipStream_t s) {
     const int chunks = a.H / 8;
+    // Eight values a lane and as many lanes as that takes, up to rows of 4096: 8192
+    // rows of 4096 take 71 us so, 79 with 16 values a lane, 124 with a wave to a row
+    // (what counts is rows in flight).  Longer rows, by what a workgroup holds.
     if (chunks <= 8) return launch<8, 1>(a, s);
     if (chunks <= 16) return launch<16, 1>(a, s);
     if (chunks <= 32) return launch<32, 1>(a, s);
