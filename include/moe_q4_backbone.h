@@ -196,7 +196,7 @@ typedef struct moe_q4_kv_cache {
  *                ldq, ldk, ldv (16-byte aligned, distances % 8 == 0).  q may be
  *                NULL: keys and values alone.
  *   seq_start    int32 [n_seq + 1] as of moe_q4_delta_decode.  Rows behind the
- *                last sequence are neither read nor written.
+ *                last sequence are not written, whatever they hold.
  *   positions    int32 [T] or NULL: a token's position is its cache index
  *   inv_freq     float [rot_dim / 2]; NULL with rot_dim = 0: no rotation.
  *                rot_dim % 16 == 0, at most head_dim.

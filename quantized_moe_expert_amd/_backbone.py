@@ -129,7 +129,8 @@ def _flat(t, what, dev, shape, dtype):
         return None
     if t.dtype != dtype or t.shape != shape or not t.is_contiguous():
         raise ValueError(f"{what}: expected contiguous {tuple(shape)} of {dtype}, got {tuple(t.shape)} of {t.dtype}")
-    _here(t, dev)
+    if t.get_device() != dev:
+        raise ValueError("moe_q4 takes device tensors of the current device")
     return t.data_ptr()
 
 

@@ -149,7 +149,7 @@ __device__ __forceinline__ Query load_query(const AttentionArgs &a, const Seq &s
     q.lo = a.window ? (int)max((int64_t)0, (int64_t)q.pos - a.window + 1) : 0;
     if (a.tree && a.window)
         for (int c = 0; c < WAVE; ++c)
-            if (s.before + depth[c] < q.lo) q.mask &= ~(1ull << c);
+            if (q.pos - (s.before + depth[c]) >= a.window) q.mask &= ~(1ull << c);
     return q;
 }
 // Bits 0 to n - 1 of 64.

@@ -195,6 +195,7 @@ int moe_q4_attention(const void *q, int64_t ldq, int32_t q_heads, int64_t T, con
     if ((st = check_cache_pointers(cache))) return st;
     const int64_t width = (int64_t)q_heads * cache->head_dim;
     if ((st = check_rows(q, ldq, width, 16, true)) || (st = check_rows(o, ldo, width, 16, true))) return st;
+    if (q == o) return MOE_Q4_ERR_INVALID_ARG;
     const size_t need = moe_q4_attention_workspace_size(T, n_seq, q_heads, cache);
     if (need && (!ws || ws_bytes < need)) return MOE_Q4_ERR_WORKSPACE;
     if (need && !aligned(ws, 256)) return MOE_Q4_ERR_INVALID_ARG;

@@ -138,6 +138,13 @@ def test_rows_before_the_first_token():
         assert (o[:n - kv] == 0).all()
 
 
+@pytest.mark.parametrize("n,kv", [(20, 7), (64, 40), (3, 1)])
+def test_drafts_before_the_first_token(n, kv):
+    c = Case([n], [kv - n], 4, 2, 64, 16, seed=n)
+    for kw in ({}, {"window": 4}, {"slopes": torch.tensor([0.1, 0.0, 0.3, 1.0], device="cuda")}):
+        both(c, f"{n} drafted of {kv} tokens {kw}", tree=random_tree([n], 3), **kw)
+
+
 def test_table_that_is_too_short():
     """Keys behind the table are seen by nobody."""
     for n in (1, 30, 140):

@@ -41,7 +41,7 @@ def cache(hkv=2, d=128, page=16, cols=8, pages=20, k=FAKE, v=FAKE, table=FAKE, k
 CACHES = [
     (INVALID, dict(hkv=0)), (INVALID, dict(hkv=3)), (INVALID, dict(d=0)), (INVALID, dict(page=0)), (INVALID, dict(cols=0)),
     (INVALID, dict(pages=0)), (UNSUPPORTED, dict(d=96)), (UNSUPPORTED, dict(d=512)), (UNSUPPORTED, dict(page=24)),
-    (UNSUPPORTED, dict(page=8)), (UNSUPPORTED, dict(pages=1 << 31)), (UNSUPPORTED, dict(cols=1 << 27)),
+    (UNSUPPORTED, dict(page=8)), (UNSUPPORTED, dict(pages=1 << 31)), (UNSUPPORTED, dict(cols=(1 << 26) + 1)),
     (INVALID, dict(k=None)), (INVALID, dict(v=None)), (INVALID, dict(table=None)), (INVALID, dict(kv_len=None)),
     (INVALID, dict(k=FAKE + 8)), (INVALID, dict(v=FAKE + 8)), (INVALID, dict(table=FAKE + 2)), (INVALID, dict(kv_len=FAKE + 1)),
 ]
@@ -106,11 +106,18 @@ def test_attention_cache(status, kw):
     (INVALID, dict(slopes=FAKE + 2)), (INVALID, dict(prefix=FAKE + 2)), (INVALID, dict(tree=FAKE + 4)),
     (INVALID, dict(start=None)), (INVALID, dict(start=FAKE + 2)), (INVALID, dict(q=None)), (INVALID, dict(o=None)),
     (INVALID, dict(q=FAKE + 8)), (INVALID, dict(o=FAKE + 8)), (INVALID, dict(ldq=504)), (INVALID, dict(ldo=516)),
-    (UNSUPPORTED, dict(ldq=(1 << 22) + 8)),
+    (UNSUPPORTED, dict(ldq=(1 << 22) + 8)), (INVALID, dict(o=FAKE)),  # q itself
     (OK, dict(T=0)), (OK, dict(n_seq=0)), (OK, dict(T=0, q=None, o=None, start=None)),
 ])
 def test_attention_validation(status, kw):
     assert _attention(**kw) == status
+
+
+def test_limits_on_sequences_and_heads():
+    """Launches of 2^32 threads: sequences times heads of the cache."""
+    assert _attention(c=cache(hkv=16), hq=16, n_seq=1 << 18, T=1 << 18) == UNSUPPORTED
+    assert _attention(c=cache(hkv=16, cols=4096), hq=16, n_seq=(1 << 18) - 1, T=1 << 18, ws=None) == WORKSPACE
+    assert m.attention_workspace_size(1 << 18, 1 << 18, 16, cache(hkv=16)) == 0
 
 
 def test_attention_workspace():
@@ -118,10 +125,10 @@ def test_attention_workspace():
     big = cache(cols=4096)
     assert size(0, 2, 4, big) == 0 and size(4, 0, 4, big) == 0 and size(4, 2, 3, big) == 0 and size(4, 2, 4, cache(d=96)) == 0
     need = size(4, 2, 4, big)
-    if need:
-        assert _attention(c=big, ws=None) == WORKSPACE
-        assert _attention(c=big, nb=need - 1) == WORKSPACE
-        assert _attention(c=big, ws=FAKE + 16, nb=need) == INVALID
+    assert need > 0  # else the calls below would be launched
+    assert _attention(c=big, ws=None) == WORKSPACE
+    assert _attention(c=big, nb=need - 1) == WORKSPACE
+    assert _attention(c=big, ws=FAKE + 16, nb=need) == INVALID
 
 
 def _norm(x=FAKE, ldx=None, u=FAKE + 256, ldu=None, udt=0, T=4, H=128, post=None, gate=None, ldg=None, act=0, scale=1.0,
