@@ -343,6 +343,8 @@ __device__ __forceinline__ float *slot_of(float *ws, const Plan &p, int hkv, int
 
 // --------------------------------------------------------------- few rows
 
+constexpr int ROWS_KEYS = 32;  // of a tile
+
 // K: A operand, row l % 16 a token, 8 entries from 8 (l / 16) on: 16 bytes from
 // memory.  Scores: lane l has query l % 16 and tokens 4 (l / 16) + 0..3 of each
 // 16.  V: the same four tokens, VE entries each; four byte permutes turn two
@@ -356,11 +358,9 @@ __device__ __forceinline__ float *slot_of(float *ws, const Plan &p, int hkv, int
 //
 // The weights enter the second product as two bf16, value and remainder (16
 // bits): the matrix cores have time to spare here.
-__host__ __device__ constexpr int rows_keys(int) { return 32; }
-
 template <int D, int MODE>
 __global__ __launch_bounds__(THREADS, 2) void attention_rows_kernel(AttentionArgs a, Plan p, float *ws) {
-    constexpr int N = rows_keys(D), NB = N / 16, ROWS = 16;
+    constexpr int N = ROWS_KEYS, NB = N / 16, ROWS = 16;
     constexpr int KS = D / 32;                       // steps of the first product
     constexpr int VE = D >= 128 ? 8 : 4, VU = D / (16 * VE);
     constexpr int PITCH = D + 4;
@@ -1034,7 +1034,7 @@ Plan make_plan(int64_t T, int n_seq, int hq, const Cache &c) {
     const bool few = few_rows(T, n_seq, r);
     p.row_shift = few ? 4 : 7;
     p.rows = 1 << p.row_shift;
-    p.key_shift = (few ? rows_keys(c.d) : tile_keys(c.d)) == 32 ? 5 : 6;
+    p.key_shift = (few ? ROWS_KEYS : tile_keys(c.d)) == 32 ? 5 : 6;
     // A tile to a wave; two tiles, so that the second comes while the first is worked on (a
     // tree of 16 over 2016 keys: 1 tile 19.9 us, 2 16.9, 8 28).
     p.cmin = few ? WAVES : 2;
