@@ -872,9 +872,9 @@ __global__ __launch_bounds__(THREADS, 2) void attention_tile_kernel(AttentionArg
             wait_lds();
             lds_barrier();
         }
-        uint64_t all = ~0ull;  // keys that the lane's query sees
+        uint64_t all = ~0ull;  // keys of the tile that the lane's query sees
         if (!whole) {
-            all = seen(a, s, query, k0);
+            all = seen(a, s, query, k0) & below(N);
 #pragma unroll
             for (int t = 0; t < NB; ++t)
                 if (!(there >> t & 1)) all &= ~(0xffffull << (16 * t));
@@ -925,7 +925,8 @@ __global__ __launch_bounds__(THREADS, 2) void attention_tile_kernel(AttentionArg
             for (int x = 0; x < 16; ++x) top = fmaxf(top, sc[t][x]);
         top = query_max<false>(top);
         if (MODE == PLAIN) top *= scale2;
-        if (MODE == CAPPED && top != -INFINITY) top = capped(top * scale2, cap2);
+        // (A product of -inf that is seen is a score of -cap.)
+        if (MODE == CAPPED && all != 0) top = capped(top * scale2, cap2);
         const bool rise = top > m_ref + RISE;
         if (__any(rise)) {
             // (Each row by its own scores: its bits do not depend on the rows beside it.)
