@@ -247,9 +247,12 @@ MOE_Q4_API int moe_q4_kv_append(const void *q, int64_t ldq, int32_t q_heads, con
  * scale, cap and the slopes must be finite, cap and window at least 0; q_heads a
  * multiple of kv_heads, at most 1024; T * q_heads < 2^26, n_seq < 2^20, n_seq * kv_heads < 2^22.
  * Rows behind the last sequence are neither read nor written.  Parts of a row's
- * keys are joined in a fixed order: the same input gives the same bits.  A NaN or
- * an infinity in a key or value reaches the queries that see it (some of their
- * outputs are NaN or infinite) and no others.
+ * keys are joined in a fixed order: the same input gives the same bits.  A NaN in
+ * a query makes its outputs NaN; one in a key or value reaches the queries that see
+ * it (some or all of a head's outputs are NaN) and no others.  Infinities go by the
+ * formula: a score of inf gives NaN; one of -inf has weight 0, and where a query
+ * sees no other the outputs are NaN; a capped score is cap or -cap.  An infinite
+ * value makes outputs of the queries that see it infinite or NaN.
  */
 MOE_Q4_API size_t moe_q4_attention_workspace_size(int64_t T, int32_t n_seq, int32_t q_heads,
                                                   const moe_q4_kv_cache *cache);

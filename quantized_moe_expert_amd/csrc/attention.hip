@@ -36,6 +36,9 @@ constexpr float LOG2E = 1.44269504088896340736f;
 // Rows are scaled to a new maximum when it is more than 2^RISE times the old
 // one: weights stay below 2^RISE, whose sums fp32 holds as well.
 constexpr float RISE = 8.0f;
+// The least maximum of a row that sees a key, whatever its scores: NaN, which a
+// maximum passes over, or -inf.  -inf itself says that a row sees none (and has o = 0).
+constexpr float LEAST = -3.402823466e38f;
 
 __device__ __forceinline__ f32x4_t mfma16(u32x4_t a, u32x4_t b, f32x4_t c) {
     return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16v8_t, a), __builtin_bit_cast(bf16v8_t, b),
@@ -475,18 +478,23 @@ __global__ __launch_bounds__(THREADS, 2) void attention_rows_kernel(AttentionArg
                 if (MODE == BIASED) v -= slope2 * fabsf((float)(query.pos - key_pos(a, s, depth, k0 + 16 * t + 4 * g + x)));
                 sc[4 * t + x] = v;
             }
+        uint32_t all = ~0u;  // keys of the tile that the lane's query sees
         if (!whole) {
-            const uint64_t bits = seen(a, s, query, k0) >> (4 * g);
+            all = (uint32_t)seen(a, s, query, k0);
+#pragma unroll
+            for (int t = 0; t < NB; ++t)
+                if (!(there >> t & 1)) all &= ~(0xffffu << (16 * t));
+            const uint32_t bits = all >> (4 * g);
 #pragma unroll
             for (int t = 0; t < NB; ++t)
 #pragma unroll
-                for (int x = 0; x < 4; ++x)
-                    sc[4 * t + x] = (there >> t & 1) && (bits >> (16 * t + x) & 1) ? sc[4 * t + x] : -INFINITY;
+                for (int x = 0; x < 4; ++x) sc[4 * t + x] = bits >> (16 * t + x) & 1 ? sc[4 * t + x] : -INFINITY;
         }
         float top = sc[0];
 #pragma unroll
         for (int x = 1; x < 4 * NB; ++x) top = fmaxf(top, sc[x]);
         top = query_max<true>(top);
+        top = all != 0 ? fmaxf(top, LEAST) : -INFINITY;
         const bool rise = top > m_ref + RISE;
         if (__any(rise)) {
             // (Each row by its own scores: its bits do not depend on the rows beside it.)
@@ -588,7 +596,7 @@ __global__ __launch_bounds__(THREADS, 2) void attention_rows_kernel(AttentionArg
             v.x = fmaf(k, y.x, v.x), v.y = fmaf(k, y.y, v.y), v.z = fmaf(k, y.z, v.z), v.w = fmaf(k, y.w, v.w);
         }
         if (direct) {
-            const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+            const float inv = top == -INFINITY ? 0.0f : 1.0f / sum;
             const int rw = row0 + rr;
             uint16_t *dst = a.o + (int64_t)(s.start + rw / r) * a.ldo + (int64_t)(hk * r + rw % r) * D + d;
             *reinterpret_cast<uint2 *>(dst) = uint2{pack_bf16x2(v.x * inv, v.y * inv), pack_bf16x2(v.z * inv, v.w * inv)};
@@ -682,7 +690,7 @@ __global__ __launch_bounds__(THREADS) void attention_join_kernel(AttentionArgs a
             }
         }
         if (g > 0 || rr >= live) continue;
-        const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+        const float inv = top == -INFINITY ? 0.0f : 1.0f / sum;
         uint16_t *dst = a.o + (int64_t)(s.start + row / r) * a.ldo + (int64_t)(hk * r + row % r) * D + d;
         *reinterpret_cast<uint2 *>(dst) = uint2{pack_bf16x2(v.x * inv, v.y * inv), pack_bf16x2(v.z * inv, v.w * inv)};
     }
@@ -926,7 +934,8 @@ __global__ __launch_bounds__(THREADS, 2) void attention_tile_kernel(AttentionArg
         top = query_max<false>(top);
         if (MODE == PLAIN) top *= scale2;
         // (A product of -inf that is seen is a score of -cap.)
-        if (MODE == CAPPED && all != 0) top = capped(top * scale2, cap2);
+        if (MODE == CAPPED) top = capped(top * scale2, cap2);
+        top = all != 0 ? fmaxf(top, LEAST) : -INFINITY;
         const bool rise = top > m_ref + RISE;
         if (__any(rise)) {
             // (Each row by its own scores: its bits do not depend on the rows beside it.)
@@ -993,7 +1002,7 @@ __global__ __launch_bounds__(THREADS, 2) void attention_tile_kernel(AttentionArg
     l_sum = query_sum<false>(l_sum);
     if (my_row >= rows) return;
     if (f.parts == 1) {
-        const float inv = l_sum == 0.0f ? 0.0f : 1.0f / l_sum;
+        const float inv = m_ref == -INFINITY ? 0.0f : 1.0f / l_sum;
         uint16_t *dst = a.o + (int64_t)(s.start + i) * a.ldo + (int64_t)head * D + d0 + 4 * hh;
 #pragma unroll
         for (int n = 0; n < DT; ++n)
