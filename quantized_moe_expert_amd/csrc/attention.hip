@@ -530,7 +530,7 @@ __global__ __launch_bounds__(THREADS, 2) void attention_rows_kernel(AttentionArg
                         bad |= b;
                     }
                     // (The lanes with the same four tokens are 16 neighbours.)
-                    if ((__ballot(bad) >> (16 * g) & 0xffffu) && sc[4 * t + x] != -INFINITY) w[4 * t + x] = NAN;
+                    if ((__ballot(bad) >> (16 * g) & 0xffffu) && (all >> (4 * g) >> (16 * t + x) & 1)) w[4 * t + x] = NAN;
                 }
         }
 #pragma unroll

@@ -194,3 +194,22 @@ def test_scores_of_infinity(lens, hist, hq, hkv, d, opt):
     o = c.run(**kw)
     torch.cuda.synchronize()
     check_rows(c, o, sorted({(b, i) for b, n in enumerate(lens) for i in (0, n // 2, n - 1)}), **kw)
+
+
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("lens,hist,hq,hkv", SHAPES)
+def test_nan_value_under_a_score_of_minus_infinity(lens, hist, hq, hkv, d):
+    """A weight of 0 times NaN: the last key's score is -inf, its value NaN."""
+    c = Case(lens, hist, hq, hkv, d, 16, seed=2)
+    c.q[:, :, 2] = c.q[:, :, 2].abs() + 0.5
+    for b, e in enumerate(c.kv):
+        p, at = place(c, b, e - 1)
+        c.k[p, :, at, 2] = -INF
+        c.v[p, :, at, 1] = NAN
+    o = c.run()
+    torch.cuda.synchronize()
+    for b, n in enumerate(lens):
+        last = sum(lens[:b + 1]) - 1
+        assert torch.isnan(o[last]).any(-1).all(), b
+        if n > 1:
+            assert torch.isfinite(o[last - 1]).all(), b
