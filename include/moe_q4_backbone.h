@@ -220,8 +220,9 @@ MOE_Q4_API int moe_q4_kv_append(const void *q, int64_t ldq, int32_t q_heads, con
  *   s = scale q . k,  then s = cap tanh(s / cap)     (cap > 0)
  *                     then s -= slopes[h] * |distance|  (with slopes)
  *   o = sum softmax(s) v
- * with scores, softmax and sums in fp32; the weights may be rounded to bf16 for
- * their products with v.  A query that sees no key gets o = 0.  The distance is
+ * with scores, softmax and sums in fp32 (capping adds at most 2^-20 of the score to
+ * its error, with caps up to 64 at most 2^-20 of the cap); the weights may be
+ * rounded to bf16 for their products with v.  A query that sees no key gets o = 0.  The distance is
  * the query's position less the key's; positions are cache indices.  A query sees
  *   - the keys up to its own index, with window > 0 only those at a distance
  *     below window,

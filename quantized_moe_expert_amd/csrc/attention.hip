@@ -31,7 +31,9 @@ typedef unsigned int u32x2_t __attribute__((ext_vector_type(2)));
 typedef __attribute__((address_space(3))) void lds_void;
 
 constexpr int THREADS = 256, WAVES = THREADS / WAVE;
-enum { PLAIN, CAPPED, BIASED };  // scores as they are; capped; less a bias (and capped, or not)
+// Scores as they are; capped by a quotient (caps up to QUOTIENT_CAP); by more; less a
+// bias (and capped by either, or not).
+enum { PLAIN, QUOTIENT, CAPPED, BIASED };
 constexpr float LOG2E = 1.44269504088896340736f;
 // Rows are scaled to a new maximum when it is more than 2^RISE times the old
 // one: weights stay below 2^RISE, whose sums fp32 holds as well.
@@ -48,15 +50,41 @@ __device__ __forceinline__ f32x16_t mfma32(u32x4_t a, u32x4_t b, f32x16_t c) {
     return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16v8_t, a), __builtin_bit_cast(bf16v8_t, b),
                                                    c, 0, 0, 0);
 }
-// What a product is multiplied by: to a power of two's exponent, or (capped) to v
-// below.  Finite, so that a product of 0 stays one.
-__device__ __forceinline__ float score_scale(const AttentionArgs &a) {
-    const float v = a.cap > 0.0f ? a.scale / a.cap * (2.0f * LOG2E) : a.scale * LOG2E;
-    return fminf(fmaxf(v, -3e38f), 3e38f);
-}
-// cap2 tanh(x), v = 2 log2(e) x: 1 - 2 / (1 + e^2x), off by 2^-22 of cap2.
+// Finite, so that a product of 0 stays one.
+__device__ __forceinline__ float finite(float v) { return fminf(fmaxf(v, -3e38f), 3e38f); }
+
+// A score's cap, cap2 tanh(w / cap2) with all in powers of two (cap2 = cap log2(e)).
+//
+// Up to QUOTIENT_CAP: the quotient rest = 1 / (1 + e^2x), x = w / cap2, of v = 2 x log2(e),
+// and from it cap2 - 2 cap2 rest.  Off by at most 10 half steps of the *cap* (2^-14.7 at 64;
+// a weight has 2^-16 of itself in the rows kernel, 2^-9 in the tile kernel).
+//
+// Beyond: score(), off by at most 12 half steps of the score.  Up to |x| = 1/2 a
+// polynomial, w p(x^2) (coefficients: least largest relative error, 2^-26), then cap2
+// (1 - 2 / (1 + e^2|x|)) with the sign of x.
+//
+// Measured, no cap / quotient / score(): pieces of long prompts, heads of 256, 1.35 / 1.56 /
+// 2.05 ms; prompt of 8192, heads of 128, 553 / 665 / 907 us; 64 streams over 790 k keys
+// 572 us in all three.
+constexpr float QUOTIENT_CAP = 64.0f;
 __device__ __forceinline__ float cap_rest(float v) { return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(v)); }
-__device__ __forceinline__ float capped(float v, float cap2) { return fmaf(-2.0f * cap2, cap_rest(v), cap2); }
+struct Cap {
+    float cap2, inverse;
+    __device__ __forceinline__ explicit Cap(float cap)
+        : cap2(finite(cap * LOG2E)), inverse(finite(1.0f / cap2)) {}
+    // Whether the quotient caps, and what a product is multiplied by: to v then, to w otherwise.
+    static __device__ __forceinline__ bool quotient(const AttentionArgs &a) { return a.cap > 0.0f && a.cap <= QUOTIENT_CAP; }
+    static __device__ __forceinline__ float scale(const AttentionArgs &a) {
+        return finite(quotient(a) ? a.scale / a.cap * (2.0f * LOG2E) : a.scale * LOG2E);
+    }
+    __device__ __forceinline__ float of_rest(float rest) const { return fmaf(-2.0f * cap2, rest, cap2); }
+    __device__ __forceinline__ float score(float w) const {
+        const float x = w * inverse, y = x * x;
+        const float p = fmaf(y, fmaf(y, fmaf(y, fmaf(y, 0.01724149f, -0.05304549f), 0.13325879f), -0.33333144f), 1.0f);
+        const float far = cap2 * fmaf(-2.0f, cap_rest(fabsf(x) * (2.0f * LOG2E)), 1.0f);
+        return fabsf(x) < 0.5f ? w * p : copysignf(far, x);
+    }
+};
 // Largest value and sum over the lanes that hold one query: l, l ^ 32 and, of
 // 16 queries, l ^ 16 and l ^ 48.
 template <bool OF16>
@@ -386,8 +414,8 @@ __global__ __launch_bounds__(THREADS, 2) void attention_rows_kernel(AttentionArg
     const int per = uniform((range.count + f.parts - 1) / f.parts);
     const int j_end = min(range.count, (f.part + 1) * per);
     const Query query = load_query(a, s, depth, i);
-    const float scale2 = score_scale(a);
-    const float cap2 = a.cap * LOG2E;
+    const Cap cap(a.cap);
+    const float scale2 = Cap::scale(a);
     const float slope2 = MODE == BIASED ? a.slopes[head] * LOG2E : 0.0f;
 
     u32x4_t q[KS];
@@ -469,15 +497,21 @@ __global__ __launch_bounds__(THREADS, 2) void attention_rows_kernel(AttentionArg
 
         const bool whole = there == (1u << NB) - 1 && sees_all<N>(a, s, i0, i1, k0);
         float sc[4 * NB];
+        auto scores = [&](auto score) {
 #pragma unroll
-        for (int t = 0; t < NB; ++t)
+            for (int x = 0; x < 4 * NB; ++x) sc[x] = score(acc[x / 4][x % 4] * scale2);
+        };
+        // (Loops of their own: in one, all three ways are computed.)
+        if (MODE == QUOTIENT || (MODE == BIASED && Cap::quotient(a)))
+            scores([&](float v) { return cap.of_rest(cap_rest(v)); });
+        else if (MODE == CAPPED || (MODE == BIASED && a.cap > 0.0f))
+            scores([&](float w) { return cap.score(w); });
+        else
+            scores([&](float w) { return w; });
+        if (MODE == BIASED)
 #pragma unroll
-            for (int x = 0; x < 4; ++x) {
-                float v = acc[t][x] * scale2;
-                if (MODE == CAPPED || (MODE == BIASED && a.cap > 0.0f)) v = capped(v, cap2);
-                if (MODE == BIASED) v -= slope2 * fabsf((float)(query.pos - key_pos(a, s, depth, k0 + 16 * t + 4 * g + x)));
-                sc[4 * t + x] = v;
-            }
+            for (int x = 0; x < 4 * NB; ++x)
+                sc[x] -= slope2 * fabsf((float)(query.pos - key_pos(a, s, depth, k0 + 16 * (x / 4) + 4 * g + x % 4)));
         uint32_t all = ~0u;  // keys of the tile that the lane's query sees
         if (!whole) {
             all = (uint32_t)seen(a, s, query, k0);
@@ -776,10 +810,10 @@ __global__ __launch_bounds__(THREADS, 2) void attention_tile_kernel(AttentionArg
     const int j0 = f.part * per, j_end = min(range.count, j0 + per);
     const Query query = load_query(a, s, depth, i);
     const bool idle = row0 + wave * 32 >= rows;  // a wave without rows brings keys for the others
+    const Cap cap(a.cap);
     // (A negative scale goes to the queries' signs, so that the largest product has the largest
     // score; above 0, so that -inf stays.)
-    const float scale2 = fmaxf(fabsf(score_scale(a)), 1e-37f);
-    const float cap2 = a.cap * LOG2E;
+    const float scale2 = fmaxf(fabsf(Cap::scale(a)), 1e-37f);
     const float slope2 = MODE == BIASED ? a.slopes[head] * LOG2E : 0.0f;
 
     u32x4_t q[DS];
@@ -902,17 +936,27 @@ __global__ __launch_bounds__(THREADS, 2) void attention_tile_kernel(AttentionArg
         }
         __builtin_amdgcn_s_setprio(1);
         if (MODE == BIASED) {
+            auto scores = [&](auto score) {
+#pragma unroll
+                for (int t = 0; t < KT; ++t)
+#pragma unroll
+                    for (int x = 0; x < 16; ++x) sc[t][x] = score(sc[t][x] * scale2);
+            };
+            if (Cap::quotient(a))  // (as in attention_rows_kernel)
+                scores([&](float v) { return cap.of_rest(cap_rest(v)); });
+            else if (a.cap > 0.0f)
+                scores([&](float w) { return cap.score(w); });
+            else
+                scores([&](float w) { return w; });
             const bool drafted = a.tree && k0 + N > s.before;
             const float gap0 = (float)(query.pos - k0 - 4 * hh);
 #pragma unroll
             for (int t = 0; t < KT; ++t)
 #pragma unroll
                 for (int x = 0; x < 16; ++x) {
-                    float v = sc[t][x] * scale2;
-                    if (a.cap > 0.0f) v = capped(v, cap2);
                     const int key = 32 * t + 8 * (x / 4) + x % 4;
                     const float gap = drafted ? (float)(query.pos - key_pos(a, s, depth, k0 + 4 * hh + key)) : gap0 - (float)key;
-                    sc[t][x] = v - slope2 * fabsf(gap);
+                    sc[t][x] -= slope2 * fabsf(gap);
                 }
         }
         if (!whole) {
@@ -934,7 +978,8 @@ __global__ __launch_bounds__(THREADS, 2) void attention_tile_kernel(AttentionArg
         top = query_max<false>(top);
         if (MODE == PLAIN) top *= scale2;
         // (A product of -inf that is seen is a score of -cap.)
-        if (MODE == CAPPED) top = capped(top * scale2, cap2);
+        if (MODE == CAPPED) top = cap.score(top * scale2);
+        if (MODE == QUOTIENT) top = cap.of_rest(cap_rest(top * scale2));
         top = all != 0 ? fmaxf(top, LEAST) : -INFINITY;
         const bool rise = top > m_ref + RISE;
         if (__any(rise)) {
@@ -949,17 +994,21 @@ __global__ __launch_bounds__(THREADS, 2) void attention_tile_kernel(AttentionArg
             m_ref = m_new;
         }
         const float m_use = m_ref == -INFINITY ? 0.0f : m_ref;
-        if (MODE == CAPPED) {
+        if (MODE == CAPPED || MODE == QUOTIENT) {
 #pragma unroll
             for (int t = 0; t < KT; ++t)
 #pragma unroll
-                for (int x = 0; x < 16; ++x) sc[t][x] = cap_rest(sc[t][x] * scale2);
+                for (int x = 0; x < 16; ++x) {
+                    const float v = sc[t][x] * scale2;
+                    sc[t][x] = MODE == CAPPED ? cap.score(v) : cap_rest(v);
+                }
             if (!whole) {
+                const float none = MODE == CAPPED ? -INFINITY : INFINITY;  // whose weight is 0
 #pragma unroll
                 for (int t = 0; t < KT; ++t) {
                     const uint32_t bits = (uint32_t)(all >> (32 * t)) >> (4 * hh);
 #pragma unroll
-                    for (int x = 0; x < 16; ++x) sc[t][x] = bits >> (8 * (x / 4) + x % 4) & 1 ? sc[t][x] : INFINITY;
+                    for (int x = 0; x < 16; ++x) sc[t][x] = bits >> (8 * (x / 4) + x % 4) & 1 ? sc[t][x] : none;
                 }
             }
         }
@@ -972,9 +1021,9 @@ __global__ __launch_bounds__(THREADS, 2) void attention_tile_kernel(AttentionArg
 #pragma unroll
                 for (int x = 0; x < 8; ++x) {
                     const float v = sc[t][8 * u + x];
-                    e[x] = __builtin_amdgcn_exp2f(MODE == PLAIN    ? fmaf(v, scale2, -m_use)
-                                                  : MODE == CAPPED ? fmaf(v, -2.0f * cap2, cap2 - m_use)
-                                                                   : v - m_use);
+                    e[x] = __builtin_amdgcn_exp2f(MODE == PLAIN      ? fmaf(v, scale2, -m_use)
+                                                  : MODE == QUOTIENT ? fmaf(v, -2.0f * cap.cap2, cap.cap2 - m_use)
+                                                                     : v - m_use);
                     l_sum += e[x];
                 }
                 const u32x4_t w = {pack_bf16x2(e[0], e[1]), pack_bf16x2(e[2], e[3]), pack_bf16x2(e[4], e[5]),
@@ -1091,7 +1140,8 @@ hipError_t launch_mode(const AttentionArgs &a, const Plan &p, float *ws, hipStre
 template <int D>
 hipError_t launch(const AttentionArgs &a, const Plan &p, float *ws, hipStream_t s) {
     if (a.slopes) return launch_mode<D, BIASED>(a, p, ws, s);
-    return a.cap > 0.0f ? launch_mode<D, CAPPED>(a, p, ws, s) : launch_mode<D, PLAIN>(a, p, ws, s);
+    if (a.cap > QUOTIENT_CAP) return launch_mode<D, CAPPED>(a, p, ws, s);
+    return a.cap > 0.0f ? launch_mode<D, QUOTIENT>(a, p, ws, s) : launch_mode<D, PLAIN>(a, p, ws, s);
 }
 
 }  // namespace
