@@ -50,7 +50,7 @@ __device__ __forceinline__ f32x16_t mfma32(u32x4_t a, u32x4_t b, f32x16_t c) {
     return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16v8_t, a), __builtin_bit_cast(bf16v8_t, b),
                                                    c, 0, 0, 0);
 }
-// Finite, so that a product of 0 stays one.
+// Finite, so that a product or a distance of 0 stays one.
 __device__ __forceinline__ float finite(float v) { return fminf(fmaxf(v, -3e38f), 3e38f); }
 
 // A score's cap, cap2 tanh(w / cap2) with all in powers of two (cap2 = cap log2(e)).
@@ -416,7 +416,7 @@ __global__ __launch_bounds__(THREADS, 2) void attention_rows_kernel(AttentionArg
     const Query query = load_query(a, s, depth, i);
     const Cap cap(a.cap);
     const float scale2 = Cap::scale(a);
-    const float slope2 = MODE == BIASED ? a.slopes[head] * LOG2E : 0.0f;
+    const float slope2 = MODE == BIASED ? finite(a.slopes[head] * LOG2E) : 0.0f;
 
     u32x4_t q[KS];
     {
@@ -814,7 +814,7 @@ __global__ __launch_bounds__(THREADS, 2) void attention_tile_kernel(AttentionArg
     // (A negative scale goes to the queries' signs, so that the largest product has the largest
     // score; above 0, so that -inf stays.)
     const float scale2 = fmaxf(fabsf(Cap::scale(a)), 1e-37f);
-    const float slope2 = MODE == BIASED ? a.slopes[head] * LOG2E : 0.0f;
+    const float slope2 = MODE == BIASED ? finite(a.slopes[head] * LOG2E) : 0.0f;
 
     u32x4_t q[DS];
     {
