@@ -237,8 +237,9 @@ def moe_q4_delta_prefill(q, k, v, g, beta, seq_start, state_idx, state_in, state
 def kv_cache_struct(k, v, page_table, kv_len) -> KVCache:
     """struct moe_q4_kv_cache from the pool's pages k, v bf16 [n_pages,
     kv_heads, page_size, head_dim], page_table int32 [n_seq, max_pages] and
-    kv_len int32 [n_seq].  The caller keeps the tensors alive; their contents
-    are read when a call runs."""
+    kv_len int32 [n_seq].  A call may have the first of these sequences alone:
+    the length of its seq_start says how many.  The caller keeps the tensors
+    alive; their contents are read when a call runs."""
     dev = k.get_device()
     if dev < 0:
         raise ValueError("moe_q4 takes device tensors")
@@ -256,10 +257,14 @@ def kv_cache_struct(k, v, page_table, kv_len) -> KVCache:
 
 
 def _cached(cache, seq_start, dev):
-    """(pointer, n_seq) of the starts of the cache's sequences."""
+    """(pointer, n_seq) of the starts of the cache's sequences, or of the first
+    of them."""
     if cache.device != dev:
         raise ValueError("moe_q4 takes device tensors of the current device")
-    return _flat(seq_start, "seq_start", dev, (cache.n_seq + 1,), torch.int32), cache.n_seq
+    n_seq = cache.n_seq if seq_start is None else seq_start.numel() - 1
+    if n_seq != cache.n_seq and not 1 <= n_seq < cache.n_seq:
+        raise ValueError(f"seq_start: expected the starts of up to {cache.n_seq} sequences and an end, got {n_seq + 1}")
+    return _flat(seq_start, "seq_start", dev, (n_seq + 1,), torch.int32), n_seq
 
 
 def moe_q4_kv_append(q, k, v, seq_start, cache, q_out, inv_freq=None, positions=None, q_norm=None, k_norm=None,

@@ -116,8 +116,9 @@ class AttentionMixer:
 
     def forward(self, x, seq_start, y, positions=None, prefix=None, tree=None, residual=None):
         """y (bf16 [T, hidden], may be x or residual) = residual + mixer(x); None:
-        x itself.  The cache's kv_len counts the T rows already; their keys and
-        values are stored by the call.  ``positions`` are the rotation's (drafted
+        x itself.  The batch's sequences are the cache's first seq_start.numel()
+        - 1.  Its kv_len counts the T rows already; their keys and values are stored by
+        the call.  ``positions`` are the rotation's (drafted
         tokens: their depth, not their place in the cache).  A row that only fills
         up the batch is a sequence of its own whose kv_len is 0."""
         T = x.shape[0]
