@@ -39,7 +39,8 @@ class DeltaShape(ctypes.Structure):
 
 
 class KVCache(ctypes.Structure):
-    """struct moe_q4_kv_cache"""
+    """struct moe_q4_kv_cache; kv_cache_struct makes those that calls take"""
+    device, n_seq = None, 0
     _fields_ = [("kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32), ("page_size", ctypes.c_int32),
                 ("max_pages", ctypes.c_int32), ("n_pages", ctypes.c_int64), ("k", ctypes.c_void_p),
                 ("v", ctypes.c_void_p), ("page_table", ctypes.c_void_p), ("kv_len", ctypes.c_void_p)]
@@ -259,6 +260,8 @@ def kv_cache_struct(k, v, page_table, kv_len) -> KVCache:
 def _cached(cache, seq_start, dev):
     """(pointer, n_seq) of the starts of the cache's sequences, or of the first
     of them."""
+    if cache.device is None:
+        raise ValueError("cache: expected one of kv_cache_struct")
     if cache.device != dev:
         raise ValueError("moe_q4 takes device tensors of the current device")
     n_seq = cache.n_seq if seq_start is None else seq_start.numel() - 1

@@ -24,3 +24,11 @@ def test_workspace_fits_every_batch(hq, hkv, max_tokens, max_seqs):
     for n in range(1, max_seqs + 1):
         for t in range(1, max_tokens + 1):
             assert m.attention_workspace_size(t, n, hq, cache) <= lay.ws.numel(), (t, n)
+
+
+def test_a_cache_needs_kv_cache_struct():
+    """A KVCache of the caller's own has no number of sequences and no device."""
+    from quantized_moe_expert_amd import _backbone
+    cache = m.KVCache(2, 64, 16, 4, 8, FAKE, FAKE, FAKE, FAKE)
+    with pytest.raises(ValueError, match="kv_cache_struct"):
+        _backbone._cached(cache, None, 0)
