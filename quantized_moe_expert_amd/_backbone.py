@@ -317,6 +317,8 @@ def moe_q4_attention(q, seq_start, cache, o, scale, ws=None, cap=0.0, window=0, 
     T, hq, d = q.shape
     if d != cache.head_dim:
         raise ValueError(f"q: expected heads of {cache.head_dim}, got {d}")
+    if not 0 <= window < 1 << 31:
+        raise ValueError(f"window: expected 0 (none) to 2^31 - 1, got {window}")
     qp, ldq = _rows(q, "q", dev, (T, hq, d))
     op, ldo = _rows(o, "o", dev, (T, hq, d))
     wp, nb = _ws(ws, dev)

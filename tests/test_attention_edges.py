@@ -78,3 +78,11 @@ def test_mixer_with_fewer_sequences(lens):
         got.append(mixer.forward(x, start, torch.empty_like(x)))
         torch.cuda.synchronize()
     assert torch.equal(*got)
+
+
+@pytest.mark.parametrize("window", [-1, 1 << 31, (1 << 32) + 5])
+def test_windows_that_do_not_fit_are_refused(window):
+    """Not cut to 32 bits: 2^32 + 5 would be a window of 5."""
+    c = Case([1], [40], 4, 2, 64, 16)
+    with pytest.raises((ValueError, m.MoeQ4Error)):
+        c.run(window=window)
