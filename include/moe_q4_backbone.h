@@ -231,8 +231,8 @@ MOE_Q4_API int moe_q4_kv_append(const void *q, int64_t ldq, int32_t q_heads, con
  * With a tree the rows of a sequence are drafted tokens, at most 64: bit j of
  * tree[t] says that row t sees row j of its sequence (itself, as a rule, and
  * those that it follows).  Cached tokens before the rows are seen as above; a
- * row's position is the number of those plus the number of other rows that it
- * sees, and distances (window, slopes) go by it.  Rows behind the 64th of a
+ * row's position is the number of those plus the number of other bits of its
+ * mask, and distances (window, slopes) go by it.  Rows behind the 64th of a
  * sequence are seen by nobody.  prefix must be NULL with a tree.
  *   q          bf16 [T] rows of [q_heads][head_dim] at distance ldq (as
  *              moe_q4_kv_append leaves them)

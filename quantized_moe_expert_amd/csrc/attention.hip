@@ -57,7 +57,7 @@ __device__ __forceinline__ float finite(float v) { return fminf(fmaxf(v, -3e38f)
 //
 // Up to QUOTIENT_CAP: the quotient rest = 1 / (1 + e^2x), x = w / cap2, of v = 2 x log2(e),
 // and from it cap2 - 2 cap2 rest.  Off by at most 10 half steps of the *cap* (2^-14.7 at 64;
-// a weight has 2^-16 of itself in the rows kernel, 2^-9 in the tile kernel).
+// a weight is then rounded to 2^-16 of itself in the rows kernel, 2^-8 in the tile kernel).
 //
 // Beyond: score(), off by at most 12 half steps of the score.  Up to |x| = 1/2 a
 // polynomial, w p(x^2) (coefficients: least largest relative error, 2^-26), then cap2
@@ -252,6 +252,11 @@ __device__ __forceinline__ Seq uniform(const Seq &s) {
 
 // Finds the part (JOIN: the split block) with this number; false: there are
 // fewer.  All threads of the workgroup call it.
+//
+// Each workgroup goes over all sequences: up to 64 in a few instructions, more in
+// steps of 256.  Single tokens over 100 keys, 8 heads on 2 of 64: 64 sequences 7.2 us, 65
+// 7.5, 256 9.1, 1024 27.5, 4096 187, 16384 2009: from about a thousand on it is
+// what the call takes, and grows with their square.
 template <bool JOIN>
 __device__ __forceinline__ bool plan_find(const AttentionArgs &a, const Plan &p, int64_t item, Found &f) {
     if (a.n_seq <= WAVE) {
@@ -383,9 +388,10 @@ constexpr int ROWS_KEYS = 32;  // of a tile
 // VE apart.  No LDS before the waves' sums are joined, no barrier: each wave keeps
 // K and V of a tile (D / 2 KB) in flight while it works on the other.
 //
-// Measured: 64 streams of 32 heads on 8 of 128, 790 k keys: 571 us, 5.7 TB/s of the
-// cache; one stream over 4097 keys, 16 heads on 2 of 256: 14.5 us with the join,
-// which is launches and chains of loads (a call over one key takes 7 us).
+// Measured: 64 streams of 32 heads on 8 of 128, 790 k keys: 572 us, 5.7 TB/s of the
+// cache; one stream over 4097 keys, 16 heads on 2 of 256: 14.2 us with the join,
+// which is launches and chains of loads (a call over one key takes 7 us).  Heads of
+// 256 have 256 registers and 44 to 76 bytes of scratch a lane.
 //
 // The weights enter the second product as two bf16, value and remainder (16
 // bits): the matrix cores have time to spare here.
@@ -773,14 +779,14 @@ __device__ __forceinline__ u32x2_t read_transposed(const u32x4_t *lds, int byte)
 // carries it), so that reads spread over the banks.
 //
 // Measured: a prompt of 8192, 32 heads on 8 of 128: 560 us, 980 TFLOP/s of what is
-// seen (matrix units 51 % of the time, vector units 48 %: exponentials and the work
-// beside them; 64 keys a tile or 32, and priority for the products, change 3 %).
+// seen, the matrix units busy 51 % of the time (64 keys a tile or 32, and priority for
+// the products, change 3 %); with a window of 1024 184 us, with slopes 789 us (144
+// bytes of scratch a lane: the three ways to a score have loops of their own).
 //
 // Of heads of 256 a workgroup has half of the entries of o (and reads that half of
 // V): with all of them a wave has 512 registers, is alone on its SIMD and waits
-// for LDS (pieces of long prompts 2.05 ms; so 1.57 ms, 590 TFLOP/s with capped
-// scores, whose exponentials and quotients take half of the vector time); the first
-// product is done twice.
+// for LDS (pieces of long prompts 2.05 ms; so 1.57 ms, 590 TFLOP/s with a cap of 50, and
+// 1.35 ms without one); the first product, cap and exponentials are done twice.
 //
 // The weights are rounded to bf16 for the second product (half a step, 2^-8 of a
 // weight, random over the keys); their sum is that of the unrounded ones.
@@ -1084,7 +1090,9 @@ __global__ __launch_bounds__(THREADS, 2) void attention_tile_kernel(AttentionArg
 // device alone knows each sequence's; both are right for any).  Measured, rows
 // / tile kernel: 16 sequences over 4096 keys, 32 heads on 8 of 128: 8 rows
 // 49 / 56 us, 16 rows 54 / 55, 24 rows 64 / 56, 64 rows 110 / 61; 64 over 2000, 16
-// on 2 of 256: 8 rows 57 / 91, 16 rows 63 / 92, 24 rows 105 / 93.
+// on 2 of 256: 8 rows 57 / 91, 16 rows 63 / 92, 24 rows 105 / 93.  Not the best where one
+// sequence is unlike the others: 999 single tokens and a piece of 3000 in one call take
+// 901 us, apart 402 and 124.
 bool few_rows(int64_t T, int n_seq, int r) { return T * r <= (int64_t)16 * n_seq; }
 
 Plan make_plan(int64_t T, int n_seq, int hq, const Cache &c) {

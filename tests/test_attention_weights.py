@@ -31,8 +31,6 @@ def gpu():
                                               ([1] * 70, [(i * 37) % 400 for i in range(70)], 2, 2), ([40], [900], 4, 2),
                                               ([64, 17], [130, 600], 8, 1), ([300, 5], [0, 500], 2, 1), ([700], [100], 1, 1)])
 def test_every_key_counts_once(lens, hist, hq, hkv, d, opt):
-    if opt == "tree" and max(lens) > 64:
-        pytest.skip("drafts have at most 64 tokens")
     c = Case(lens, hist, hq, hkv, d, 16, seed=3, q_scale=0.0)
     kw = {"plain": {}, "window": {"window": 150},
           "prefix": {"window": 40, "prefix": torch.tensor([(i * 29) % 200 for i in range(len(lens))], dtype=torch.int32, device="cuda")},
