@@ -117,10 +117,11 @@ class AttentionMixer:
     def forward(self, x, seq_start, y, positions=None, prefix=None, tree=None, residual=None):
         """y (bf16 [T, hidden], may be x or residual) = residual + mixer(x); None:
         x itself.  The batch's sequences are the cache's first seq_start.numel()
-        - 1.  Its kv_len counts the T rows already; their keys and values are stored by
-        the call.  ``positions`` are the rotation's (drafted
-        tokens: their depth, not their place in the cache).  A row that only fills
-        up the batch is a sequence of its own whose kv_len is 0."""
+        - 1.  Its kv_len counts the T rows already; their keys and values are stored
+        by the call.  ``positions`` are the rotation's (drafted tokens: their depth,
+        not their place in the cache).  Every one of the T rows must belong to a
+        sequence: one that only fills up the batch is a sequence of its own whose
+        kv_len is 0."""
         T = x.shape[0]
         if T > self.max_tokens or seq_start.numel() - 1 > self.max_seqs:
             raise ValueError(f"{T} tokens of {seq_start.numel() - 1} sequences do not fit in the buffers")
